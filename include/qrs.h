@@ -89,6 +89,10 @@ typedef enum qrs_x_dtype {
 typedef enum qrs_scale_layout {
   QRS_SCALE_F32_GROUP128 = 0,
   QRS_SCALE_E8M0_BLOCK32 = 1,
+  QRS_SCALE_F32_ROW = 2, /* float32 [rows], one scale for each row: the
+                            operands of qrs_matmul_int. Not a mode of the
+                            reduce-scatter: only qrs_add_rms_norm_quantize
+                            takes it. */
   QRS_SCALE_LAYOUT_RANGE_MIN_ = -2147483647 - 1, /* range markers, not layouts */
   QRS_SCALE_LAYOUT_RANGE_MAX_ = 2147483647
 } qrs_scale_layout;
@@ -295,6 +299,133 @@ qrs_status qrs_run_strided(qrs_plan_t plan, const void* const* x_slices, int64_t
  */
 qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scale_layout scale_layout,
                         const void* x_bf16, void* x_codes, void* scales, void* stream);
+
+/*
+ * The layer between two shares. A tensor-parallel layer takes the rows that
+ * one reduce-scatter leaves, adds them to the residual stream, normalizes
+ * them, and multiplies by 8-bit weights until the partial sums of the next
+ * reduce-scatter are there:
+ *
+ *   qrs_add_rms_norm_quantize  residual sum, RMS norm, codes and scales
+ *   qrs_rms_norm_backward      its gradients
+ *   qrs_quantize_rows          codes with one scale for each row
+ *   qrs_matmul_int             8-bit integer product, scales for each token
+ *                              and channel; also two products joined as
+ *                              silu(gate) * up
+ *   qrs_matmul_int_quantize    the same product, written as the codes and
+ *                              scales that qrs_run reads
+ *
+ * Common to all of them: asynchronous on `stream` (a hipStream_t, NULL = the
+ * default stream); kernels only, so they may be captured in a HIP graph;
+ * nothing is allocated (a workspace, where one is needed, is the caller's);
+ * rows are given by row strides in elements, elements within a row adjacent;
+ * any alignment of the element type is accepted, and rows that start on
+ * 16-byte boundaries are read and written 16 bytes at a time. Sizes must be
+ * positive. An output's address span must not overlap an input's or another
+ * output's, except where a call allows a buffer to be updated in place
+ * (then pointer and row stride are the same). Results are deterministic:
+ * every sum has a fixed order. Errors as for qrs_run.
+ */
+
+/*
+ * s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight along each row,
+ * and y as codes and scales.
+ *
+ * s is rounded once to the activations' type and stored in sum_out; y is
+ * computed from the stored s in binary32 and quantized without another
+ * rounding, by qrs_quantize's rules for QRS_SCALE_F32_GROUP128 and
+ * QRS_SCALE_E8M0_BLOCK32. QRS_SCALE_F32_ROW takes the whole row as one group
+ * of the same rule. A group that holds a NaN or an infinity gets a NaN or
+ * infinite scale (E8M0 code 255), so that it stays visible; its codes are
+ * unspecified. Squares are summed in binary32: rows whose sum of squares
+ * overflows it are taken as infinitely large (y = 0).
+ *
+ *   tokens, h     rows of x; h in [1, 65536], a multiple of the layout's
+ *                 group (128 or 32; any for QRS_SCALE_F32_ROW).
+ *   io_dtype      type of x, residual, weight and sum_out.
+ *   x_dtype, scale_layout
+ *                 a mode of qrs_quantize, or any x_dtype with
+ *                 QRS_SCALE_F32_ROW.
+ *   eps           >= 0, finite.
+ *   residual      may be NULL: s = x, and sum_out is not written (it may be
+ *                 NULL).
+ *   weight        [h].
+ *   sum_out       may be x or residual themselves (same pointer and stride).
+ *   codes         uint8; scales contiguous in the layout's shape.
+ */
+qrs_status qrs_add_rms_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype io_dtype, qrs_x_dtype x_dtype,
+                                     qrs_scale_layout scale_layout, float eps, const void* x, int64_t x_row_stride,
+                                     const void* residual, int64_t residual_row_stride, const void* weight,
+                                     void* sum_out, int64_t sum_row_stride, void* codes, int64_t codes_row_stride,
+                                     void* scales, void* stream);
+
+/*
+ * Gradients of y = s * r * weight, r = 1 / sqrt(mean(s^2) + eps), with the
+ * quantization passed through (its rounding has no gradient):
+ *
+ *   grad_x      = grad_sum + r * (weight * grad_y - s * r^2 * mean(weight * grad_y * s))
+ *   grad_weight = sum over tokens of grad_y * s * r
+ *
+ * grad_x is the gradient of s, and so of x and of residual alike. grad_sum
+ * is what reaches s by the residual stream; NULL = zero. All arithmetic is
+ * binary32; grad_x is rounded once to io_dtype, grad_weight is binary32.
+ *
+ *   grad_x      may be grad_y or grad_sum themselves (same pointer and
+ *               stride).
+ *   workspace   DEVICE memory of at least qrs_rms_norm_backward_workspace
+ *               bytes, 16-byte aligned, for this call alone until it ends.
+ */
+qrs_status qrs_rms_norm_backward_workspace(int64_t tokens, int64_t h, size_t* bytes_out);
+qrs_status qrs_rms_norm_backward(int64_t tokens, int64_t h, qrs_out_dtype io_dtype, float eps, const void* grad_y,
+                                 int64_t grad_y_row_stride, const void* sum, int64_t sum_row_stride,
+                                 const void* weight, const void* grad_sum, int64_t grad_sum_row_stride, void* grad_x,
+                                 int64_t grad_x_row_stride, float* grad_weight, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of activations or weights as codes with one binary32 scale for each
+ * row: qrs_quantize's per-group rule with the whole row as the group
+ * (scale = amax / qmax, codes = RNE(clamp(v * (qmax / amax), +-qmax)), the
+ * scale kept at or above 2^-126). NaN and infinity as for
+ * qrs_add_rms_norm_quantize. cols in [1, 65536].
+ */
+qrs_status qrs_quantize_rows(int64_t rows, int64_t cols, qrs_out_dtype in_dtype, qrs_x_dtype x_dtype, const void* x,
+                             int64_t x_row_stride, void* codes, int64_t codes_row_stride, float* scales, void* stream);
+
+/*
+ * out[i][j] = fp32(fp32(P[i][j]) * a_scales[i]) * b_scales[j], rounded to
+ * out_dtype, with P[i][j] the sum over k of a[i][k] * b[j][k]: a is [m, k]
+ * (tokens), b is [n, k] (output channels), both int8. The integer sum is
+ * exact (32 bits hold it up to the largest k), so the result does not depend
+ * on how the work is split.
+ *
+ *   gated      1: b is [2n, k], n gate channels and then n up channels, and
+ *              out = silu(g) * u of the two scaled products, with
+ *              silu(g) = g / (1 + exp(-g)) in binary32.
+ *   k          in [1, 131071]; m, n below 2^31.
+ *   a_scales   float32 [m]; b_scales float32 [n], or [2n] if gated.
+ *   workspace  DEVICE memory of at least qrs_matmul_int_workspace bytes (the
+ *              same for both calls), 16-byte aligned, for this call alone
+ *              until it ends; may be NULL where that size is 0.
+ */
+qrs_status qrs_matmul_int_workspace(int64_t m, int64_t n, int64_t k, int gated, size_t* bytes_out);
+qrs_status qrs_matmul_int(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype, const void* a,
+                          int64_t a_row_stride, const float* a_scales, const void* b, int64_t b_row_stride,
+                          const float* b_scales, void* out, int64_t out_row_stride, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * The same product (not gated), quantized in binary32 by qrs_quantize's
+ * rules: the codes and scales of one rank's partial sums, as qrs_run and
+ * qrs_run_all_shares read them. n is a multiple of 128 here; codes 16-byte
+ * aligned, its row stride a multiple of 16; scales contiguous [m, n / G].
+ * NaN and infinite scales as for qrs_add_rms_norm_quantize.
+ */
+qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype x_dtype,
+                                   qrs_scale_layout scale_layout, const void* a, int64_t a_row_stride,
+                                   const float* a_scales, const void* b, int64_t b_row_stride, const float* b_scales,
+                                   void* codes, int64_t codes_row_stride, void* scales, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* Free a plan. NULL is accepted. Plans in use by queued runs may be freed:
  * qrs_run copies what the kernel needs into its launch arguments. */

@@ -27,6 +27,8 @@ Modules:
 * ``quantize`` -- the producer side: bf16 activations to codes and scales,
   MX by the OCP Microscaling conversion, per-token-per-group by one fp32
   multiplier qmax / amax per group and one rounded product per element.
+* ``layer`` -- what a layer computes between two shares: residual sum and RMS
+  norm, its gradients, the scaled 8-bit product and its gated form.
 
 Pins (tests marked "not gpu"): every decode table entry against torch's CPU
 float8 casts; bf16 rounding against torch's CPU cast; ``reduce`` against
@@ -41,6 +43,8 @@ round-half-even, re-quantizing quantized MX blocks, hand-derived shared
 exponents, zero and tiny groups, a round-trip error bound, and hand-derived
 per-group cases at rounding midpoints that fix the multiplier reading
 against dividing by the stored scale or multiplying by its reciprocal.
+``layer``: the gradients against central differences, the product against
+Python integers, row scales against one group per row.
 """
 
 from .decode import (

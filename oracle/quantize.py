@@ -80,18 +80,24 @@ def encode_int8_rne(q):
 def quantize(x_bf16_bits, x_format, scale_layout):
     """bf16 ``[tokens, H]`` (uint16 bit patterns) -> (codes uint8
     ``[tokens, H]``, scales ``[tokens, H/G]``: float32 or E8M0 uint8)."""
+    return quantize_values(bf16_bits_to_fp32(x_bf16_bits), x_format, scale_layout)
+
+
+def quantize_values(v, x_format, scale_layout):
+    """``quantize`` of binary32 values. ``f32_row`` is the per-group rule with
+    the whole row as one group (scales ``[tokens, 1]``)."""
     if scale_layout == "e8m0_block32" and x_format == "int8":
         raise ValueError("INT8 is paired with fp32 per-group scales only")
-    g = GROUP_SIZE[scale_layout]
-    v = bf16_bits_to_fp32(x_bf16_bits)
+    v = np.asarray(v, dtype=np.float32)
     t, h = v.shape
+    g = h if scale_layout == "f32_row" else GROUP_SIZE[scale_layout]
     if h % g:
         raise ValueError(f"H={h} is not a multiple of {g}")
     if not np.all(np.isfinite(v)):
         raise ValueError("quantize takes finite inputs")
     blocks = v.reshape(t, h // g, g)
     amax = np.max(np.abs(blocks), axis=2)  # exact
-    if scale_layout == "f32_group128":
+    if scale_layout != "e8m0_block32":
         qmax = np.float32(QMAX[x_format])
         floor = np.float32(2.0 ** -126)
         scale = (amax / qmax).astype(np.float32)

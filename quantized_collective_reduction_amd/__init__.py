@@ -12,6 +12,13 @@ is no CPU fallback.
 
 ``x_slices`` / ``scale_slices`` are sequences of W device tensors (or raw
 device pointers as ints); ``out`` is a ``[rows, H]`` device tensor.
+
+What a layer computes between one share and the next, with 8-bit weights:
+
+    add_rms_norm_quantize(x, residual, weight, eps, total, codes, scales, "int8", "f32_row")
+    matmul_int8(codes, scales, w, w_scales, out)               # gated=True: silu(gate) * up
+    quantize_rows(out, codes2, scales2, "int8")
+    matmul_int8_quantize(codes2, scales2, w2, w2_scales, x_codes, x_scales, "e4m3fn", "e8m0_block32")
 """
 
 import ctypes
@@ -39,6 +46,11 @@ __all__ = [
     "StridedLaunch",
     "AllSharesLaunch",
     "QuantizeLaunch",
+    "add_rms_norm_quantize",
+    "rms_norm_backward",
+    "quantize_rows",
+    "matmul_int8",
+    "matmul_int8_quantize",
     "stream_copy",
     "run_launch_info",
     "LaunchInfo",
@@ -64,6 +76,7 @@ class XDtype(IntEnum):
 class ScaleLayout(IntEnum):
     F32_GROUP128 = 0
     E8M0_BLOCK32 = 1
+    F32_ROW = 2  # add_rms_norm_quantize only
 
 
 class OutDtype(IntEnum):
@@ -73,7 +86,8 @@ class OutDtype(IntEnum):
 
 
 _X_NAMES = {"int8": XDtype.INT8, "e4m3fn": XDtype.FP8_E4M3FN, "e5m2": XDtype.FP8_E5M2, "hifloat8": XDtype.HIFLOAT8}
-_SCALE_NAMES = {"f32_group128": ScaleLayout.F32_GROUP128, "e8m0_block32": ScaleLayout.E8M0_BLOCK32}
+_SCALE_NAMES = {"f32_group128": ScaleLayout.F32_GROUP128, "e8m0_block32": ScaleLayout.E8M0_BLOCK32,
+                "f32_row": ScaleLayout.F32_ROW}
 _OUT_NAMES = {"f32": OutDtype.F32, "bf16": OutDtype.BF16, "f16": OutDtype.F16}
 
 # Every function include/qrs.h declares.
@@ -93,6 +107,13 @@ EXPORTED_SYMBOLS = (
     "qrs_launch_create",
     "qrs_launch_enqueue",
     "qrs_launch_destroy",
+    "qrs_add_rms_norm_quantize",
+    "qrs_rms_norm_backward",
+    "qrs_rms_norm_backward_workspace",
+    "qrs_quantize_rows",
+    "qrs_matmul_int",
+    "qrs_matmul_int_quantize",
+    "qrs_matmul_int_workspace",
 )
 
 
@@ -165,6 +186,25 @@ def load_library(path: str = LIB_PATH):
     lib.qrs_stream_copy.restype = c_int
     lib.qrs_run_launch_info.argtypes = [vp, vp, ctypes.POINTER(LaunchInfo)]
     lib.qrs_run_launch_info.restype = c_int
+    c_f = ctypes.c_float
+    lib.qrs_add_rms_norm_quantize.argtypes = [c_i64, c_i64, c_int, c_int, c_int, c_f, vp, c_i64, vp, c_i64, vp, vp,
+                                              c_i64, vp, c_i64, vp, vp]
+    lib.qrs_add_rms_norm_quantize.restype = c_int
+    lib.qrs_rms_norm_backward_workspace.argtypes = [c_i64, c_i64, ctypes.POINTER(c_sz)]
+    lib.qrs_rms_norm_backward_workspace.restype = c_int
+    lib.qrs_rms_norm_backward.argtypes = [c_i64, c_i64, c_int, c_f, vp, c_i64, vp, c_i64, vp, vp, c_i64, vp, c_i64, vp,
+                                          vp, c_sz, vp]
+    lib.qrs_rms_norm_backward.restype = c_int
+    lib.qrs_quantize_rows.argtypes = [c_i64, c_i64, c_int, c_int, vp, c_i64, vp, c_i64, vp, vp]
+    lib.qrs_quantize_rows.restype = c_int
+    lib.qrs_matmul_int_workspace.argtypes = [c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]
+    lib.qrs_matmul_int_workspace.restype = c_int
+    lib.qrs_matmul_int.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, vp, c_i64, vp, vp, c_i64, vp, vp, c_i64, vp,
+                                   c_sz, vp]
+    lib.qrs_matmul_int.restype = c_int
+    lib.qrs_matmul_int_quantize.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, vp, c_i64, vp, vp, c_i64, vp, vp,
+                                            c_i64, vp, vp, c_sz, vp]
+    lib.qrs_matmul_int_quantize.restype = c_int
     _lib = lib
     return lib
 
@@ -567,6 +607,189 @@ class QuantizeLaunch:
         status = self._fn(*self._args)
         if status:
             _check(status)
+
+
+# ---- between two shares -----------------------------------------------------
+
+
+def _act_dtype(t, what):
+    import torch
+
+    kinds = {torch.float32: OutDtype.F32, torch.bfloat16: OutDtype.BF16, torch.float16: OutDtype.F16}
+    if t.dtype not in kinds:
+        raise ValueError(f"{what}: float32, bfloat16 or float16 expected, got {t.dtype}")
+    return int(kinds[t.dtype])
+
+
+def _matrix(t, what, shape=None, dtype=None):
+    """Row stride of a 2-D device view whose elements within a row are
+    adjacent, after checking its shape and element type."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: device tensors only (there is no CPU path)")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        want = "two dimensions" if shape is None else f"shape {list(shape)}"
+        raise ValueError(f"{what}: expected {want}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: elements within a row must be adjacent")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, what, n, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: device tensors only (there is no CPU path)")
+    if t.numel() != n or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError(f"{what}: {n} contiguous {dtype} elements expected, got {list(t.shape)} {t.dtype}")
+
+
+def _codes_and_scales(codes, scales, rows, h, xd, sl):
+    """Checks codes and scales of a mode; the codes' row stride."""
+    import torch
+
+    x_dt, s_dt, _ = _element_dtypes()
+    ld = _matrix(codes, "codes", (rows, h))
+    if codes.element_size() != 1:
+        raise ValueError(f"codes: 1-byte elements expected, got {codes.dtype}")
+    _check_dtype(codes, x_dt.get(xd), "codes")
+    n = rows if sl == ScaleLayout.F32_ROW else rows * h // (128 if sl == ScaleLayout.F32_GROUP128 else 32)
+    if sl == ScaleLayout.E8M0_BLOCK32:
+        _check_tensor(scales, n, "scales")
+        _check_dtype(scales, s_dt[sl], "scales")
+    else:
+        _vector(scales, "scales", n, torch.float32)
+    return ld
+
+
+def _workspace(workspace, nbytes, like, stream):
+    """The caller's workspace, or one from torch's allocator, which keeps it
+    until the work enqueued on ``stream`` so far has ended."""
+    import torch
+
+    if workspace is not None:
+        return _ptr(workspace), workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return ws.data_ptr(), nbytes
+
+
+def add_rms_norm_quantize(x, residual, weight, eps, sum_out, codes, scales, x_dtype, scale_layout, stream=None):
+    """s = x + residual, y = s / sqrt(mean(s**2) + eps) * weight along each
+    row, and y as codes and scales (qrs_add_rms_norm_quantize).
+
+    ``x``, ``residual``, ``sum_out``: ``[tokens, h]`` of one type (float32,
+    bfloat16 or float16); ``weight``: ``[h]`` of that type. ``sum_out`` receives
+    s and may be ``x`` or ``residual`` itself. With ``residual=None``, s = x and
+    ``sum_out`` is not used. ``scale_layout``: "f32_group128", "e8m0_block32",
+    or "f32_row" (one scale per token, for ``matmul_int8``)."""
+    lib = load_library()
+    io = _act_dtype(x, "x")
+    ld_x = _matrix(x, "x")
+    tokens, h = x.shape
+    _vector(weight, "weight", h, x.dtype)
+    ld_r = ld_s = 0
+    if residual is not None:
+        ld_r = _matrix(residual, "residual", x.shape, x.dtype)
+        ld_s = _matrix(sum_out, "sum_out", x.shape, x.dtype)
+    xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
+    ld_c = _codes_and_scales(codes, scales, tokens, h, xd, sl)
+    _check(lib.qrs_add_rms_norm_quantize(
+        tokens, h, io, int(xd), int(sl), eps, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(),
+        ld_r, weight.data_ptr(), None if residual is None else sum_out.data_ptr(), ld_s, codes.data_ptr(), ld_c,
+        _ptr(scales), _stream_handle(stream)))
+
+
+def rms_norm_backward(grad_y, sum, weight, eps, grad_sum, grad_x, grad_weight, workspace=None, stream=None):
+    """Gradients of ``add_rms_norm_quantize``'s y, with the quantization passed
+    through (qrs_rms_norm_backward): ``grad_x`` of s (so of x and of residual
+    alike), ``grad_weight`` (float32 ``[h]``).
+
+    ``sum`` is s; ``grad_sum`` the gradient that reaches s by the residual
+    stream (None = zero). ``grad_x`` may be ``grad_y`` or ``grad_sum`` itself.
+    ``workspace``: device memory of ``rms_norm_backward_workspace`` bytes, by
+    default taken from torch's allocator."""
+    import torch
+
+    lib = load_library()
+    io = _act_dtype(sum, "sum")
+    ld_s = _matrix(sum, "sum")
+    tokens, h = sum.shape
+    ld_y = _matrix(grad_y, "grad_y", sum.shape, sum.dtype)
+    ld_g = 0 if grad_sum is None else _matrix(grad_sum, "grad_sum", sum.shape, sum.dtype)
+    ld_x = _matrix(grad_x, "grad_x", sum.shape, sum.dtype)
+    _vector(weight, "weight", h, sum.dtype)
+    _vector(grad_weight, "grad_weight", h, torch.float32)
+    need = ctypes.c_size_t()
+    _check(lib.qrs_rms_norm_backward_workspace(tokens, h, ctypes.byref(need)))
+    ws, nbytes = _workspace(workspace, need.value, sum, stream)
+    _check(lib.qrs_rms_norm_backward(
+        tokens, h, io, eps, grad_y.data_ptr(), ld_y, sum.data_ptr(), ld_s, weight.data_ptr(),
+        None if grad_sum is None else grad_sum.data_ptr(), ld_g, grad_x.data_ptr(), ld_x, grad_weight.data_ptr(), ws,
+        nbytes, _stream_handle(stream)))
+
+
+def quantize_rows(x, codes, scales, x_dtype="int8", stream=None):
+    """Rows of activations or weights ``[rows, cols]`` (float32, bfloat16 or
+    float16) as ``codes`` with one float32 scale per row (qrs_quantize_rows)."""
+    lib = load_library()
+    kind = _act_dtype(x, "x")
+    ld_x = _matrix(x, "x")
+    rows, cols = x.shape
+    xd = _enum(x_dtype, _X_NAMES, XDtype)
+    ld_c = _codes_and_scales(codes, scales, rows, cols, xd, ScaleLayout.F32_ROW)
+    _check(lib.qrs_quantize_rows(rows, cols, kind, int(xd), x.data_ptr(), ld_x, codes.data_ptr(), ld_c,
+                                 scales.data_ptr(), _stream_handle(stream)))
+
+
+def _matmul_operands(lib, a, a_scales, b, b_scales, gated, workspace, stream):
+    import torch
+
+    ld_a = _matrix(a, "a", None, torch.int8)
+    ld_b = _matrix(b, "b", None, torch.int8)
+    m, k = a.shape
+    wide = b.shape[0]
+    if b.shape[1] != k or (gated and wide % 2):
+        raise ValueError(f"b: expected [{'2 n' if gated else 'n'}, {k}], got {list(b.shape)}")
+    _vector(a_scales, "a_scales", m, torch.float32)
+    _vector(b_scales, "b_scales", wide, torch.float32)
+    n = wide // 2 if gated else wide
+    need = ctypes.c_size_t()
+    _check(lib.qrs_matmul_int_workspace(m, n, k, 1 if gated else 0, ctypes.byref(need)))
+    ws, nbytes = _workspace(workspace, need.value, a, stream)
+    return m, n, k, ld_a, ld_b, ws, nbytes
+
+
+def matmul_int8(a, a_scales, b, b_scales, out, gated=False, workspace=None, stream=None):
+    """``out = (a @ b.T) * a_scales[:, None] * b_scales`` of int8 ``a [m, k]``
+    (tokens) and ``b [n, k]`` (channels), float32 scales, summed exactly
+    (qrs_matmul_int). ``out [m, n]``: float32, bfloat16 or float16.
+
+    ``gated``: ``b`` is ``[2 n, k]``, n gate and then n up channels, and
+    ``out = silu(gate product) * up product``. ``workspace``: device memory of
+    qrs_matmul_int_workspace bytes, by default taken from torch's allocator."""
+    lib = load_library()
+    m, n, k, ld_a, ld_b, ws, nbytes = _matmul_operands(lib, a, a_scales, b, b_scales, gated, workspace, stream)
+    kind = _act_dtype(out, "out")
+    ld_o = _matrix(out, "out", (m, n))
+    _check(lib.qrs_matmul_int(m, n, k, 1 if gated else 0, kind, a.data_ptr(), ld_a, a_scales.data_ptr(), b.data_ptr(),
+                              ld_b, b_scales.data_ptr(), out.data_ptr(), ld_o, ws, nbytes, _stream_handle(stream)))
+
+
+def matmul_int8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_layout, workspace=None, stream=None):
+    """``matmul_int8``'s product, quantized in float32 into the codes
+    ``[m, n]`` and scales that ``run`` and ``run_all_shares`` read
+    (qrs_matmul_int_quantize): one rank's partial sums. n is a multiple of 128."""
+    lib = load_library()
+    m, n, k, ld_a, ld_b, ws, nbytes = _matmul_operands(lib, a, a_scales, b, b_scales, False, workspace, stream)
+    xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
+    ld_c = _codes_and_scales(codes, scales, m, n, xd, sl)
+    _check(lib.qrs_matmul_int_quantize(m, n, k, int(xd), int(sl), a.data_ptr(), ld_a, a_scales.data_ptr(),
+                                       b.data_ptr(), ld_b, b_scales.data_ptr(), codes.data_ptr(), ld_c, _ptr(scales),
+                                       ws, nbytes, _stream_handle(stream)))
 
 
 def run_launch_info(p: Plan, stream=None) -> dict:

@@ -12,6 +12,7 @@ import os
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_ROOT = os.path.dirname(PKG_DIR)
@@ -23,6 +24,9 @@ SOURCES = [
     os.path.join(CSRC, "qrs.cpp"),
     os.path.join(CSRC, "qrs_kernels.hip"),
     os.path.join(CSRC, "qrs_quantize.hip"),
+    os.path.join(CSRC, "qrs_layer.cpp"),
+    os.path.join(CSRC, "qrs_rows.hip"),
+    os.path.join(CSRC, "qrs_matmul.hip"),
 ]
 
 BASE_FLAGS = [
@@ -47,17 +51,31 @@ def hipcc() -> str:
 
 
 def build(out_path: str = LIB_PATH, defines=(), verbose: bool = False) -> str:
-    """Compile the sources into ``out_path`` (atomically replaced)."""
+    """Compile the sources into ``out_path`` (atomically replaced): one
+    compiler per source at a time on each of up to eight threads, then one
+    link."""
     out_dir = os.path.dirname(os.path.abspath(out_path))
     fd, tmp = tempfile.mkstemp(prefix=".libqrs.", suffix=".so.tmp", dir=out_dir)
     os.close(fd)
-    cmd = [hipcc(), *BASE_FLAGS, "-I", INCLUDE, "-I", CSRC, *[f"-D{d}" for d in defines], *SOURCES, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    try:
+    flags = [f for f in BASE_FLAGS if f != "-shared"]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
+
+    try:
+        with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(max_workers=8) as pool:
+            jobs = []
+            for src in SOURCES:
+                obj = os.path.join(objs, os.path.basename(src) + ".o")
+                jobs.append((obj, pool.submit(run, [hipcc(), *flags, "-I", INCLUDE, "-I", CSRC,
+                                                    *[f"-D{d}" for d in defines], "-c", src, "-o", obj])))
+            for _, job in jobs:
+                job.result()
+            run([hipcc(), "--offload-arch=gfx950", "-shared", *[obj for obj, _ in jobs], "-o", tmp])
         os.replace(tmp, out_path)
     finally:
         if os.path.exists(tmp):

@@ -12,6 +12,7 @@
 #include <cstring>
 #include <new>
 
+#include "qrs_host.h"
 #include "qrs_launch.h"
 
 struct qrs_launch_s {
@@ -30,9 +31,11 @@ struct qrs_plan_s {
   qrs::OutFormat out_format;
 };
 
-namespace {
+namespace qrs {
 
+namespace {
 thread_local char g_last_error[512];
+}
 
 qrs_status fail(qrs_status s, const char* fmt, ...) {
   va_list ap;
@@ -47,12 +50,16 @@ qrs_status ok() {
   return QRS_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+const char* last_error() { return g_last_error; }
 
-bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
+}  // namespace qrs
+
+namespace {
+
+using qrs::aligned;
+using qrs::fail;
+using qrs::ok;
+using qrs::overlaps;
 
 // The (x format, scale layout) pair selects one of the page's modes.
 qrs_status check_mode(qrs_x_dtype x_dtype, qrs_scale_layout scale_layout) {
@@ -61,7 +68,7 @@ qrs_status check_mode(qrs_x_dtype x_dtype, qrs_scale_layout scale_layout) {
   if (x_dtype != QRS_X_INT8 && x_dtype != QRS_X_FP8_E4M3FN && x_dtype != QRS_X_FP8_E5M2)
     return fail(QRS_ERR_INVALID_ARG, "x_dtype %d is not a qrs_x_dtype", static_cast<int>(x_dtype));
   if (scale_layout != QRS_SCALE_F32_GROUP128 && scale_layout != QRS_SCALE_E8M0_BLOCK32)
-    return fail(QRS_ERR_INVALID_ARG, "scale_layout %d is not a qrs_scale_layout", static_cast<int>(scale_layout));
+    return fail(QRS_ERR_INVALID_ARG, "scale_layout %d is not a mode of the reduce-scatter", static_cast<int>(scale_layout));
   // MX mode (E8M0 scales) is defined for the FP8 formats only.
   if (scale_layout == QRS_SCALE_E8M0_BLOCK32 && x_dtype == QRS_X_INT8)
     return fail(QRS_ERR_INVALID_ARG, "INT8 x is paired with fp32 per-group scales only");
@@ -191,7 +198,7 @@ const char* qrs_status_string(qrs_status status) {
   return "QRS_ERR_UNKNOWN";
 }
 
-const char* qrs_last_error(void) { return g_last_error; }
+const char* qrs_last_error(void) { return qrs::last_error(); }
 
 qrs_status qrs_plan(int world_size, int64_t bs, int64_t h, qrs_x_dtype x_dtype, qrs_scale_layout scale_layout,
                     qrs_out_dtype out_dtype, qrs_plan_t* plan_out, size_t* workspace_bytes_out) {
