@@ -46,10 +46,9 @@ __device__ __forceinline__ PieceScales piece_scales(const MatmulLaunch& a, uint3
 // Eight outputs [j0, j0 + 8) of token i from their integer sums. `active`
 // says whether i and j0 are inside the output; in the quantized form all
 // lanes of a group (16 or 4 consecutive ones) call this together.
-__device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active,
+__device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, float sa,
                                              const PieceScales& s, const int32_t* acc, const int32_t* up) {
   float v[kPiece];
-  const float sa = active ? a.a_scales[i] : 0.0f;
 #pragma unroll
   for (int j = 0; j < kPiece; ++j) v[j] = static_cast<float>(acc[j]) * sa * s.b[j];
   if (a.quantize) {
@@ -179,7 +178,8 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulLaunch a) {
   for (uint32_t t = threadIdx.x; t < kTileM * pieces; t += 256) {
     const uint32_t i = t / pieces, j = t % pieces * kPiece;
     const int32_t* p = lc + i * kCPitch + j;
-    finish_piece(a, i0 + i, j0 + j, i0 + i < a.m && j0 + j < a.n, piece_scales(a, j0 + j), p, p + kTileN / 2);
+    finish_piece(a, i0 + i, j0 + j, i0 + i < a.m && j0 + j < a.n, a.a_scales[min(i0 + i, a.m - 1)],
+                 piece_scales(a, j0 + j), p, p + kTileN / 2);
   }
 }
 
@@ -198,9 +198,9 @@ hipError_t launch_tiles(const MatmulLaunch& l, hipStream_t stream) {
 //
 // Operands go from memory straight into LDS, S - 1 stages ahead. A stage's
 // row is 64 bytes, four chunks of 16; chunk c of row r lies in slot
-// c ^ (r / 2 % 4), so that the eight lanes of a 128-byte LDS read (eight
-// rows, one chunk) touch every bank once. The load fills LDS in lane order,
-// so each lane asks for the chunk that belongs in its slot.
+// c ^ (r / 4 % 4), so that the sixteen lanes that LDS serves at once (rows
+// r .. r + 15, one chunk) touch each of its 64 banks once. The load fills LDS
+// in lane order, so each lane asks for the chunk that belongs in its slot.
 //
 // One barrier a stage, between the products of its first and second half:
 // by then every wave holds the stage's second half in registers (its LDS is
@@ -254,6 +254,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, WTN, S>::kThreads), 1) void pipe
   using P = Pipe<TM, TN, WTM, WTN, S>;
   constexpr int FM = P::FM, FN = P::FN;
   __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+  __shared__ float token_scale[TM];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave % P::kWavesM, wn = wave / P::kWavesM;
@@ -279,7 +280,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, WTN, S>::kThreads), 1) void pipe
       const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, 0x7FFFFFFF, 0x00020000);
   uint32_t off_a[P::kLoadsA], off_b[P::kLoadsB];
   const uint32_t row16 = lane / kChunks;
-  const uint32_t chunk = (lane % kChunks ^ row16 / 2 % kChunks) * 16;
+  const uint32_t chunk = (lane % kChunks ^ row16 / 4 % kChunks) * 16;
 #pragma unroll
   for (int t = 0; t < P::kLoadsA; ++t) {
     // Rows past the end load the last row; what they give is not stored.
@@ -326,6 +327,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, WTN, S>::kThreads), 1) void pipe
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
+  for (uint32_t t = threadIdx.x; t < TM; t += P::kThreads) token_scale[t] = a.a_scales[min(i0 + t, a.m - 1)];
   if (tail != 0) load_stage(0, a.k - tail, chunk < tail ? chunk : 0);
 #pragma unroll
   for (uint32_t st = 0; st < S; ++st)
@@ -346,7 +348,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, WTN, S>::kThreads), 1) void pipe
   }
 
   // Lane l reads row l % 32 of a fragment, chunk l / 32 of the half's two.
-  const uint32_t swz = lane / 2 % kChunks;
+  const uint32_t swz = lane / 4 % kChunks;
   const uint32_t lane_off[2] = {lane % 32 * kStep + ((lane / 32) ^ swz) * 16, lane % 32 * kStep + ((2 + lane / 32) ^ swz) * 16};
   const char* base_a = lds + wm * WTM * kStep;
   const char* base_b = lds + TM * kStep + wn * WTN * kStep;
@@ -416,7 +418,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, WTN, S>::kThreads), 1) void pipe
 #pragma unroll
         for (int e = 0; e < kPiece; ++e) u[e] = p[WTN / 2 + e];
       }
-      finish_piece(a, i, j, i < a.m && j < a.n, scales, v, u);
+      finish_piece(a, i, j, i < a.m && j < a.n, token_scale[wm * WTM + 32 * f + t], scales, v, u);
     }
   }
 #endif
