@@ -211,14 +211,12 @@ __device__ __forceinline__ float exp2_int(int k) {
 
 // What a group with this absolute maximum is multiplied by, and its scale.
 // f32 scales: scale = amax / qmax, at least 2^-126 (zero groups included).
-template <int XF>
-__device__ __forceinline__ float f32_multiplier(uint32_t amax_bits, float* scale) {
-  constexpr float kMax = CodeFormat<XF>::kMax;
+__device__ __forceinline__ float f32_multiplier(uint32_t amax_bits, float top, float* scale) {
   const float amax = __builtin_bit_cast(float, amax_bits);
-  const float s = amax / kMax;
+  const float s = amax / top;
   const bool small = s < 0x1p-126f;
   *scale = small ? 0x1p-126f : s;
-  return small ? 0x1p126f : kMax / amax;
+  return small ? 0x1p126f : top / amax;
 }
 
 // E8M0: the scale 2^(floor(log2 amax) - emax) limited to [2^-127, 2^127];
@@ -277,7 +275,7 @@ __device__ __forceinline__ void quantize_group_piece(const float* v, bool active
   float mul, scale = 0.0f;
   uint32_t code = 0;
   if constexpr (SL == kScaleF32Group128)
-    mul = f32_multiplier<XF>(amax, &scale);
+    mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
   else
     mul = mx_multiplier<XF>(amax, &code);
   const u32x2 w = encode_piece<XF>(v, mul);

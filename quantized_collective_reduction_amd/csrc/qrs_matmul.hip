@@ -28,67 +28,96 @@ using namespace dev;
 
 // ---- epilogue ----------------------------------------------------------
 
-// The scales of channels [j0, j0 + 8) of a token's piece.
+// What a kernel instance writes.
+enum Finish : int { kValues = 0, kGated = 1, kCodes = 2 };
+
+// The scales of channels [j0, j0 + 8): of the product, or of its gate, and
+// of its up channels.
 struct PieceScales {
   float b[kPiece], up[kPiece];
 };
 
+template <int F>
 __device__ __forceinline__ PieceScales piece_scales(const MatmulLaunch& a, uint32_t j0) {
   PieceScales s;
 #pragma unroll
   for (int j = 0; j < kPiece; ++j) {
     s.b[j] = j0 + j < a.n ? a.b_scales[j0 + j] : 0.0f;
-    s.up[j] = a.gated && j0 + j < a.n ? a.b_scales[a.n + j0 + j] : 0.0f;
+    if constexpr (F == kGated) s.up[j] = j0 + j < a.n ? a.b_scales[a.n + j0 + j] : 0.0f;
   }
   return s;
 }
 
-// Eight outputs [j0, j0 + 8) of token i from their integer sums. `active`
-// says whether i and j0 are inside the output; in the quantized form all
-// lanes of a group (16 or 4 consecutive ones) call this together.
-__device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, float sa,
-                                             const PieceScales& s, const int32_t* acc, const int32_t* up) {
-  float v[kPiece];
+// The codes of a piece and its group's scale, the mode chosen at run time: a
+// kernel's epilogue repeats this for every fragment, and a copy for each mode
+// would be five times the code.
+__device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, const float* v) {
+  const bool mx = a.scale_layout == kScaleE8M0Block32;
+  uint32_t amax = 0;
 #pragma unroll
-  for (int j = 0; j < kPiece; ++j) v[j] = static_cast<float>(acc[j]) * sa * s.b[j];
-  if (a.quantize) {
-    uint8_t* codes_row = static_cast<uint8_t*>(a.out) + static_cast<uint64_t>(i) * a.out_stride;
-    if (a.scale_layout == kScaleF32Group128) {
-      const uint64_t first = static_cast<uint64_t>(i) * (a.n / 128);
-      if (a.x_format == kXE4M3FN)
-        quantize_group_piece<kXE4M3FN, kScaleF32Group128, true>(v, active, j0, a.n, codes_row, a.scales, first);
-      else if (a.x_format == kXE5M2)
-        quantize_group_piece<kXE5M2, kScaleF32Group128, true>(v, active, j0, a.n, codes_row, a.scales, first);
-      else
-        quantize_group_piece<kXInt8, kScaleF32Group128, true>(v, active, j0, a.n, codes_row, a.scales, first);
-    } else {
-      const uint64_t first = static_cast<uint64_t>(i) * (a.n / 32);
-      if (a.x_format == kXE4M3FN)
-        quantize_group_piece<kXE4M3FN, kScaleE8M0Block32, true>(v, active, j0, a.n, codes_row, a.scales, first);
-      else
-        quantize_group_piece<kXE5M2, kScaleE8M0Block32, true>(v, active, j0, a.n, codes_row, a.scales, first);
-    }
-    return;
-  }
-  if (!active) return;
-  if (a.gated) {
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-      const float u = static_cast<float>(up[j]) * sa * s.up[j];
-      v[j] = v[j] / (1.0f + expf(-v[j])) * u;
-    }
-  }
-  const uint64_t row = static_cast<uint64_t>(i) * a.out_stride;
-  const bool whole = a.out_vec && j0 + kPiece <= a.n;
-  if (a.out_format == kOutF32) {
-    float* p = static_cast<float*>(a.out) + row;
-    whole ? store_piece<kOutF32, true>(p, j0, a.n, v) : store_piece<kOutF32, false>(p, j0, a.n, v);
-  } else if (a.out_format == kOutBF16) {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + row;
-    whole ? store_piece<kOutBF16, true>(p, j0, a.n, v) : store_piece<kOutBF16, false>(p, j0, a.n, v);
+  for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[j]));
+  amax = group_max<4>(amax);
+  float mul, scale = 0.0f;
+  uint32_t code = 0;
+  if (mx) {
+    mul = a.x_format == kXE4M3FN ? mx_multiplier<kXE4M3FN>(amax, &code) : mx_multiplier<kXE5M2>(amax, &code);
   } else {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + row;
-    whole ? store_piece<kOutF16, true>(p, j0, a.n, v) : store_piece<kOutF16, false>(p, j0, a.n, v);
+    amax = max(amax, dpp<kDppHalfMirror>(amax));
+    amax = max(amax, dpp<kDppMirror>(amax));
+    const float top = a.x_format == kXE4M3FN ? CodeFormat<kXE4M3FN>::kMax
+                      : a.x_format == kXE5M2 ? CodeFormat<kXE5M2>::kMax
+                                             : CodeFormat<kXInt8>::kMax;
+    mul = f32_multiplier(amax, top, &scale);
+  }
+  u32x2 w;
+  if (a.x_format == kXE4M3FN)
+    w = encode_piece<kXE4M3FN>(v, mul);
+  else if (a.x_format == kXE5M2)
+    w = encode_piece<kXE5M2>(v, mul);
+  else
+    w = encode_piece<kXInt8>(v, mul);
+  if (!active) return;
+  *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + static_cast<uint64_t>(i) * a.out_stride + j0) = w;
+  if (mx) {
+    if (j0 % 32 == 0)
+      static_cast<uint8_t*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 32) + j0 / 32] = static_cast<uint8_t>(code);
+  } else {
+    if (j0 % 128 == 0) static_cast<float*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 128) + j0 / 128] = scale;
+  }
+}
+
+template <int OF>
+__device__ __forceinline__ void finish_values(const MatmulLaunch& a, uint32_t i, uint32_t j0, const float* v) {
+  char* row = static_cast<char*>(a.out) + static_cast<uint64_t>(i) * a.out_stride * kOutSize<OF>;
+  if (a.out_vec && j0 + kPiece <= a.n)
+    store_piece<OF, true>(row, j0, a.n, v);
+  else
+    store_piece<OF, false>(row, j0, a.n, v);
+}
+
+// Eight outputs [j0, j0 + 8) of token i. v: the integer sums as binary32
+// times the token's scale (gated: of the gates; up: of the ups). `active`
+// says whether i and j0 are inside the output; where codes are written, all
+// lanes of a group (16 or 4 consecutive ones) call this together.
+template <int F>
+__device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active,
+                                             const PieceScales& s, float* v, const float* up) {
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) v[j] *= s.b[j];
+  if constexpr (F == kCodes) {
+    finish_codes(a, i, j0, active, v);
+  } else {
+    if constexpr (F == kGated) {
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) v[j] = v[j] / (1.0f + expf(-v[j])) * (up[j] * s.up[j]);
+    }
+    if (!active) return;
+    if (a.out_format == kOutF32)
+      finish_values<kOutF32>(a, i, j0, v);
+    else if (a.out_format == kOutBF16)
+      finish_values<kOutBF16>(a, i, j0, v);
+    else
+      finish_values<kOutF16>(a, i, j0, v);
   }
 }
 
@@ -116,13 +145,13 @@ constexpr int kTileM = 64, kTileN = 128, kTileK = 64;
 constexpr int kPitch = kTileK + 16;   // bytes; rows 5 quarter-lines apart
 constexpr int kCPitch = kTileN + 4;   // words of the staged sums
 
-template <bool VEC>
+template <bool VEC, int F>
 __global__ __launch_bounds__(256) void tile_kernel(const MatmulLaunch a) {
   __shared__ __attribute__((aligned(16))) char lds[kTileM * kCPitch * 4];
   static_assert((kTileM + kTileN) * kPitch <= kTileM * kCPitch * 4, "operands share the staging buffer");
   char* la = lds;
   char* lb = lds + kTileM * kPitch;
-  const uint32_t tile_n = a.gated ? kTileN / 2 : kTileN;
+  constexpr uint32_t tile_n = F == kGated ? kTileN / 2 : kTileN;
   const uint32_t tiles_n = (a.n + tile_n - 1) / tile_n;
   const uint32_t i0 = blockIdx.x / tiles_n * kTileM;
   const uint32_t j0 = blockIdx.x % tiles_n * tile_n;
@@ -141,7 +170,7 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulLaunch a) {
   const int8_t* pb[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t rb = a.gated ? min(j0 + r, a.n - 1) + (h ? a.n : 0) : min(j0 + r + 64 * h, a.n - 1);
+    const uint32_t rb = F == kGated ? min(j0 + r, a.n - 1) + (h ? a.n : 0) : min(j0 + r + 64 * h, a.n - 1);
     pb[h] = a.b + rb * a.b_stride;
   }
   for (uint32_t k0 = 0; k0 < a.k; k0 += kTileK) {
@@ -174,40 +203,59 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulLaunch a) {
     for (int j = 0; j < 2; ++j)
       *reinterpret_cast<i32x4*>(lc + (16 * i + lane % 16) * kCPitch + 32 * wave + 16 * j + lane / 16 * 4) = acc[i][j];
   __syncthreads();
-  const uint32_t pieces = tile_n / kPiece;
+  constexpr uint32_t pieces = tile_n / kPiece;
   for (uint32_t t = threadIdx.x; t < kTileM * pieces; t += 256) {
     const uint32_t i = t / pieces, j = t % pieces * kPiece;
     const int32_t* p = lc + i * kCPitch + j;
-    finish_piece(a, i0 + i, j0 + j, i0 + i < a.m && j0 + j < a.n, a.a_scales[min(i0 + i, a.m - 1)],
-                 piece_scales(a, j0 + j), p, p + kTileN / 2);
+    const float sa = a.a_scales[min(i0 + i, a.m - 1)];
+    float v[kPiece], up[kPiece];
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      v[e] = static_cast<float>(p[e]) * sa;
+      if constexpr (F == kGated) up[e] = static_cast<float>(p[kTileN / 2 + e]) * sa;
+    }
+    finish_piece<F>(a, i0 + i, j0 + j, i0 + i < a.m && j0 + j < a.n, piece_scales<F>(a, j0 + j), v, up);
   }
 }
 
-template <bool VEC>
+template <bool VEC, int F>
 hipError_t launch_tiles(const MatmulLaunch& l, hipStream_t stream) {
   const uint32_t tile_n = l.gated ? kTileN / 2 : kTileN;
   const uint64_t tiles = static_cast<uint64_t>((l.m + kTileM - 1) / kTileM) * ((l.n + tile_n - 1) / tile_n);
   if (tiles >= uint64_t{1} << 24) return hipErrorInvalidValue;  // 2^32 work-items
-  return launch_kernel(tile_kernel<VEC>, dim3(static_cast<uint32_t>(tiles)), dim3(256), stream, l);
+  return launch_kernel(tile_kernel<VEC, F>, dim3(static_cast<uint32_t>(tiles)), dim3(256), stream, l);
 }
 
 // ---- pipelined tile kernel ---------------------------------------------
 
 // TM tokens by TN rows of b, kStep bytes of k a stage, S stages in LDS.
-// Waves of WTM tokens by WTN rows of b in 32x32x32 products.
+// Waves of WTM tokens by 128 rows of b in 16x16x64 products: with operands
+// of random bits the card's power limit holds a loop of these from registers
+// to 4.1 POP/s, and of 32x32x32 ones (more accumulator traffic) to 3.5.
 //
-// Operands go from memory straight into LDS, S - 1 stages ahead. A stage's
-// row is 64 bytes, four chunks of 16; chunk c of row r lies in slot
-// c ^ (r / 4 % 4), so that the sixteen lanes that LDS serves at once (rows
-// r .. r + 15, one chunk) touch each of its 64 banks once. The load fills LDS
-// in lane order, so each lane asks for the chunk that belongs in its slot.
+// Work-groups stay on the card and walk over tiles. Operands go from memory
+// straight into LDS, up to S stages ahead and across the end of a tile, so
+// that a tile's epilogue runs while the next one's first stages arrive.
 //
-// One barrier a stage, between the products of its first and second half:
-// by then every wave holds the stage's second half in registers (its LDS is
-// free for the stage S ahead), and the next stage has landed, so its first
-// half is read while the second half is multiplied.
+// A stage's row is 64 bytes, four chunks of 16; chunk c of row r lies in
+// slot c ^ swizzle(r / 4 % 4). LDS serves a 16-byte read of a wave in four
+// groups of 16 lanes, {0-3, 12-15, 20-23, 24-27} and {4-11, 16-19, 28-31} of
+// each half; with this order of slots none of them has two lanes on a bank
+// (measured: c ^ (r / 4 % 4) doubles the reads' time). The loads fill LDS in
+// lane order, so each lane asks for the chunk that belongs in its slot.
+//
+// A wave's products of a stage are four quarters, of half its a and half its
+// b fragments each, in an order in which consecutive quarters share one half:
+// then the other is free to be read for the quarter after, and one set of
+// fragment registers is enough (a second one costs 32 moves a stage):
+//   even stages  (a0 b0) (a0 b1) | (a1 b1) (a1 b0)
+//   odd stages   (a0 b1) (a0 b0) | (a1 b0) (a1 b1)
+// At the bar, the stage's one barrier, every wave holds the whole stage in
+// registers (its LDS is free for the stage S ahead) and the next stage has
+// landed.
 constexpr int kStep = 64;
 constexpr int kChunks = kStep / 16;
+constexpr int kWaveN = 128;
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -218,217 +266,298 @@ __device__ __forceinline__ void wait_loads_and_sync() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Orders what was issued since the last barrier: R reads from LDS
-// each behind one of the first products, then L loads to LDS each behind one
-// of the next, so that the matrix unit never waits for a row of other
-// instructions to issue.
-template <int R, int L>
-__device__ __forceinline__ void spread() {
-  constexpr int kMfma = 0x8, kVmemRead = 0x20, kDsRead = 0x100;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < L; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
-  }
+// acc += b a^T of one 16x16x64 product, in place. Written out because the
+// compiler takes a result for a value of its own and, over several stages,
+// moves accumulators between registers inside the pipeline. It sees no
+// matrix instruction here, so the waits that such results need before other
+// instructions touch them stand in settle().
+__device__ __forceinline__ void mfma(i32x4& acc, const i32x4& b, const i32x4& a) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
-template <int TM, int TN, int WTM, int WTN, int S>
+// A row of accumulators, readable by other instructions (after at most 18
+// cycles) and, cleared, by the next products.
+template <int N>
+__device__ __forceinline__ void settle(i32x4 (&acc)[N]) {
+  static_assert(N == 8, "one operand for each");
+  asm volatile("s_nop 15\n\ts_nop 3"
+               : "+a"(acc[0]), "+a"(acc[1]), "+a"(acc[2]), "+a"(acc[3]), "+a"(acc[4]), "+a"(acc[5]), "+a"(acc[6]),
+                 "+a"(acc[7]));
+}
+
+template <int TM, int TN, int WTM, int S>
 struct Pipe {
-  static constexpr int kWavesM = TM / WTM, kWavesN = TN / WTN, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
-  static constexpr int FM = WTM / 32, FN = WTN / 32;
+  static constexpr int kWavesM = TM / WTM, kWavesN = TN / kWaveN, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
+  static constexpr int FM = WTM / 16, FN = kWaveN / 16;
   static constexpr int kLoadsA = TM / 16 / kWaves, kLoadsB = TN / 16 / kWaves, kLoads = kLoadsA + kLoadsB;
   static constexpr int kStageBytes = (TM + TN) * kStep;
-  static constexpr int kSumPitch = WTN + 4;  // words of a staged token
-  static constexpr int kLds = S * kStageBytes > kWaves * 32 * kSumPitch * 4 ? S * kStageBytes : kWaves * 32 * kSumPitch * 4;
+  static constexpr int kSumsBytes = 16 * kWaveN * 4;  // 16 tokens of a wave
+  static constexpr int kLds = S * kStageBytes + kWaves * kSumsBytes;
+  static constexpr int kPerCu = 163840 / kLds;  // work-groups a CU holds
   static_assert(TM % (16 * kWaves) == 0 && TN % (16 * kWaves) == 0, "whole loads a wave");
+  static_assert(kLoads % 4 == 0 && S % 2 == 0 && FM % 2 == 0, "quarters");
 };
 
-template <int TM, int TN, int WTM, int WTN, int S>
-__global__ __launch_bounds__((Pipe<TM, TN, WTM, WTN, S>::kThreads), 1) void pipe_kernel(const MatmulLaunch a) {
+// Offsets of rows within a tile stay below kFar; a lane that has nothing to
+// load adds kFar, which is past the buffer's range, so that the hardware's
+// range check gives zero.
+constexpr uint32_t kFar = 1u << 30;
+
+// Tiles in the order in which an XCD should run them: patches of kGroup
+// token tiles by whole columns share their operands in its L2.
+struct TileOrder {
+  uint32_t tiles_m, tiles_n;
+  __device__ void at(uint32_t tile, uint32_t* tm, uint32_t* tn) const {
+    constexpr uint32_t kGroup = 8;
+    const uint32_t group = tile / (kGroup * tiles_n), in_group = tile % (kGroup * tiles_n);
+    const uint32_t group_m = min(kGroup, tiles_m - group * kGroup);
+    *tm = group * kGroup + in_group % group_m;
+    *tn = in_group / group_m;
+  }
+};
+
+template <int TM, int TN, int WTM, int S, int F>
+__global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kernel(const MatmulLaunch a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the buffer builtins' types exist in the device pass alone
-  using P = Pipe<TM, TN, WTM, WTN, S>;
-  constexpr int FM = P::FM, FN = P::FN;
+  using P = Pipe<TM, TN, WTM, S>;
+  constexpr int FM = P::FM, FN = P::FN, HM = FM / 2, HN = FN / 2;
   __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
-  __shared__ float token_scale[TM];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave % P::kWavesM, wn = wave / P::kWavesM;
 
-  // Work-groups go round the eight XCDs, so XCD x takes every eighth one:
-  // give it a run of consecutive tiles, and order tiles so that a run is a
-  // patch of kGroup tokens-tiles by whole columns, which shares its operands
-  // in the XCD's L2.
-  constexpr uint32_t kGroup = 8;
-  const uint32_t tile_n = a.gated ? TN / 2 : TN;
-  const uint32_t tiles_m = (a.m + TM - 1) / TM, tiles_n = (a.n + tile_n - 1) / tile_n, tiles = tiles_m * tiles_n;
-  const uint32_t xcd = blockIdx.x % 8, turn = blockIdx.x / 8;
-  const uint32_t tile = xcd * (tiles / 8) + min(xcd, tiles % 8) + turn;
-  const uint32_t group = tile / (kGroup * tiles_n), in_group = tile % (kGroup * tiles_n);
-  const uint32_t group_m = min(kGroup, tiles_m - group * kGroup);
-  const uint32_t i0 = (group * kGroup + in_group % group_m) * TM;
-  const uint32_t j0 = in_group / group_m * tile_n;
+  // Work-groups go round the eight XCDs: XCD x runs one eighth of the tiles,
+  // consecutive ones, its work-groups taking every (gridDim / 8)th.
+  constexpr uint32_t tile_n = F == kGated ? TN / 2 : TN;
+  const TileOrder order = {(a.m + TM - 1) / TM, (a.n + tile_n - 1) / tile_n};
+  const uint32_t tiles = order.tiles_m * order.tiles_n;
+  const uint32_t xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+  const uint32_t end = (tiles / 8) * (xcd + 1) + min(xcd + 1, tiles % 8);
+  uint32_t tile = (tiles / 8) * xcd + min(xcd, tiles % 8) + blockIdx.x / 8;
+  if (tile >= end) return;
 
-  // Addresses: a uniform base, a lane's offset of 32 bits, and k in a scalar.
-  __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<int8_t*>(a.a + static_cast<uint64_t>(i0) * a.a_stride), 0, 0x7FFFFFFF, 0x00020000);
-  __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, 0x7FFFFFFF, 0x00020000);
-  uint32_t off_a[P::kLoadsA], off_b[P::kLoadsB];
+  // The loads' cursor: a tile, a stage in it, and its lanes' offsets. A
+  // ragged end of k (k % 128) makes the first two stages.
   const uint32_t row16 = lane / kChunks;
-  const uint32_t chunk = (lane % kChunks ^ row16 / 4 % kChunks) * 16;
-#pragma unroll
-  for (int t = 0; t < P::kLoadsA; ++t) {
+  const uint32_t swizzle = 0x78u >> (lane / 16 % 4 * 2) & 3;  // of row16 / 4: 0, 2, 3, 1
+  const uint32_t chunk = (lane % kChunks ^ swizzle) * 16;
+  const uint32_t tail = a.k % (2 * kStep), lead = tail != 0 ? 2 : 0;
+  const uint32_t stages = (a.k + 2 * kStep - 1) / (2 * kStep) * 2;
+  __amdgpu_buffer_rsrc_t ra, rb;
+  uint32_t off_a[P::kLoadsA], off_b[P::kLoadsB];
+  uint32_t load_tile = tile, load_stage = 0, load_slot = 0, load_k = 0, load_chunk = 0;
+  auto aim_tile = [&]() {
+    uint32_t tm, tn;
+    order.at(load_tile, &tm, &tn);
+    const uint32_t i0 = tm * TM, j0 = tn * tile_n;
+    ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.a + static_cast<uint64_t>(i0) * a.a_stride), 0, kFar,
+                                           0x00020000);
+    rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar,
+                                           0x00020000);
     // Rows past the end load the last row; what they give is not stored.
-    const uint32_t r = (wave * P::kLoadsA + t) * 16 + row16;
-    off_a[t] = (min(i0 + r, a.m - 1) - i0) * static_cast<uint32_t>(a.a_stride);
-  }
-  const uint32_t up_rows = a.n;  // gated: where the up channels start
 #pragma unroll
-  for (int t = 0; t < P::kLoadsB; ++t) {
-    const uint32_t r = (wave * P::kLoadsB + t) * 16 + row16;
-    uint32_t j = r;
-    if (a.gated) j = r / WTN * (WTN / 2) + r % (WTN / 2);  // a wave's rows: WTN / 2 gates, then their ups
-    j = min(j0 + j, a.n - 1) - j0;
-    if (a.gated && r % WTN >= WTN / 2) j += up_rows;
-    off_b[t] = j * static_cast<uint32_t>(a.b_stride);
-  }
-
-  auto load_stage = [&](uint32_t slot, uint32_t k, uint32_t in_row) {
-    const uint32_t k0 = __builtin_amdgcn_readfirstlane(k);
-    char* base = lds + slot * P::kStageBytes;
-#pragma unroll
-    for (int t = 0; t < P::kLoadsA; ++t)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(base + (wave * P::kLoadsA + t) * 1024), 16,
-                                               off_a[t] + in_row, k0, 0, 0);
-#pragma unroll
-    for (int t = 0; t < P::kLoadsB; ++t)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(base + TM * kStep + (wave * P::kLoadsB + t) * 1024), 16,
-                                               off_b[t] + in_row, k0, 0, 0);
-  };
-
-  // A ragged end of k is the first stage: its chunks past the end load the
-  // row's first chunk instead, and a's are then cleared in LDS, which is
-  // enough for the products to be zero.
-  const uint32_t tail = a.k % kStep;
-  const uint32_t first_full = tail != 0 ? 1 : 0;
-  const uint32_t stages = a.k / kStep + first_full;
-  auto load = [&](uint32_t st) { load_stage(st % S, (st - first_full) * kStep, chunk); };
-
-  i32x16 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
-
-  for (uint32_t t = threadIdx.x; t < TM; t += P::kThreads) token_scale[t] = a.a_scales[min(i0 + t, a.m - 1)];
-  if (tail != 0) load_stage(0, a.k - tail, chunk < tail ? chunk : 0);
-#pragma unroll
-  for (uint32_t st = 0; st < S; ++st)
-    if (st >= first_full && st < stages) load(st);
-
-  if (tail != 0) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (chunk >= tail) {
-#pragma unroll
-      for (int t = 0; t < P::kLoadsA; ++t)
-        *reinterpret_cast<u32x4*>(lds + (wave * P::kLoadsA + t) * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+    for (int t = 0; t < P::kLoadsA; ++t) {
+      const uint32_t r = (wave * P::kLoadsA + t) * 16 + row16;
+      off_a[t] = (min(i0 + r, a.m - 1) - i0) * static_cast<uint32_t>(a.a_stride);
     }
-    wait_loads_and_sync<0>();
-  } else if (stages >= S) {
-    wait_loads_and_sync<P::kLoads * (S - 1)>();
-  } else {
-    wait_loads_and_sync<0>();
-  }
-
-  // Lane l reads row l % 32 of a fragment, chunk l / 32 of the half's two.
-  const uint32_t swz = lane / 4 % kChunks;
-  const uint32_t lane_off[2] = {lane % 32 * kStep + ((lane / 32) ^ swz) * 16, lane % 32 * kStep + ((2 + lane / 32) ^ swz) * 16};
-  const char* base_a = lds + wm * WTM * kStep;
-  const char* base_b = lds + TM * kStep + wn * WTN * kStep;
-  i32x4 fa[2][FM], fb[2][FN];
-  auto read_half = [&](uint32_t slot, int half) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fa[half][i] = *reinterpret_cast<const i32x4*>(base_a + slot * P::kStageBytes + i * 32 * kStep + lane_off[half]);
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-      fb[half][j] = *reinterpret_cast<const i32x4*>(base_b + slot * P::kStageBytes + j * 32 * kStep + lane_off[half]);
+    for (int t = 0; t < P::kLoadsB; ++t) {
+      const uint32_t r = (wave * P::kLoadsB + t) * 16 + row16;
+      uint32_t j = r;
+      if constexpr (F == kGated) j = r / kWaveN * (kWaveN / 2) + r % (kWaveN / 2);  // a wave's gates, then its ups
+      j = min(j0 + j, a.n - 1) - j0;
+      if (F == kGated && r % kWaveN >= kWaveN / 2) j += a.n;
+      off_b[t] = j * static_cast<uint32_t>(a.b_stride);
+    }
   };
-  auto multiply = [&](int half) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[half][j], fa[half][i], acc[i][j], 0, 0, 0);
+  auto aim_stage = [&]() {  // no branch: this runs inside the pipeline
+    const bool ragged = load_stage < lead;
+    const uint32_t k0 = load_stage * kStep + (ragged ? a.k - tail : -lead * kStep);
+    const uint32_t left = tail > load_stage * kStep ? tail - load_stage * kStep : 0;
+    const uint32_t limit = load_tile >= end ? 0 : ragged ? left : kStep;
+    load_k = __builtin_amdgcn_readfirstlane(k0);
+    load_chunk = chunk < limit ? chunk : kFar;
   };
-
-  read_half(0, 0);
-  uint32_t st = 0;
-  for (; st + S < stages; ++st) {
-    read_half(st % S, 1);
-    multiply(0);
-    spread<FM + FN, 0>();
-    wait_loads_and_sync<P::kLoads * (S - 2)>();
-    read_half((st + 1) % S, 0);
-    load(st + S);
-    multiply(1);
-    spread<FM + FN, P::kLoads>();
-  }
-  for (; st + 1 < stages; ++st) {
-    read_half(st % S, 1);
-    multiply(0);
-    wait_loads_and_sync<0>();
-    read_half((st + 1) % S, 0);
-    multiply(1);
-  }
-  read_half(st % S, 1);
-  multiply(0);
-  multiply(1);
-
-  // Epilogue: a wave's 32 tokens at a time through its own part of LDS.
-  __syncthreads();
-  int32_t* sums = reinterpret_cast<int32_t*>(lds) + wave * 32 * P::kSumPitch;
-  const uint32_t out_n = a.gated ? WTN / 2 : WTN;  // output channels of a wave
-  const uint32_t pieces = out_n / kPiece;
-  const uint32_t jj = lane % pieces * kPiece, j = j0 + wn * out_n + jj;
-  const PieceScales scales = piece_scales(a, j);
+  auto advance = [&]() {
+    load_slot = (load_slot + 1) % S;
+    ++load_stage;
+    aim_stage();
+  };
+  auto next_tile = [&]() {
+    load_slot = (load_slot + 1) % S;
+    load_stage = 0;
+    load_tile += stride;
+    if (load_tile < end) aim_tile();
+    aim_stage();
+  };
+  // Loads [first, first + n) of the cursor's stage.
+  auto load = [&](int first, int n) {
+    char* base = lds + load_slot * P::kStageBytes;
 #pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    // Lane l holds token l % 32, channels 8 q + 4 (l / 32) .. + 3.
-#pragma unroll
-    for (int g = 0; g < FN; ++g)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<i32x4*>(sums + lane % 32 * P::kSumPitch + 32 * g + 8 * q + lane / 32 * 4) =
-            i32x4{acc[f][g][4 * q], acc[f][g][4 * q + 1], acc[f][g][4 * q + 2], acc[f][g][4 * q + 3]};
-    for (uint32_t t = lane / pieces; t < 32; t += 64 / pieces) {
-      const uint32_t i = i0 + wm * WTM + 32 * f + t;
-      const int32_t* p = sums + t * P::kSumPitch + jj;
-      int32_t v[kPiece], u[kPiece];
-#pragma unroll
-      for (int e = 0; e < kPiece; ++e) v[e] = p[e];
-      if (a.gated) {
-#pragma unroll
-        for (int e = 0; e < kPiece; ++e) u[e] = p[WTN / 2 + e];
+    for (int t = first; t < first + n; ++t) {
+      if (t < P::kLoadsA) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(base + (wave * P::kLoadsA + t) * 1024), 16,
+                                                 off_a[t] + load_chunk, load_k, 0, 0);
+      } else {
+        const int u = t - P::kLoadsA;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(base + TM * kStep + (wave * P::kLoadsB + u) * 1024), 16,
+                                                 off_b[u] + load_chunk, load_k, 0, 0);
       }
-      finish_piece(a, i, j, i < a.m && j < a.n, token_scale[wm * WTM + 32 * f + t], scales, v, u);
+    }
+  };
+
+  constexpr int kQuarter = P::kLoads / 4;
+  aim_tile();
+  aim_stage();
+#pragma unroll
+  for (int st = 0; st < S - 1; ++st) {
+    load(0, P::kLoads);
+    advance();
+  }
+  load(0, 2 * kQuarter);
+
+  // Lane l reads chunk l / 16 of row l % 16 of a fragment.
+  const uint32_t lane_off = lane % 16 * kStep + ((lane / 16) ^ (0x78u >> (lane % 16 / 4 * 2) & 3)) * 16;
+  const char* base_a = lds + wm * WTM * kStep + lane_off;
+  const char* base_b = lds + TM * kStep + wn * kWaveN * kStep + lane_off;
+  i32x4 acc[FM][FN], fa[FM], fb[FN];
+  uint32_t slot = 0;
+  auto read_a = [&](uint32_t from, int i) {
+    fa[i] = *reinterpret_cast<const i32x4*>(base_a + from * P::kStageBytes + i * 16 * kStep);
+  };
+  auto read_b = [&](uint32_t from, int j) {
+    fb[j] = *reinterpret_cast<const i32x4*>(base_b + from * P::kStageBytes + j * 16 * kStep);
+  };
+  // Products of a's half ha and b's half hb, each with at most one other
+  // instruction behind it: first the reads of the quarter after, then loads
+  // kQuarter * part and on of the cursor's stage, spread over the rest. In
+  // this order, so that the matrix unit never waits for a row of others.
+  auto quarter = [&](int ha, int hb, bool reads_a, uint32_t from, int half, int part) {
+    const int reads = reads_a ? HM : HN;
+    constexpr int kProducts = HM * HN, kOthers = (HM > HN ? HM : HN) + kQuarter;
+    const int each = kProducts > reads + kQuarter ? (kProducts - reads) / kQuarter : 1;
+#pragma unroll
+    for (int x = 0; x < (kProducts > kOthers ? kProducts : kOthers); ++x) {
+      if (x < kProducts) {
+        const int i = ha * HM + x / HN, j = hb * HN + x % HN;
+        mfma(acc[i][j], fb[j], fa[i]);
+      }
+      if (x < reads) {
+        if (reads_a)
+          read_a(from, half * HM + x);
+        else
+          read_b(from, half * HN + x);
+      } else if ((x - reads) % each == 0 && (x - reads) / each < kQuarter) {
+        load(part * kQuarter + (x - reads) / each, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // b's half `first` is in registers when the stage begins. `last_load`: the
+  // cursor's stage is its tile's last.
+  auto stage = [&](int first, bool last_load) {
+    const uint32_t next = (slot + 1) % S;
+    quarter(0, first, false, slot, 1 - first, 2);
+    quarter(0, 1 - first, true, slot, 1, 3);
+    if (last_load)
+      next_tile();
+    else
+      advance();
+    wait_loads_and_sync<P::kLoads * (S - 2)>();
+    quarter(1, 1 - first, true, next, 0, 0);
+    quarter(1, first, false, next, 1 - first, 1);
+    slot = next;
+  };
+
+  wait_loads_and_sync<P::kLoads * (S - 2) + 2 * kQuarter>();
+#pragma unroll
+  for (int i = 0; i < HM; ++i) read_a(0, i);
+#pragma unroll
+  for (int j = 0; j < HN; ++j) read_b(0, j);
+  auto clear = [&](int i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    settle(acc[i]);
+  };
+#pragma unroll
+  for (int i = 0; i < FM; ++i) clear(i);
+  constexpr uint32_t out_n = F == kGated ? kWaveN / 2 : kWaveN;  // output channels of a wave
+  constexpr uint32_t pieces = out_n / kPiece;
+  float* sums = reinterpret_cast<float*>(lds + S * P::kStageBytes + wave * P::kSumsBytes);
+  for (; tile < end; tile += stride) {
+    uint32_t tm, tn;
+    order.at(tile, &tm, &tn);
+    const uint32_t i0 = tm * TM + wm * WTM;
+    const uint32_t j = tn * tile_n + wn * out_n + lane % pieces * kPiece;
+    float sa[FM];  // of token l % 16 of each fragment
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = a.a_scales[min(i0 + 16 * i + lane % 16, a.m - 1)];
+    const PieceScales sb = piece_scales<F>(a, j);
+    // From the middle of stage st on, the loads are at stage st + S.
+    for (uint32_t st = S; st < stages; st += 2) {
+      stage(0, false);
+      stage(1, false);
+    }
+    stage(0, true);
+    stage(1, false);
+#pragma unroll
+    for (int st = 2; st < S; st += 2) {
+      stage(0, false);
+      stage(1, false);
+    }
+    // 16 tokens at a time through the wave's own part of LDS, as binary32
+    // times the token's scale; 16-byte units of a token's row are xored with
+    // the token, which keeps writes of one column off one bank.
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      __builtin_amdgcn_sched_barrier(0);  // one fragment's values in registers at a time
+      settle(acc[i]);
+#pragma unroll
+      for (int g = 0; g < FN; ++g) {
+        // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16.
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][g][e]) * sa[i];
+        *reinterpret_cast<f32x4*>(sums + lane % 16 * kWaveN + ((4 * g + lane / 16) ^ (lane % 16)) * 4) = v;
+      }
+      clear(i);
+#pragma unroll
+      for (uint32_t t0 = 0; t0 < 16; t0 += 64 / pieces) {
+        const uint32_t t = t0 + lane / pieces, u = lane % pieces * 2;
+        const f32x4* row = reinterpret_cast<const f32x4*>(sums + t * kWaveN);
+        float v[kPiece], up[kPiece];
+        *reinterpret_cast<f32x4*>(v) = row[u ^ t];
+        *reinterpret_cast<f32x4*>(v + 4) = row[(u + 1) ^ t];
+        if constexpr (F == kGated) {
+          *reinterpret_cast<f32x4*>(up) = row[(u + 2 * pieces) ^ t];
+          *reinterpret_cast<f32x4*>(up + 4) = row[(u + 2 * pieces + 1) ^ t];
+        }
+        const uint32_t token = i0 + 16 * i + t;
+        finish_piece<F>(a, token, j, token < a.m && j < a.n, sb, v, up);
+      }
     }
   }
+  // Nothing is in flight to this work-group's LDS when it ends.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #endif
 }
 
-template <int TM, int TN, int WTM, int WTN, int S>
+constexpr uint32_t kCus = 256;
+
+template <int TM, int TN, int WTM, int S, int F>
 hipError_t launch_pipe(const MatmulLaunch& l, hipStream_t stream) {
-  const uint32_t tile_n = l.gated ? TN / 2 : TN;
-  const uint32_t tiles = ((l.m + TM - 1) / TM) * ((l.n + tile_n - 1) / tile_n);
-  return launch_kernel(pipe_kernel<TM, TN, WTM, WTN, S>, dim3(tiles), dim3(Pipe<TM, TN, WTM, WTN, S>::kThreads), stream, l);
+  using P = Pipe<TM, TN, WTM, S>;
+  return launch_kernel(pipe_kernel<TM, TN, WTM, S, F>, dim3(kCus * P::kPerCu), dim3(P::kThreads), stream, l);
+}
+
+template <int F>
+hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
+  if (!l.vec) return launch_tiles<false, F>(l, stream);
+  // The pipelined kernel's offsets within a tile are below kFar.
+  const bool near = (256 + (F == kGated ? static_cast<uint64_t>(l.n) : 0)) * l.b_stride + l.k < kFar &&
+                    256 * l.a_stride + l.k < kFar;
+  if (!near || l.m <= 64 || l.k <= 2 * kStep) return launch_tiles<true, F>(l, stream);
+  return launch_pipe<256, 256, 128, 4, F>(l, stream);
 }
 
 }  // namespace
@@ -436,11 +565,8 @@ hipError_t launch_pipe(const MatmulLaunch& l, hipStream_t stream) {
 uint64_t matmul_workspace_bytes(uint32_t, uint32_t, uint32_t, bool) { return 0; }
 
 hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream) {
-  if (!l.vec) return launch_tiles<false>(l, stream);
-  // The pipelined kernel's offsets within a tile are 31 bits.
-  const bool near = l.a_stride < (1u << 22) && (l.b_stride * (static_cast<uint64_t>(l.gated ? l.n : 0) + 512)) < (1u << 31);
-  if (!near || l.m <= 64) return launch_tiles<true>(l, stream);
-  return launch_pipe<256, 256, 128, 128, 4>(l, stream);
+  if (l.quantize) return launch_as<kCodes>(l, stream);
+  return l.gated ? launch_as<kGated>(l, stream) : launch_as<kValues>(l, stream);
 }
 
 }  // namespace qrs

@@ -70,7 +70,7 @@ __device__ __forceinline__ void quantize_row(float (*v)[kPiece], const RowsLaunc
       for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[p][j]));
     amax = block_max<NT>(amax, part);
     float scale;
-    const float mul = f32_multiplier<XF>(amax, &scale);
+    const float mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
 #pragma unroll
     for (int p = 0; p < P; ++p)
       store_codes<VEC>(codes_row, (p * NT + lane) * kPiece, a.h, encode_piece<XF>(v[p], mul));
