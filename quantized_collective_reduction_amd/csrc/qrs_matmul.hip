@@ -542,6 +542,130 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
 #endif
 }
 
+// ---- few tokens --------------------------------------------------------
+
+// Up to 16 * MT tokens: the weights are read once and bound the time, so
+// they go from memory straight into fragment registers, many at a time and
+// without LDS. A work-group of 16 waves takes 32 * GW rows of b (gated: 16
+// gates and 16 ups); its GW groups of KW waves take 32 rows each and share k:
+// wave w of a group takes every KW'th pair of 64-byte steps (a 128-byte line
+// of each row). Their integer sums meet in LDS, where the order of the
+// additions cannot matter.
+template <int MT, int GW, int F>
+__global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) {
+  constexpr int KW = 16 / GW;
+  constexpr int kPairs = MT == 1 ? 4 : MT == 2 ? 2 : 1;  // in flight at a time
+  constexpr uint32_t kRows = 32 * GW, kOut = F == kGated ? kRows / 2 : kRows;
+  constexpr uint32_t kPitch = kRows + 4;
+  __shared__ __attribute__((aligned(16))) int32_t sums[16 * MT * kPitch];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const uint32_t group = wave / KW, kw = wave % KW;
+  const uint32_t j0 = blockIdx.x * kOut;
+
+  // What this thread finishes, and its scales, asked for before all else.
+  constexpr uint32_t pieces = kOut / kPiece;
+  static_assert(16 * MT * pieces <= 1024, "one piece a thread");
+  const uint32_t ti = threadIdx.x / pieces, tj = threadIdx.x % pieces * kPiece;
+  const bool finishes = threadIdx.x < 16 * MT * pieces;
+  PieceScales sb = {};
+  float sa = 0.0f;
+  if (finishes) {
+    sb = piece_scales<F>(a, j0 + tj);
+    sa = a.a_scales[min(ti, a.m - 1)];
+  }
+
+  const int8_t* pb[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t j;
+    if constexpr (F == kGated)
+      j = min(j0 + group * 16 + lane % 16, a.n - 1) + h * a.n;
+    else
+      j = min(j0 + group * 32 + h * 16 + lane % 16, a.n - 1);
+    pb[h] = a.b + j * a.b_stride;
+  }
+  const int8_t* pa[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) pa[i] = a.a + min(16u * i + lane % 16, a.m - 1) * a.a_stride;
+
+  i32x4 acc[MT][2];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) acc[i][h] = i32x4{0, 0, 0, 0};
+  const uint32_t pairs = (a.k + 127) / 128;
+  for (uint32_t p0 = kw; p0 < pairs; p0 += KW * kPairs) {
+    i32x4 fb[2 * kPairs][2], fa[2 * kPairs][MT];
+#pragma unroll
+    for (int q = 0; q < 2 * kPairs; ++q) {
+      const uint32_t k = (p0 + q / 2 * KW) * 128 + q % 2 * 64 + lane / 16 * 16;
+      const bool inside = k < a.k;  // past the end: the row's start, with zeros for a
+      const uint32_t kk = inside ? k : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fb[q][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[h] + kk));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const i32x4 v = *reinterpret_cast<const i32x4*>(pa[i] + kk);
+        fa[q][i] = inside ? v : i32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2 * kPairs; ++q)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[i][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[q][h], fa[q][i], acc[i][h], 0, 0, 0);
+  }
+
+  for (uint32_t t = threadIdx.x; t < 16 * MT * kPitch; t += 1024) sums[t] = 0;
+  __syncthreads();
+  // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16.
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        atomicAdd(&sums[(16 * i + lane % 16) * kPitch + group * 32 + h * 16 + lane / 16 * 4 + e], acc[i][h][e]);
+  __syncthreads();
+  if (!finishes) return;
+  const int32_t* row = sums + ti * kPitch;
+  float v[kPiece], up[kPiece];
+#pragma unroll
+  for (int e = 0; e < kPiece; ++e) {
+    if constexpr (F == kGated) {
+      const int32_t* p = row + tj / 16 * 32 + tj % 16;
+      v[e] = static_cast<float>(p[e]) * sa;
+      up[e] = static_cast<float>(p[16 + e]) * sa;
+    } else {
+      v[e] = static_cast<float>(row[tj + e]) * sa;
+    }
+  }
+  finish_piece<F>(a, ti, j0 + tj, ti < a.m && j0 + tj < a.n, sb, v, up);
+}
+
+template <int MT, int GW, int F>
+hipError_t launch_few(const MatmulLaunch& l, hipStream_t stream) {
+  constexpr uint32_t out = (F == kGated ? 16 : 32) * GW;
+  return launch_kernel(few_tokens_kernel<MT, GW, F>, dim3((l.n + out - 1) / out), dim3(1024), stream, l);
+}
+
+template <int F>
+hipError_t launch_few_sized(const MatmulLaunch& l, hipStream_t stream) {
+  if constexpr (F == kCodes) {
+    // Codes need a whole group in one work-group.
+    if (l.scale_layout == kScaleF32Group128) {
+      if (l.m <= 16) return launch_few<1, 4, F>(l, stream);
+      if (l.m <= 32) return launch_few<2, 4, F>(l, stream);
+      return launch_few<4, 4, F>(l, stream);
+    }
+  }
+  if (l.m <= 16) return launch_few<1, 1, F>(l, stream);
+  if (l.m <= 32) return launch_few<2, 1, F>(l, stream);
+  return launch_few<4, 1, F>(l, stream);
+}
+
 constexpr uint32_t kCus = 256;
 
 template <int TM, int TN, int WTM, int S, int F>
@@ -556,7 +680,8 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   // The pipelined kernel's offsets within a tile are below kFar.
   const bool near = (256 + (F == kGated ? static_cast<uint64_t>(l.n) : 0)) * l.b_stride + l.k < kFar &&
                     256 * l.a_stride + l.k < kFar;
-  if (!near || l.m <= 64 || l.k <= 2 * kStep) return launch_tiles<true, F>(l, stream);
+  if (l.m <= 64) return launch_few_sized<F>(l, stream);
+  if (!near || l.k <= 2 * kStep) return launch_tiles<true, F>(l, stream);
   return launch_pipe<256, 256, 128, 4, F>(l, stream);
 }
 
