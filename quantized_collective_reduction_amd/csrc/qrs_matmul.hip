@@ -545,72 +545,72 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
 // ---- few tokens --------------------------------------------------------
 
 // Up to 16 * MT tokens: the weights are read once and bound the time, so
-// they go from memory straight into fragment registers, many at a time and
-// without LDS. A work-group of 16 waves takes 32 * GW rows of b (gated: 16
-// gates and 16 ups); its GW groups of KW waves take 32 rows each and share k:
-// wave w of a group takes every KW'th pair of 64-byte steps (a 128-byte line
-// of each row). Their integer sums meet in LDS, where the order of the
-// additions cannot matter.
+// they go from memory straight into fragment registers, without LDS. A
+// work-group of 16 waves takes 32 * GW rows of b (gated: 16 gates and 16
+// ups); its GW groups of KW waves take 32 rows each and share k: wave w of a
+// group takes every KW'th pair of 64-byte steps (a 128-byte line of each
+// row), kPairs of them in flight at a time. Their integer sums meet in LDS,
+// where the order of the additions cannot matter.
 template <int MT, int GW, int F>
 __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) {
+#ifdef __HIP_DEVICE_COMPILE__
   constexpr int KW = 16 / GW;
-  constexpr int kPairs = MT == 1 ? 4 : MT == 2 ? 2 : 1;  // in flight at a time
+  constexpr int kPairs = MT == 1 ? 4 : MT == 2 ? 2 : 1, kUnits = 2 * kPairs;
   constexpr uint32_t kRows = 32 * GW, kOut = F == kGated ? kRows / 2 : kRows;
   constexpr uint32_t kPitch = kRows + 4;
   __shared__ __attribute__((aligned(16))) int32_t sums[16 * MT * kPitch];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  __shared__ float row_scale[kRows], token_scale[16 * MT];
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t group = wave / KW, kw = wave % KW;
   const uint32_t j0 = blockIdx.x * kOut;
 
-  // What this thread finishes, and its scales, asked for before all else.
-  constexpr uint32_t pieces = kOut / kPiece;
-  static_assert(16 * MT * pieces <= 1024, "one piece a thread");
-  const uint32_t ti = threadIdx.x / pieces, tj = threadIdx.x % pieces * kPiece;
-  const bool finishes = threadIdx.x < 16 * MT * pieces;
-  PieceScales sb = {};
-  float sa = 0.0f;
-  if (finishes) {
-    sb = piece_scales<F>(a, j0 + tj);
-    sa = a.a_scales[min(ti, a.m - 1)];
-  }
-
-  const int8_t* pb[2];
+  // Row r of the work-group's part of b: in the gated form 16 gates, then
+  // their ups.
+  auto row_of = [&](uint32_t r) {
+    if constexpr (F == kGated) return min(j0 + r / 32 * 16 + r % 16, a.n - 1) + (r % 32 >= 16 ? a.n : 0);
+    return min(j0 + r, a.n - 1);
+  };
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.a), 0, kFar, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar, 0x00020000);
+  const uint32_t chunk = lane / 16 * 16;
+  uint32_t off_b[2], off_a[MT];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t j;
-    if constexpr (F == kGated)
-      j = min(j0 + group * 16 + lane % 16, a.n - 1) + h * a.n;
-    else
-      j = min(j0 + group * 32 + h * 16 + lane % 16, a.n - 1);
-    pb[h] = a.b + j * a.b_stride;
-  }
-  const int8_t* pa[MT];
+  for (int h = 0; h < 2; ++h)
+    off_b[h] = (row_of(group * 32 + h * 16 + lane % 16) - j0) * static_cast<uint32_t>(a.b_stride) + chunk;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) pa[i] = a.a + min(16u * i + lane % 16, a.m - 1) * a.a_stride;
+  for (int i = 0; i < MT; ++i)
+    off_a[i] = min(16u * i + lane % 16, a.m - 1) * static_cast<uint32_t>(a.a_stride) + chunk;
 
   i32x4 acc[MT][2];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) acc[i][h] = i32x4{0, 0, 0, 0};
+  // One of the work-group's scales a thread: of its rows of b, then of the tokens.
+  const bool has_scale = threadIdx.x < kRows + 16 * MT;
+  const float* scale_at = threadIdx.x < kRows ? a.b_scales + row_of(threadIdx.x)
+                                              : a.a_scales + min(threadIdx.x - kRows, a.m - 1);
+  float scale = 0.0f;
   const uint32_t pairs = (a.k + 127) / 128;
   for (uint32_t p0 = kw; p0 < pairs; p0 += KW * kPairs) {
-    i32x4 fb[2 * kPairs][2], fa[2 * kPairs][MT];
+    i32x4 fb[kUnits][2], fa[kUnits][MT];
 #pragma unroll
-    for (int q = 0; q < 2 * kPairs; ++q) {
-      const uint32_t k = (p0 + q / 2 * KW) * 128 + q % 2 * 64 + lane / 16 * 16;
-      const bool inside = k < a.k;  // past the end: the row's start, with zeros for a
-      const uint32_t kk = inside ? k : 0;
+    for (int q = 0; q < kUnits; ++q) {
+      const uint32_t k = (p0 + q / 2 * KW) * 128 + q % 2 * 64;
+      const uint32_t far = k + chunk < a.k ? 0 : kFar;  // past the end of k: zeros
 #pragma unroll
-      for (int h = 0; h < 2; ++h) fb[q][h] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[h] + kk));
+      for (int h = 0; h < 2; ++h)
+        fb[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b[h] + far, k, 2);  // 2: streamed, not kept
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const i32x4 v = *reinterpret_cast<const i32x4*>(pa[i] + kk);
-        fa[q][i] = inside ? v : i32x4{0, 0, 0, 0};
-      }
+      for (int i = 0; i < MT; ++i) fa[q][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, off_a[i] + far, k, 0);
     }
+    if (p0 == kw && has_scale) scale = *scale_at;  // behind the first operands, which do not wait for it
+    __builtin_amdgcn_sched_barrier(0);  // all loads, then the products
 #pragma unroll
-    for (int q = 0; q < 2 * kPairs; ++q)
+    for (int q = 0; q < kUnits; ++q)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -619,6 +619,11 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
   }
 
   for (uint32_t t = threadIdx.x; t < 16 * MT * kPitch; t += 1024) sums[t] = 0;
+  if (kw >= pairs && has_scale) scale = *scale_at;  // a wave without a step
+  if (threadIdx.x < kRows)
+    row_scale[threadIdx.x] = scale;
+  else if (threadIdx.x < kRows + 16 * MT)
+    token_scale[threadIdx.x - kRows] = scale;
   __syncthreads();
   // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16.
 #pragma unroll
@@ -629,20 +634,25 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
       for (int e = 0; e < 4; ++e)
         atomicAdd(&sums[(16 * i + lane % 16) * kPitch + group * 32 + h * 16 + lane / 16 * 4 + e], acc[i][h][e]);
   __syncthreads();
-  if (!finishes) return;
-  const int32_t* row = sums + ti * kPitch;
+  constexpr uint32_t pieces = kOut / kPiece;
+  static_assert(16 * MT * pieces <= 1024, "one piece a thread");
+  if (threadIdx.x >= 16 * MT * pieces) return;
+  const uint32_t i = threadIdx.x / pieces, jj = threadIdx.x % pieces * kPiece;
+  const uint32_t r = F == kGated ? jj / 16 * 32 + jj % 16 : jj;
+  const int32_t* row = sums + i * kPitch + r;
   float v[kPiece], up[kPiece];
+  PieceScales sb;
 #pragma unroll
   for (int e = 0; e < kPiece; ++e) {
+    v[e] = static_cast<float>(row[e]) * token_scale[i];
+    sb.b[e] = row_scale[r + e];
     if constexpr (F == kGated) {
-      const int32_t* p = row + tj / 16 * 32 + tj % 16;
-      v[e] = static_cast<float>(p[e]) * sa;
-      up[e] = static_cast<float>(p[16 + e]) * sa;
-    } else {
-      v[e] = static_cast<float>(row[tj + e]) * sa;
+      up[e] = static_cast<float>(row[16 + e]) * token_scale[i];
+      sb.up[e] = row_scale[r + 16 + e];
     }
   }
-  finish_piece<F>(a, ti, j0 + tj, ti < a.m && j0 + tj < a.n, sb, v, up);
+  finish_piece<F>(a, i, j0 + jj, i < a.m && j0 + jj < a.n, sb, v, up);
+#endif
 }
 
 template <int MT, int GW, int F>
@@ -680,7 +690,7 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   // The pipelined kernel's offsets within a tile are below kFar.
   const bool near = (256 + (F == kGated ? static_cast<uint64_t>(l.n) : 0)) * l.b_stride + l.k < kFar &&
                     256 * l.a_stride + l.k < kFar;
-  if (l.m <= 64) return launch_few_sized<F>(l, stream);
+  if (near && l.m <= 64) return launch_few_sized<F>(l, stream);
   if (!near || l.k <= 2 * kStep) return launch_tiles<true, F>(l, stream);
   return launch_pipe<256, 256, 128, 4, F>(l, stream);
 }
