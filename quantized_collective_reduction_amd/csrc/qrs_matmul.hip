@@ -545,21 +545,30 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
 // ---- few tokens --------------------------------------------------------
 
 // Up to 16 * MT tokens: the weights are read once and bound the time, so
-// they go from memory straight into fragment registers, without LDS. A
-// work-group of 16 waves takes 32 * GW rows of b (gated: 16 gates and 16
-// ups); its GW groups of KW waves take 32 rows each and share k: wave w of a
-// group takes every KW'th pair of 64-byte steps (a 128-byte line of each
-// row), kPairs of them in flight at a time. Their integer sums meet in LDS,
-// where the order of the additions cannot matter.
+// many loads are in flight at once, straight into registers. A work-group of
+// 16 waves takes 32 * GW rows of b (gated: 16 gates and 16 ups); its GW groups
+// of KW waves take 32 rows each and share k: wave w of a group takes every
+// KW'th 128 bytes of its rows (a line of each), kPairs of them in flight.
+//
+// Eight neighbouring lanes load the line of a row. Fragments want one row a
+// lane, but loads of that shape cost an access to the first cache for every
+// lane (16 bytes a cycle: 12.5 us for one token by 1024 x 8192), so a wave
+// turns its lines round in its own part of LDS; chunk c of row r lies in slot
+// c ^ (r / 2 % 8), which keeps the reads off each other's banks.
+//
+// The waves' integer sums meet in LDS, where the order of the additions
+// cannot matter.
 template <int MT, int GW, int F>
 __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int KW = 16 / GW;
-  constexpr int kPairs = MT == 1 ? 4 : MT == 2 ? 2 : 1, kUnits = 2 * kPairs;
+  constexpr int kPairs = MT == 1 ? 4 : 2;
   constexpr uint32_t kRows = 32 * GW, kOut = F == kGated ? kRows / 2 : kRows;
   constexpr uint32_t kPitch = kRows + 4;
   __shared__ __attribute__((aligned(16))) int32_t sums[16 * MT * kPitch];
   __shared__ float row_scale[kRows], token_scale[16 * MT];
+  constexpr int kWaveRows = 32 + 16 * MT;  // of b, then the tokens
+  __shared__ __attribute__((aligned(128))) char turn[16 * kWaveRows * 128];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t group = wave / KW, kw = wave % KW;
@@ -575,14 +584,18 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
       __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.a), 0, kFar, 0x00020000);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar, 0x00020000);
-  const uint32_t chunk = lane / 16 * 16;
-  uint32_t off_b[2], off_a[MT];
+  // Load t of a line covers rows 8 t .. 8 t + 7; tokens past the last are zeros.
+  const uint32_t chunk = lane % 8 * 16;
+  uint32_t off_b[4], off_a[2 * MT];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    off_b[h] = (row_of(group * 32 + h * 16 + lane % 16) - j0) * static_cast<uint32_t>(a.b_stride) + chunk;
+  for (int t = 0; t < 4; ++t)
+    off_b[t] = (row_of(group * 32 + 8 * t + lane / 8) - j0) * static_cast<uint32_t>(a.b_stride) + chunk;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    off_a[i] = min(16u * i + lane % 16, a.m - 1) * static_cast<uint32_t>(a.a_stride) + chunk;
+  for (int t = 0; t < 2 * MT; ++t) {
+    const uint32_t i = 8 * t + lane / 8;
+    off_a[t] = i < a.m ? i * static_cast<uint32_t>(a.a_stride) + chunk : kFar;
+  }
+  char* mine = turn + wave * kWaveRows * 128;
 
   i32x4 acc[MT][2];
 #pragma unroll
@@ -596,26 +609,44 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
   float scale = 0.0f;
   const uint32_t pairs = (a.k + 127) / 128;
   for (uint32_t p0 = kw; p0 < pairs; p0 += KW * kPairs) {
-    i32x4 fb[kUnits][2], fa[kUnits][MT];
+    i32x4 lb[kPairs][4], la[kPairs][2 * MT];
 #pragma unroll
-    for (int q = 0; q < kUnits; ++q) {
-      const uint32_t k = (p0 + q / 2 * KW) * 128 + q % 2 * 64;
+    for (int q = 0; q < kPairs; ++q) {
+      const uint32_t k = (p0 + q * KW) * 128;
       const uint32_t far = k + chunk < a.k ? 0 : kFar;  // past the end of k: zeros
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        fb[q][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b[h] + far, k, 2);  // 2: streamed, not kept
+      for (int t = 0; t < 4; ++t)
+        lb[q][t] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b[t] + far, k, 2);  // 2: streamed, not kept
 #pragma unroll
-      for (int i = 0; i < MT; ++i) fa[q][i] = __builtin_amdgcn_raw_buffer_load_b128(ra, off_a[i] + far, k, 0);
+      for (int t = 0; t < 2 * MT; ++t) la[q][t] = __builtin_amdgcn_raw_buffer_load_b128(ra, off_a[t] | far, k, 0);
     }
     if (p0 == kw && has_scale) scale = *scale_at;  // behind the first operands, which do not wait for it
     __builtin_amdgcn_sched_barrier(0);  // all loads, then the products
 #pragma unroll
-    for (int q = 0; q < kUnits; ++q)
+    for (int q = 0; q < kPairs; ++q) {
+      auto put = [&](int t, const i32x4& v) {  // rows 8 t .. 8 t + 7 of the wave's
+        const uint32_t slot = lane % 8 ^ (t % 2 * 4 + lane / 16);
+        *reinterpret_cast<i32x4*>(mine + (8 * t + lane / 8) * 128 + slot * 16) = v;
+      };
+      auto fragment = [&](int f, int unit) {  // rows 16 f .. 16 f + 15, chunks 4 unit ..
+        const uint32_t slot = (4 * unit + lane / 16) ^ (lane % 16 / 2);
+        return *reinterpret_cast<const i32x4*>(mine + (16 * f + lane % 16) * 128 + slot * 16);
+      };
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int t = 0; t < 4; ++t) put(t, lb[q][t]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          acc[i][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[q][h], fa[q][i], acc[i][h], 0, 0, 0);
+      for (int t = 0; t < 2 * MT; ++t) put(4 + t, la[q][t]);
+#pragma unroll
+      for (int unit = 0; unit < 2; ++unit) {
+        const i32x4 fb[2] = {fragment(0, unit), fragment(1, unit)};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const i32x4 fa = fragment(2 + i, unit);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) acc[i][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h], fa, acc[i][h], 0, 0, 0);
+        }
+      }
+    }
   }
 
   for (uint32_t t = threadIdx.x; t < 16 * MT * kPitch; t += 1024) sums[t] = 0;
@@ -667,13 +698,11 @@ hipError_t launch_few_sized(const MatmulLaunch& l, hipStream_t stream) {
     // Codes need a whole group in one work-group.
     if (l.scale_layout == kScaleF32Group128) {
       if (l.m <= 16) return launch_few<1, 4, F>(l, stream);
-      if (l.m <= 32) return launch_few<2, 4, F>(l, stream);
-      return launch_few<4, 4, F>(l, stream);
+      return launch_few<2, 4, F>(l, stream);
     }
   }
   if (l.m <= 16) return launch_few<1, 1, F>(l, stream);
-  if (l.m <= 32) return launch_few<2, 1, F>(l, stream);
-  return launch_few<4, 1, F>(l, stream);
+  return launch_few<2, 1, F>(l, stream);
 }
 
 constexpr uint32_t kCus = 256;
@@ -690,7 +719,7 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   // The pipelined kernel's offsets within a tile are below kFar.
   const bool near = (256 + (F == kGated ? static_cast<uint64_t>(l.n) : 0)) * l.b_stride + l.k < kFar &&
                     256 * l.a_stride + l.k < kFar;
-  if (near && l.m <= 64) return launch_few_sized<F>(l, stream);
+  if (near && l.m <= 32) return launch_few_sized<F>(l, stream);
   if (!near || l.k <= 2 * kStep) return launch_tiles<true, F>(l, stream);
   return launch_pipe<256, 256, 128, 4, F>(l, stream);
 }
