@@ -14,6 +14,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "qrs_device.h"
 #include "qrs_layer.h"
@@ -25,6 +26,8 @@ namespace qrs {
 namespace {
 
 using namespace dev;
+
+constexpr uint32_t kCus = 256;
 
 // ---- epilogue ----------------------------------------------------------
 
@@ -546,9 +549,10 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
 
 // Up to 16 * MT tokens: the weights are read once and bound the time, so
 // many loads are in flight at once, straight into registers. A work-group of
-// 16 waves takes 32 * GW rows of b (gated: 16 gates and 16 ups); its GW groups
-// of KW waves take 32 rows each and share k: wave w of a group takes every
-// KW'th 128 bytes of its rows (a line of each), kPairs of them in flight.
+// 16 waves takes RB * GW rows of b (gated: in runs of RB / 2 gates and their
+// ups); its GW groups of KW waves take RB rows each and share k: wave w of a
+// group takes every KW'th 128 bytes of its rows (a line of each), kPairs of
+// them in flight.
 //
 // Eight neighbouring lanes load the line of a row. Fragments want one row a
 // lane, but loads of that shape cost an access to the first cache for every
@@ -558,26 +562,24 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
 //
 // The waves' integer sums meet in LDS, where the order of the additions
 // cannot matter.
-template <int MT, int GW, int F>
+template <int MT, int GW, int RB, int F>
 __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) {
 #ifdef __HIP_DEVICE_COMPILE__
   constexpr int KW = 16 / GW;
-  constexpr int kPairs = MT == 1 ? 4 : 2;
-  constexpr uint32_t kRows = 32 * GW, kOut = F == kGated ? kRows / 2 : kRows;
+  constexpr int kPairs = MT == 1 ? 4 : 2, FB = RB / 16, kLinesB = RB / 8;
+  constexpr uint32_t kRows = RB * GW, kOut = F == kGated ? kRows / 2 : kRows;
   constexpr uint32_t kPitch = kRows + 4;
   __shared__ __attribute__((aligned(16))) int32_t sums[16 * MT * kPitch];
   __shared__ float row_scale[kRows], token_scale[16 * MT];
-  constexpr int kWaveRows = 32 + 16 * MT;  // of b, then the tokens
+  constexpr int kWaveRows = RB + 16 * MT;  // of b, then the tokens
   __shared__ __attribute__((aligned(128))) char turn[16 * kWaveRows * 128];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t group = wave / KW, kw = wave % KW;
   const uint32_t j0 = blockIdx.x * kOut;
 
-  // Row r of the work-group's part of b: in the gated form 16 gates, then
-  // their ups.
-  auto row_of = [&](uint32_t r) {
-    if constexpr (F == kGated) return min(j0 + r / 32 * 16 + r % 16, a.n - 1) + (r % 32 >= 16 ? a.n : 0);
+  auto row_of = [&](uint32_t r) {  // of the work-group's part of b
+    if constexpr (F == kGated) return min(j0 + r / RB * (RB / 2) + r % (RB / 2), a.n - 1) + (r % RB >= RB / 2 ? a.n : 0);
     return min(j0 + r, a.n - 1);
   };
   const __amdgpu_buffer_rsrc_t ra =
@@ -586,10 +588,10 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
       const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar, 0x00020000);
   // Load t of a line covers rows 8 t .. 8 t + 7; tokens past the last are zeros.
   const uint32_t chunk = lane % 8 * 16;
-  uint32_t off_b[4], off_a[2 * MT];
+  uint32_t off_b[kLinesB], off_a[2 * MT];
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    off_b[t] = (row_of(group * 32 + 8 * t + lane / 8) - j0) * static_cast<uint32_t>(a.b_stride) + chunk;
+  for (int t = 0; t < kLinesB; ++t)
+    off_b[t] = (row_of(group * RB + 8 * t + lane / 8) - j0) * static_cast<uint32_t>(a.b_stride) + chunk;
 #pragma unroll
   for (int t = 0; t < 2 * MT; ++t) {
     const uint32_t i = 8 * t + lane / 8;
@@ -597,11 +599,11 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
   }
   char* mine = turn + wave * kWaveRows * 128;
 
-  i32x4 acc[MT][2];
+  i32x4 acc[MT][FB];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) acc[i][h] = i32x4{0, 0, 0, 0};
+    for (int h = 0; h < FB; ++h) acc[i][h] = i32x4{0, 0, 0, 0};
   // One of the work-group's scales a thread: of its rows of b, then of the tokens.
   const bool has_scale = threadIdx.x < kRows + 16 * MT;
   const float* scale_at = threadIdx.x < kRows ? a.b_scales + row_of(threadIdx.x)
@@ -609,13 +611,13 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
   float scale = 0.0f;
   const uint32_t pairs = (a.k + 127) / 128;
   for (uint32_t p0 = kw; p0 < pairs; p0 += KW * kPairs) {
-    i32x4 lb[kPairs][4], la[kPairs][2 * MT];
+    i32x4 lb[kPairs][kLinesB], la[kPairs][2 * MT];
 #pragma unroll
     for (int q = 0; q < kPairs; ++q) {
       const uint32_t k = (p0 + q * KW) * 128;
       const uint32_t far = k + chunk < a.k ? 0 : kFar;  // past the end of k: zeros
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < kLinesB; ++t)
         lb[q][t] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b[t] + far, k, 2);  // 2: streamed, not kept
 #pragma unroll
       for (int t = 0; t < 2 * MT; ++t) la[q][t] = __builtin_amdgcn_raw_buffer_load_b128(ra, off_a[t] | far, k, 0);
@@ -633,17 +635,19 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
         return *reinterpret_cast<const i32x4*>(mine + (16 * f + lane % 16) * 128 + slot * 16);
       };
 #pragma unroll
-      for (int t = 0; t < 4; ++t) put(t, lb[q][t]);
+      for (int t = 0; t < kLinesB; ++t) put(t, lb[q][t]);
 #pragma unroll
-      for (int t = 0; t < 2 * MT; ++t) put(4 + t, la[q][t]);
+      for (int t = 0; t < 2 * MT; ++t) put(kLinesB + t, la[q][t]);
 #pragma unroll
       for (int unit = 0; unit < 2; ++unit) {
-        const i32x4 fb[2] = {fragment(0, unit), fragment(1, unit)};
+        i32x4 fb[FB];
+#pragma unroll
+        for (int h = 0; h < FB; ++h) fb[h] = fragment(h, unit);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const i32x4 fa = fragment(2 + i, unit);
+          const i32x4 fa = fragment(FB + i, unit);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) acc[i][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h], fa, acc[i][h], 0, 0, 0);
+          for (int h = 0; h < FB; ++h) acc[i][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h], fa, acc[i][h], 0, 0, 0);
         }
       }
     }
@@ -660,16 +664,16 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < FB; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        atomicAdd(&sums[(16 * i + lane % 16) * kPitch + group * 32 + h * 16 + lane / 16 * 4 + e], acc[i][h][e]);
+        atomicAdd(&sums[(16 * i + lane % 16) * kPitch + group * RB + h * 16 + lane / 16 * 4 + e], acc[i][h][e]);
   __syncthreads();
   constexpr uint32_t pieces = kOut / kPiece;
   static_assert(16 * MT * pieces <= 1024, "one piece a thread");
   if (threadIdx.x >= 16 * MT * pieces) return;
   const uint32_t i = threadIdx.x / pieces, jj = threadIdx.x % pieces * kPiece;
-  const uint32_t r = F == kGated ? jj / 16 * 32 + jj % 16 : jj;
+  const uint32_t r = F == kGated ? jj / (RB / 2) * RB + jj % (RB / 2) : jj;
   const int32_t* row = sums + i * kPitch + r;
   float v[kPiece], up[kPiece];
   PieceScales sb;
@@ -678,34 +682,211 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
     v[e] = static_cast<float>(row[e]) * token_scale[i];
     sb.b[e] = row_scale[r + e];
     if constexpr (F == kGated) {
-      up[e] = static_cast<float>(row[16 + e]) * token_scale[i];
-      sb.up[e] = row_scale[r + 16 + e];
+      up[e] = static_cast<float>(row[RB / 2 + e]) * token_scale[i];
+      sb.up[e] = row_scale[r + RB / 2 + e];
     }
   }
   finish_piece<F>(a, i, j0 + jj, i < a.m && j0 + jj < a.n, sb, v, up);
 #endif
 }
 
-template <int MT, int GW, int F>
+template <int MT, int GW, int RB, int F>
 hipError_t launch_few(const MatmulLaunch& l, hipStream_t stream) {
-  constexpr uint32_t out = (F == kGated ? 16 : 32) * GW;
-  return launch_kernel(few_tokens_kernel<MT, GW, F>, dim3((l.n + out - 1) / out), dim3(1024), stream, l);
+  constexpr uint32_t out = (F == kGated ? RB / 2 : RB) * GW;
+  return launch_kernel(few_tokens_kernel<MT, GW, RB, F>, dim3((l.n + out - 1) / out), dim3(1024), stream, l);
 }
 
-template <int F>
+template <int MT, int F>
 hipError_t launch_few_sized(const MatmulLaunch& l, hipStream_t stream) {
   if constexpr (F == kCodes) {
-    // Codes need a whole group in one work-group.
-    if (l.scale_layout == kScaleF32Group128) {
-      if (l.m <= 16) return launch_few<1, 4, F>(l, stream);
-      return launch_few<2, 4, F>(l, stream);
-    }
+    // Codes need a whole group of 128 or 32 channels in one work-group.
+    if (l.scale_layout == kScaleF32Group128) return launch_few<MT, 4, 32, F>(l, stream);
+    return launch_few<MT, 1, 32, F>(l, stream);
+  } else {
+    // Narrow work-groups where wide ones would leave half of the CUs idle.
+    const uint32_t rows = F == kGated ? 2 * l.n : l.n;
+    return rows <= 16 * kCus ? launch_few<MT, 1, 16, F>(l, stream) : launch_few<MT, 1, 32, F>(l, stream);
   }
-  if (l.m <= 16) return launch_few<1, 1, F>(l, stream);
-  return launch_few<2, 1, F>(l, stream);
 }
 
-constexpr uint32_t kCus = 256;
+// ---- tens to hundreds of tokens ----------------------------------------
+
+// Too few tiles of the pipelined kernel for 256 CUs: TM tokens by TN rows of
+// b a work-group, whose eight waves also share k, so that its sums need no
+// second pass through memory. Wave (g, w) takes 64-byte step g of each
+// stage's KG steps and TN / (8 / KG) rows of b.
+//
+// A stage is KG / 2 blocks of rows of 128 bytes, loaded straight into LDS, 8
+// rows a load, S - 1 stages ahead: what bounds these tiles is the 64 bytes a
+// cycle that a CU takes from L2, so whole lines are asked for and most of
+// LDS holds operands in flight. Slots as in few_tokens_kernel. Two waves a
+// SIMD hide each other's reads; one barrier a stage.
+template <int TM, int TN, int KG, int S>
+struct Mid {
+  static constexpr int kThreads = 512, kWavesN = 8 / KG, WTN = TN / kWavesN;
+  static constexpr int FM = TM / 16, FN = WTN / 16;
+  static constexpr int kRows = TM + TN, kStageK = 64 * KG;
+  static constexpr int kStageBytes = kRows * kStageK;
+  static constexpr int kLoads = kStageBytes / 1024 / 8;  // a wave
+  static constexpr int kPitch = TN + 4;  // words of a token's sums
+  static constexpr int kScales = S * kStageBytes > TM * kPitch * 4 ? S * kStageBytes : TM * kPitch * 4;
+  static constexpr int kLds = kScales + kRows * 4;
+  static_assert(KG % 2 == 0 && kStageBytes % 8192 == 0 && WTN % 16 == 0 && TM % 16 == 0, "whole loads and fragments");
+  static_assert(kRows <= kThreads, "one scale a thread");
+};
+
+template <int TM, int TN, int KG, int S, int F>
+__global__ __launch_bounds__(512, 1) void mid_kernel(const MatmulLaunch a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using P = Mid<TM, TN, KG, S>;
+  constexpr int FM = P::FM, FN = P::FN;
+  // One array: with several, the compiler tells their accesses apart and
+  // waits for every load to LDS before it reads any.
+  __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+  float* scales = reinterpret_cast<float*>(lds + P::kScales);
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int g = wave % KG, wn = wave / KG;
+
+  constexpr uint32_t kOut = F == kGated ? TN / 2 : TN;
+  const TileOrder order = {(a.m + TM - 1) / TM, (a.n + kOut - 1) / kOut};
+  const uint32_t tiles = order.tiles_m * order.tiles_n, xcd = blockIdx.x % 8;
+  uint32_t tm, tn;
+  order.at((tiles / 8) * xcd + min(xcd, tiles % 8) + blockIdx.x / 8, &tm, &tn);
+  const uint32_t i0 = tm * TM, j0 = tn * kOut;
+  // Row r of the tile's part of b: in the gated form every fragment of 16
+  // gates is followed by their ups.
+  auto row_of = [&](uint32_t r) {
+    if constexpr (F == kGated) return min(j0 + r / 32 * 16 + r % 16, a.n - 1) + (r % 32 >= 16 ? a.n : 0);
+    return min(j0 + r, a.n - 1);
+  };
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(a.a + static_cast<uint64_t>(i0) * a.a_stride), 0, kFar, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar, 0x00020000);
+
+  // Load t covers rows 8 (t % (kRows / 8)) .. + 7 of block t / (kRows / 8);
+  // lane l the chunk of row l / 8 whose slot is l % 8.
+  uint32_t offset[P::kLoads], in_k[P::kLoads];
+#pragma unroll
+  for (int t = 0; t < P::kLoads; ++t) {
+    const uint32_t at = wave * P::kLoads + t, r = at % (P::kRows / 8) * 8 + lane / 8;
+    in_k[t] = at / (P::kRows / 8) * 128 + (lane % 8 ^ (r / 2 % 8)) * 16;
+    offset[t] = (r < TM ? (min(i0 + r, a.m - 1) - i0) * static_cast<uint32_t>(a.a_stride)
+                        : (row_of(r - TM) - j0) * static_cast<uint32_t>(a.b_stride)) + in_k[t];
+  }
+  auto load = [&](uint32_t st, int t) {
+    const uint32_t k = __builtin_amdgcn_readfirstlane(st * P::kStageK);
+    const uint32_t at = wave * P::kLoads + t;
+    char* to = lds + st % S * P::kStageBytes + at * 1024;
+    const uint32_t far = k + in_k[t] < a.k ? 0 : kFar;  // past the end of k: zeros
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(at % (P::kRows / 8) * 8 < TM ? ra : rb, (lds_ptr)to, 16, offset[t] + far, k,
+                                             0, 0);
+  };
+
+  float scale = 0.0f;
+  if (threadIdx.x < P::kRows)
+    scale = threadIdx.x < TM ? a.a_scales[min(i0 + threadIdx.x, a.m - 1)] : a.b_scales[row_of(threadIdx.x - TM)];
+  const uint32_t stages = (a.k + P::kStageK - 1) / P::kStageK;
+#pragma unroll
+  for (uint32_t st = 0; st < S; ++st)  // past the last stage: zeros
+#pragma unroll
+    for (int t = 0; t < P::kLoads; ++t) load(st, t);
+
+  i32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const uint32_t slot = ((4 * (g % 2) + lane / 16) ^ (lane % 16 / 2)) * 16;
+  const char* frag = lds + g / 2 * P::kRows * 128 + lane % 16 * 128 + slot;
+  const char* frag_b = frag + (TM + wn * P::WTN) * 128;
+  i32x4 fa[2][FM], fb[2][FN];  // of even and odd stages
+  auto read = [&](int set, uint32_t st, int x) {
+    const uint32_t base = st % S * P::kStageBytes;
+    if (x < FN)
+      fb[set][x] = *reinterpret_cast<const i32x4*>(frag_b + base + x * 16 * 128);
+    else
+      fa[set][x - FN] = *reinterpret_cast<const i32x4*>(frag + base + (x - FN) * 16 * 128);
+  };
+  // Multiplies stage st, in registers, while stage st + 1 is read and stage
+  // st + S loaded into st's place in LDS.
+  auto stage = [&](uint32_t st, int set) {
+    wait_loads_and_sync<P::kLoads * (S - 2)>();
+    constexpr int kProducts = FM * FN, kReads = FM + FN, kOthers = kReads + P::kLoads;
+#pragma unroll
+    for (int x = 0; x < (kProducts > kOthers ? kProducts : kOthers); ++x) {
+      if (x < kProducts) {
+        const int i = x / FN, j = x % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+      }
+      if (x < kReads)
+        read(1 - set, st + 1, x);
+      else if (x < kOthers)
+        load(st + S, x - kReads);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  wait_loads_and_sync<P::kLoads * (S - 1)>();
+#pragma unroll
+  for (int x = 0; x < FM + FN; ++x) read(0, 0, x);
+  // Two stages a round; an odd last one is followed by zeros.
+  for (uint32_t st = 0; st < stages; st += 2) {
+    stage(st, 0);
+    stage(st + 1, 1);
+  }
+
+  // The KG partial sums meet in LDS: one wave of each column writes, the
+  // others add.
+  wait_loads_and_sync<0>();
+  int32_t* sums = reinterpret_cast<int32_t*>(lds);
+  // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16 of a fragment.
+  int32_t* at = sums + lane % 16 * P::kPitch + wn * P::WTN + lane / 16 * 4;
+  if (g == 0) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) *reinterpret_cast<i32x4*>(at + i * 16 * P::kPitch + j * 16) = acc[i][j];
+  }
+  if (threadIdx.x < P::kRows) scales[threadIdx.x] = scale;
+  __syncthreads();
+  if (g != 0) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) atomicAdd(at + i * 16 * P::kPitch + j * 16 + e, acc[i][j][e]);
+  }
+  __syncthreads();
+  constexpr uint32_t pieces = kOut / kPiece;
+  static_assert(TM * pieces % 64 == 0, "whole waves");
+  for (uint32_t t = threadIdx.x; t < TM * pieces; t += P::kThreads) {
+    const uint32_t i = t / pieces, jj = t % pieces * kPiece;
+    const uint32_t r = F == kGated ? jj / 16 * 32 + jj % 16 : jj;
+    const int32_t* row = sums + i * P::kPitch + r;
+    float v[kPiece], up[kPiece];
+    PieceScales sb;
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      v[e] = static_cast<float>(row[e]) * scales[i];
+      sb.b[e] = scales[TM + r + e];
+      if constexpr (F == kGated) {
+        up[e] = static_cast<float>(row[16 + e]) * scales[i];
+        sb.up[e] = scales[TM + r + 16 + e];
+      }
+    }
+    finish_piece<F>(a, i0 + i, j0 + jj, i0 + i < a.m && j0 + jj < a.n, sb, v, up);
+  }
+#endif
+}
+
+template <int TM, int TN, int KG, int S, int F>
+hipError_t launch_mid(const MatmulLaunch& l, hipStream_t stream) {
+  constexpr uint32_t out = F == kGated ? TN / 2 : TN;
+  const uint32_t tiles = ((l.m + TM - 1) / TM) * ((l.n + out - 1) / out);
+  return launch_kernel(mid_kernel<TM, TN, KG, S, F>, dim3(tiles), dim3(512), stream, l);
+}
 
 template <int TM, int TN, int WTM, int S, int F>
 hipError_t launch_pipe(const MatmulLaunch& l, hipStream_t stream) {
@@ -713,15 +894,54 @@ hipError_t launch_pipe(const MatmulLaunch& l, hipStream_t stream) {
   return launch_kernel(pipe_kernel<TM, TN, WTM, S, F>, dim3(kCus * P::kPerCu), dim3(P::kThreads), stream, l);
 }
 
+// Rows of operands that the busiest CU loads with tiles of TM tokens by TN
+// rows of b: what a call's time goes by.
+template <int TM, int TN, int F>
+uint32_t rows_a_cu(const MatmulLaunch& l) {
+  constexpr uint32_t out = F == kGated ? TN / 2 : TN;
+  const uint32_t tiles = ((l.m + TM - 1) / TM) * ((l.n + out - 1) / out);
+  return (tiles + kCus - 1) / kCus * (TM + TN);
+}
+
 template <int F>
 hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   if (!l.vec) return launch_tiles<false, F>(l, stream);
-  // The pipelined kernel's offsets within a tile are below kFar.
+  // All but the general kernel hold offsets within a tile in 30 bits.
   const bool near = (256 + (F == kGated ? static_cast<uint64_t>(l.n) : 0)) * l.b_stride + l.k < kFar &&
                     256 * l.a_stride + l.k < kFar;
-  if (near && l.m <= 32) return launch_few_sized<F>(l, stream);
-  if (!near || l.k <= 2 * kStep) return launch_tiles<true, F>(l, stream);
-  return launch_pipe<256, 256, 128, 4, F>(l, stream);
+  if (!near) return launch_tiles<true, F>(l, stream);
+  if (l.m <= 16) return launch_few_sized<1, F>(l, stream);
+  if (l.m <= 32) return launch_few_sized<2, F>(l, stream);
+  // The tile whose busiest CU loads least. The pipelined kernel's rows count
+  // half as much again: its CU takes 36 GB/s (the matrix units and the power
+  // limit bound it), the others' 50 to 58.
+  const bool narrow = F != kCodes || l.scale_layout == kScaleE8M0Block32;  // less than 128 channels a tile
+  uint32_t best = ~0u;
+  hipError_t (*launch)(const MatmulLaunch&, hipStream_t) = nullptr;
+  auto offer = [&](uint32_t rows, hipError_t (*f)(const MatmulLaunch&, hipStream_t)) {
+    if (rows < best) {
+      best = rows;
+      launch = f;
+    }
+  };
+  if (l.k > 2 * kStep) offer(rows_a_cu<256, 256, F>(l) * 3 / 2, launch_pipe<256, 256, 128, 4, F>);
+  offer(rows_a_cu<128, 256, F>(l), launch_mid<128, 256, 2, 3, F>);
+  offer(rows_a_cu<128, 128, F>(l), launch_mid<128, 128, 2, 4, F>);
+  offer(rows_a_cu<64, 128, F>(l), launch_mid<64, 128, 2, 6, F>);
+  if (narrow) {
+    offer(rows_a_cu<64, 64, F>(l), launch_mid<64, 64, 4, 4, F>);
+    offer(rows_a_cu<64, 32, F>(l), launch_mid<64, 32, 8, 3, F>);
+  }
+  const char* e = getenv("QRS_MID");
+  if (e) switch (atoi(e)) {
+    case 0: return launch_pipe<256, 256, 128, 4, F>(l, stream);
+    case 1: return launch_mid<128, 256, 2, 3, F>(l, stream);
+    case 2: return launch_mid<128, 128, 2, 4, F>(l, stream);
+    case 3: return launch_mid<64, 128, 2, 6, F>(l, stream);
+    case 4: return launch_mid<64, 64, 4, 4, F>(l, stream);
+    case 5: return launch_mid<64, 32, 8, 3, F>(l, stream);
+  }
+  return launch(l, stream);
 }
 
 }  // namespace
