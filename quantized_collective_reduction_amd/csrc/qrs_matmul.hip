@@ -231,34 +231,37 @@ hipError_t launch_tiles(const MatmulLaunch& l, hipStream_t stream) {
 
 // ---- pipelined tile kernel ---------------------------------------------
 
-// TM tokens by TN rows of b, kStep bytes of k a stage, S stages in LDS.
+// TM tokens by TN rows of b, 128 bytes of k a block, two blocks in LDS.
 // Waves of WTM tokens by 128 rows of b in 16x16x64 products: with operands
 // of random bits the card's power limit holds a loop of these from registers
 // to 4.1 POP/s, and of 32x32x32 ones (more accumulator traffic) to 3.5.
 //
 // Work-groups stay on the card and walk over tiles. Operands go from memory
-// straight into LDS, up to S stages ahead and across the end of a tile, so
-// that a tile's epilogue runs while the next one's first stages arrive.
+// straight into LDS, a block ahead and across the end of a tile, so that a
+// tile's epilogue runs while the next one's first blocks arrive. A load
+// covers 8 rows of 128 bytes: of whole lines the L2 caches deliver 32 TB/s,
+// of 16 half lines a load 17 TB/s.
 //
-// A stage's row is 64 bytes, four chunks of 16; chunk c of row r lies in
-// slot c ^ swizzle(r / 4 % 4). LDS serves a 16-byte read of a wave in four
-// groups of 16 lanes, {0-3, 12-15, 20-23, 24-27} and {4-11, 16-19, 28-31} of
-// each half; with this order of slots none of them has two lanes on a bank
-// (measured: c ^ (r / 4 % 4) doubles the reads' time). The loads fill LDS in
-// lane order, so each lane asks for the chunk that belongs in its slot.
+// Chunk c (16 bytes) of row r lies in slot c ^ (r / 2 % 8). LDS serves a
+// 16-byte read of a wave in four groups of 16 lanes, {0-3, 12-15, 20-23,
+// 24-27} and {4-11, 16-19, 28-31} of each half; with this order of slots none
+// of them has two lanes on a bank. The loads fill LDS in lane order, so each
+// lane asks for the chunk that belongs in its slot.
 //
-// A wave's products of a stage are four quarters, of half its a and half its
-// b fragments each, in an order in which consecutive quarters share one half:
-// then the other is free to be read for the quarter after, and one set of
-// fragment registers is enough (a second one costs 32 moves a stage):
-//   even stages  (a0 b0) (a0 b1) | (a1 b1) (a1 b0)
-//   odd stages   (a0 b1) (a0 b0) | (a1 b0) (a1 b1)
-// At the bar, the stage's one barrier, every wave holds the whole stage in
-// registers (its LDS is free for the stage S ahead) and the next stage has
-// landed.
+// A block is two stages of 64 bytes of k. A wave's products of a stage are
+// four quarters, of half its a and half its b fragments each, in an order in
+// which consecutive quarters share one half: then the other is free to be
+// read for the quarter after, and one set of fragment registers is enough (a
+// second one costs 32 moves a stage):
+//   first stage   (a0 b0) (a0 b1)   (a1 b1) (a1 b0)
+//   second stage  (a0 b1) (a0 b0) | (a1 b0) (a1 b1)
+// At the bar, the block's one barrier, every wave holds all of the block that
+// it still needs in registers (its LDS is free for the block after next) and
+// the next block has landed.
 constexpr int kStep = 64;
-constexpr int kChunks = kStep / 16;
+constexpr int kBlockK = 2 * kStep;
 constexpr int kWaveN = 128;
+constexpr int kLoadQuarters = 4;  // quarters that a block's loads are spread over
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -288,17 +291,17 @@ __device__ __forceinline__ void settle(i32x4 (&acc)[N]) {
                  "+a"(acc[7]));
 }
 
-template <int TM, int TN, int WTM, int S>
+template <int TM, int TN, int WTM>
 struct Pipe {
   static constexpr int kWavesM = TM / WTM, kWavesN = TN / kWaveN, kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves;
   static constexpr int FM = WTM / 16, FN = kWaveN / 16;
-  static constexpr int kLoadsA = TM / 16 / kWaves, kLoadsB = TN / 16 / kWaves, kLoads = kLoadsA + kLoadsB;
-  static constexpr int kStageBytes = (TM + TN) * kStep;
+  static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsB = TN / 8 / kWaves, kLoads = kLoadsA + kLoadsB;
+  static constexpr int kBlockBytes = (TM + TN) * kBlockK;
   static constexpr int kSumsBytes = 16 * kWaveN * 4;  // 16 tokens of a wave
-  static constexpr int kLds = S * kStageBytes + kWaves * kSumsBytes;
+  static constexpr int kLds = 2 * kBlockBytes + kWaves * kSumsBytes;
   static constexpr int kPerCu = 163840 / kLds;  // work-groups a CU holds
-  static_assert(TM % (16 * kWaves) == 0 && TN % (16 * kWaves) == 0, "whole loads a wave");
-  static_assert(kLoads % 4 == 0 && S % 2 == 0 && FM % 2 == 0, "quarters");
+  static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0, "whole loads a wave");
+  static_assert(kLoads % 4 == 0 && FM % 2 == 0, "quarters");
 };
 
 // Offsets of rows within a tile stay below kFar; a lane that has nothing to
@@ -319,10 +322,10 @@ struct TileOrder {
   }
 };
 
-template <int TM, int TN, int WTM, int S, int F>
-__global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kernel(const MatmulLaunch a) {
+template <int TM, int TN, int WTM, int F>
+__global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(const MatmulLaunch a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the buffer builtins' types exist in the device pass alone
-  using P = Pipe<TM, TN, WTM, S>;
+  using P = Pipe<TM, TN, WTM>;
   constexpr int FM = P::FM, FN = P::FN, HM = FM / 2, HN = FN / 2;
   __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
   const int lane = threadIdx.x % 64;
@@ -339,16 +342,14 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
   uint32_t tile = (tiles / 8) * xcd + min(xcd, tiles % 8) + blockIdx.x / 8;
   if (tile >= end) return;
 
-  // The loads' cursor: a tile, a stage in it, and its lanes' offsets. A
-  // ragged end of k (k % 128) makes the first two stages.
-  const uint32_t row16 = lane / kChunks;
-  const uint32_t swizzle = 0x78u >> (lane / 16 % 4 * 2) & 3;  // of row16 / 4: 0, 2, 3, 1
-  const uint32_t chunk = (lane % kChunks ^ swizzle) * 16;
-  const uint32_t tail = a.k % (2 * kStep), lead = tail != 0 ? 2 : 0;
-  const uint32_t stages = (a.k + 2 * kStep - 1) / (2 * kStep) * 2;
+  // The loads' cursor: a tile, a block in it, and the lanes' offsets. Load t
+  // of a wave covers 8 rows; lane l the chunk of row l / 8 whose slot is l % 8.
+  const uint32_t blocks = (a.k + kBlockK - 1) / kBlockK;
   __amdgpu_buffer_rsrc_t ra, rb;
   uint32_t off_a[P::kLoadsA], off_b[P::kLoadsB];
-  uint32_t load_tile = tile, load_stage = 0, load_slot = 0, load_k = 0, load_chunk = 0;
+  uint32_t load_tile = tile, load_block = 0, load_slot = 0, load_k = 0, far[2] = {0, 0};
+  // The chunk of an even or odd load: rows 8 t + l / 8, so r / 2 % 8 = 4 (t % 2) + l / 16.
+  const uint32_t chunk[2] = {(lane % 8 ^ lane / 16) * 16u, (lane % 8 ^ (4 + lane / 16)) * 16u};
   auto aim_tile = [&]() {
     uint32_t tm, tn;
     order.at(load_tile, &tm, &tn);
@@ -360,12 +361,12 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
     // Rows past the end load the last row; what they give is not stored.
 #pragma unroll
     for (int t = 0; t < P::kLoadsA; ++t) {
-      const uint32_t r = (wave * P::kLoadsA + t) * 16 + row16;
+      const uint32_t r = (wave * P::kLoadsA + t) * 8 + lane / 8;
       off_a[t] = (min(i0 + r, a.m - 1) - i0) * static_cast<uint32_t>(a.a_stride);
     }
 #pragma unroll
     for (int t = 0; t < P::kLoadsB; ++t) {
-      const uint32_t r = (wave * P::kLoadsB + t) * 16 + row16;
+      const uint32_t r = (wave * P::kLoadsB + t) * 8 + lane / 8;
       uint32_t j = r;
       if constexpr (F == kGated) j = r / kWaveN * (kWaveN / 2) + r % (kWaveN / 2);  // a wave's gates, then its ups
       j = min(j0 + j, a.n - 1) - j0;
@@ -373,70 +374,69 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
       off_b[t] = j * static_cast<uint32_t>(a.b_stride);
     }
   };
-  auto aim_stage = [&]() {  // no branch: this runs inside the pipeline
-    const bool ragged = load_stage < lead;
-    const uint32_t k0 = load_stage * kStep + (ragged ? a.k - tail : -lead * kStep);
-    const uint32_t left = tail > load_stage * kStep ? tail - load_stage * kStep : 0;
-    const uint32_t limit = load_tile >= end ? 0 : ragged ? left : kStep;
-    load_k = __builtin_amdgcn_readfirstlane(k0);
-    load_chunk = chunk < limit ? chunk : kFar;
+  auto aim_block = [&]() {  // no branch: this runs inside the pipeline
+    load_k = __builtin_amdgcn_readfirstlane(load_block * kBlockK);
+    const uint32_t k_end = load_tile < end ? a.k : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) far[h] = load_k + chunk[h] < k_end ? chunk[h] : kFar;
   };
   auto advance = [&]() {
-    load_slot = (load_slot + 1) % S;
-    ++load_stage;
-    aim_stage();
+    load_slot ^= 1;
+    ++load_block;
+    aim_block();
   };
   auto next_tile = [&]() {
-    load_slot = (load_slot + 1) % S;
-    load_stage = 0;
+    load_slot ^= 1;
+    load_block = 0;
     load_tile += stride;
     if (load_tile < end) aim_tile();
-    aim_stage();
+    aim_block();
   };
-  // Loads [first, first + n) of the cursor's stage.
-  auto load = [&](int first, int n) {
-    char* base = lds + load_slot * P::kStageBytes;
-#pragma unroll
-    for (int t = first; t < first + n; ++t) {
-      if (t < P::kLoadsA) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(base + (wave * P::kLoadsA + t) * 1024), 16,
-                                                 off_a[t] + load_chunk, load_k, 0, 0);
-      } else {
-        const int u = t - P::kLoadsA;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(base + TM * kStep + (wave * P::kLoadsB + u) * 1024), 16,
-                                                 off_b[u] + load_chunk, load_k, 0, 0);
-      }
+  // Load t of the cursor's block: a's, then b's.
+  static_assert(P::kLoadsA % 2 == 0 && P::kLoadsB % 2 == 0, "loads alternate between even and odd rows of 8");
+  auto load = [&](int t) {
+    char* base = lds + load_slot * P::kBlockBytes;
+    if (t < P::kLoadsA) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(base + (wave * P::kLoadsA + t) * 1024), 16,
+                                               off_a[t] + far[t % 2], load_k, 0, 0);
+    } else {
+      const int u = t - P::kLoadsA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(base + TM * kBlockK + (wave * P::kLoadsB + u) * 1024), 16,
+                                               off_b[u] + far[u % 2], load_k, 0, 0);
     }
   };
 
-  constexpr int kQuarter = P::kLoads / 4;
+  // A quarter issues kQuarter loads; kEarly quarters' worth of a block's go
+  // out in the block before the one that precedes it ends.
+  constexpr int kQuarter = P::kLoads / kLoadQuarters, kEarly = kLoadQuarters < 2 ? kLoadQuarters : 2;
   aim_tile();
-  aim_stage();
+  aim_block();
 #pragma unroll
-  for (int st = 0; st < S - 1; ++st) {
-    load(0, P::kLoads);
-    advance();
-  }
-  load(0, 2 * kQuarter);
+  for (int t = 0; t < P::kLoads; ++t) load(t);
+  advance();
+#pragma unroll
+  for (int t = 0; t < kEarly * kQuarter; ++t) load(t);
 
-  // Lane l reads chunk l / 16 of row l % 16 of a fragment.
-  const uint32_t lane_off = lane % 16 * kStep + ((lane / 16) ^ (0x78u >> (lane % 16 / 4 * 2) & 3)) * 16;
-  const char* base_a = lds + wm * WTM * kStep + lane_off;
-  const char* base_b = lds + TM * kStep + wn * kWaveN * kStep + lane_off;
+  // Lane l reads row l % 16 of a fragment, chunk l / 16 of a stage's four.
+  const uint32_t lane_off[2] = {lane % 16 * kBlockK + ((lane / 16) ^ (lane % 16 / 2)) * 16u,
+                                lane % 16 * kBlockK + ((4 + lane / 16) ^ (lane % 16 / 2)) * 16u};
+  const char* base_a = lds + wm * WTM * kBlockK;
+  const char* base_b = lds + TM * kBlockK + wn * kWaveN * kBlockK;
   i32x4 acc[FM][FN], fa[FM], fb[FN];
   uint32_t slot = 0;
-  auto read_a = [&](uint32_t from, int i) {
-    fa[i] = *reinterpret_cast<const i32x4*>(base_a + from * P::kStageBytes + i * 16 * kStep);
+  auto read_a = [&](uint32_t from, int st, int i) {
+    fa[i] = *reinterpret_cast<const i32x4*>(base_a + from * P::kBlockBytes + lane_off[st] + i * 16 * kBlockK);
   };
-  auto read_b = [&](uint32_t from, int j) {
-    fb[j] = *reinterpret_cast<const i32x4*>(base_b + from * P::kStageBytes + j * 16 * kStep);
+  auto read_b = [&](uint32_t from, int st, int j) {
+    fb[j] = *reinterpret_cast<const i32x4*>(base_b + from * P::kBlockBytes + lane_off[st] + j * 16 * kBlockK);
   };
   // Products of a's half ha and b's half hb, each with at most one other
-  // instruction behind it: first the reads of the quarter after, then loads
-  // kQuarter * part and on of the cursor's stage, spread over the rest. In
-  // this order, so that the matrix unit never waits for a row of others.
-  auto quarter = [&](int ha, int hb, bool reads_a, uint32_t from, int half, int part) {
+  // instruction behind it: first the reads of the quarter after, of stage st
+  // of block `from`, then the loads of `part`, spread over the rest. In this
+  // order, so that the matrix unit never waits for a row of others.
+  auto quarter = [&](int ha, int hb, bool reads_a, uint32_t from, int st, int half, int part) {
     const int reads = reads_a ? HM : HN;
+    const int loads = part < kLoadQuarters ? kQuarter : 0;
     constexpr int kProducts = HM * HN, kOthers = (HM > HN ? HM : HN) + kQuarter;
     const int each = kProducts > reads + kQuarter ? (kProducts - reads) / kQuarter : 1;
 #pragma unroll
@@ -447,36 +447,40 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
       }
       if (x < reads) {
         if (reads_a)
-          read_a(from, half * HM + x);
+          read_a(from, st, half * HM + x);
         else
-          read_b(from, half * HN + x);
-      } else if ((x - reads) % each == 0 && (x - reads) / each < kQuarter) {
-        load(part * kQuarter + (x - reads) / each, 1);
+          read_b(from, st, half * HN + x);
+      } else if ((x - reads) % each == 0 && (x - reads) / each < loads) {
+        load(part * kQuarter + (x - reads) / each);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // b's half `first` is in registers when the stage begins. `last_load`: the
-  // cursor's stage is its tile's last.
-  auto stage = [&](int first, bool last_load) {
-    const uint32_t next = (slot + 1) % S;
-    quarter(0, first, false, slot, 1 - first, 2);
-    quarter(0, 1 - first, true, slot, 1, 3);
+  constexpr int kNone = kLoadQuarters;
+  // `last_load`: the cursor's block is its tile's last.
+  auto block = [&](bool last_load) {
+    const uint32_t next = slot ^ 1;
+    quarter(0, 0, false, slot, 0, 1, 2);
+    quarter(0, 1, true, slot, 0, 1, 3);
+    quarter(1, 1, true, slot, 1, 0, kNone);
+    quarter(1, 0, false, slot, 1, 1, kNone);
+    quarter(0, 1, false, slot, 1, 0, kNone);
+    quarter(0, 0, true, slot, 1, 1, kNone);
     if (last_load)
       next_tile();
     else
       advance();
-    wait_loads_and_sync<P::kLoads * (S - 2)>();
-    quarter(1, 1 - first, true, next, 0, 0);
-    quarter(1, first, false, next, 1 - first, 1);
+    wait_loads_and_sync<0>();
+    quarter(1, 0, true, next, 0, 0, 0);
+    quarter(1, 1, false, next, 0, 0, 1);
     slot = next;
   };
 
-  wait_loads_and_sync<P::kLoads * (S - 2) + 2 * kQuarter>();
+  wait_loads_and_sync<kEarly * kQuarter>();
 #pragma unroll
-  for (int i = 0; i < HM; ++i) read_a(0, i);
+  for (int i = 0; i < HM; ++i) read_a(0, 0, i);
 #pragma unroll
-  for (int j = 0; j < HN; ++j) read_b(0, j);
+  for (int j = 0; j < HN; ++j) read_b(0, 0, j);
   auto clear = [&](int i) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
@@ -486,7 +490,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
   for (int i = 0; i < FM; ++i) clear(i);
   constexpr uint32_t out_n = F == kGated ? kWaveN / 2 : kWaveN;  // output channels of a wave
   constexpr uint32_t pieces = out_n / kPiece;
-  float* sums = reinterpret_cast<float*>(lds + S * P::kStageBytes + wave * P::kSumsBytes);
+  float* sums = reinterpret_cast<float*>(lds + 2 * P::kBlockBytes + wave * P::kSumsBytes);
   for (; tile < end; tile += stride) {
     uint32_t tm, tn;
     order.at(tile, &tm, &tn);
@@ -496,19 +500,12 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM, S>::kThreads), 1) void pipe_kern
 #pragma unroll
     for (int i = 0; i < FM; ++i) sa[i] = a.a_scales[min(i0 + 16 * i + lane % 16, a.m - 1)];
     const PieceScales sb = piece_scales<F>(a, j);
-    // From the middle of stage st on, the loads are at stage st + S.
-    for (uint32_t st = S; st < stages; st += 2) {
-      stage(0, false);
-      stage(1, false);
-    }
-    stage(0, true);
-    stage(1, false);
-#pragma unroll
-    for (int st = 2; st < S; st += 2) {
-      stage(0, false);
-      stage(1, false);
-    }
-    // 16 tokens at a time through the wave's own part of LDS, as binary32
+    // At a block's bar the loads move on to the block after next: to the next
+    // tile's first two in this tile's last two.
+    for (uint32_t b = 2; b < blocks; ++b) block(false);
+    block(true);
+    block(false);
+  // 16 tokens at a time through the wave's own part of LDS, as binary32
     // times the token's scale; 16-byte units of a token's row are xored with
     // the token, which keeps writes of one column off one bank.
 #pragma unroll
@@ -888,10 +885,10 @@ hipError_t launch_mid(const MatmulLaunch& l, hipStream_t stream) {
   return launch_kernel(mid_kernel<TM, TN, KG, S, F>, dim3(tiles), dim3(512), stream, l);
 }
 
-template <int TM, int TN, int WTM, int S, int F>
+template <int TM, int TN, int WTM, int F>
 hipError_t launch_pipe(const MatmulLaunch& l, hipStream_t stream) {
-  using P = Pipe<TM, TN, WTM, S>;
-  return launch_kernel(pipe_kernel<TM, TN, WTM, S, F>, dim3(kCus * P::kPerCu), dim3(P::kThreads), stream, l);
+  using P = Pipe<TM, TN, WTM>;
+  return launch_kernel(pipe_kernel<TM, TN, WTM, F>, dim3(kCus * P::kPerCu), dim3(P::kThreads), stream, l);
 }
 
 // Rows of operands that the busiest CU loads with tiles of TM tokens by TN
@@ -924,7 +921,7 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
       launch = f;
     }
   };
-  if (l.k > 2 * kStep) offer(rows_a_cu<256, 256, F>(l) * 3 / 2, launch_pipe<256, 256, 128, 4, F>);
+  if (l.k > kBlockK) offer(rows_a_cu<256, 256, F>(l) * 3 / 2, launch_pipe<256, 256, 128, F>);
   offer(rows_a_cu<128, 256, F>(l), launch_mid<128, 256, 2, 3, F>);
   offer(rows_a_cu<128, 128, F>(l), launch_mid<128, 128, 2, 4, F>);
   offer(rows_a_cu<64, 128, F>(l), launch_mid<64, 128, 2, 6, F>);
@@ -934,7 +931,7 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   }
   const char* e = getenv("QRS_MID");
   if (e) switch (atoi(e)) {
-    case 0: return launch_pipe<256, 256, 128, 4, F>(l, stream);
+    case 0: return launch_pipe<256, 256, 128, F>(l, stream);
     case 1: return launch_mid<128, 256, 2, 3, F>(l, stream);
     case 2: return launch_mid<128, 128, 2, 4, F>(l, stream);
     case 3: return launch_mid<64, 128, 2, 6, F>(l, stream);
