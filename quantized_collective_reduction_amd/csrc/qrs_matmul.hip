@@ -31,6 +31,21 @@ constexpr uint32_t kCus = 256;
 
 // ---- epilogue ----------------------------------------------------------
 
+// g / (1 + exp(-g)). exp as a power of two whose exponent's rounding error is
+// put back as a factor, 1 / d as the hardware's estimate and one Newton step:
+// each within a few units of the last place, for a third of the instructions
+// of the library's exp and divide (a gated tile's epilogue 9 us -> 4 us). The
+// power is kept below 2^126, so that its reciprocal is a normal number.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+  const float p = -g * kLog2e;
+  const float low = __builtin_fmaf(-g, kLog2eLow, __builtin_fmaf(-g, kLog2e, -p));
+  const float e = __builtin_amdgcn_exp2f(p);
+  const float d = 1.0f + __builtin_fminf(__builtin_fmaf(e, low * kLn2, e), 0x1p126f);
+  const float r = __builtin_amdgcn_rcpf(d);
+  return g * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
 // What a kernel instance writes.
 enum Finish : int { kValues = 0, kGated = 1, kCodes = 2 };
 
@@ -89,10 +104,10 @@ __device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, 
   }
 }
 
-template <int OF>
+template <int OF, bool WHOLE>
 __device__ __forceinline__ void finish_values(const MatmulLaunch& a, uint32_t i, uint32_t j0, const float* v) {
   char* row = static_cast<char*>(a.out) + static_cast<uint64_t>(i) * a.out_stride * kOutSize<OF>;
-  if (a.out_vec && j0 + kPiece <= a.n)
+  if (WHOLE || (a.out_vec && j0 + kPiece <= a.n))
     store_piece<OF, true>(row, j0, a.n, v);
   else
     store_piece<OF, false>(row, j0, a.n, v);
@@ -101,26 +116,27 @@ __device__ __forceinline__ void finish_values(const MatmulLaunch& a, uint32_t i,
 // Eight outputs [j0, j0 + 8) of token i. v: the integer sums as binary32
 // times the token's scale (gated: of the gates; up: of the ups). `active`
 // says whether i and j0 are inside the output; where codes are written, all
-// lanes of a group (16 or 4 consecutive ones) call this together.
-template <int F>
+// lanes of a group (16 or 4 consecutive ones) call this together. WHOLE: every
+// piece of the tile is inside and may be stored 16 bytes at a time.
+template <int F, bool WHOLE = false>
 __device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active,
                                              const PieceScales& s, float* v, const float* up) {
 #pragma unroll
   for (int j = 0; j < kPiece; ++j) v[j] *= s.b[j];
   if constexpr (F == kCodes) {
-    finish_codes(a, i, j0, active, v);
+    finish_codes(a, i, j0, WHOLE || active, v);
   } else {
     if constexpr (F == kGated) {
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) v[j] = v[j] / (1.0f + expf(-v[j])) * (up[j] * s.up[j]);
+      for (int j = 0; j < kPiece; ++j) v[j] = silu(v[j]) * (up[j] * s.up[j]);
     }
-    if (!active) return;
+    if (!WHOLE && !active) return;
     if (a.out_format == kOutF32)
-      finish_values<kOutF32>(a, i, j0, v);
+      finish_values<kOutF32, WHOLE>(a, i, j0, v);
     else if (a.out_format == kOutBF16)
-      finish_values<kOutBF16>(a, i, j0, v);
+      finish_values<kOutBF16, WHOLE>(a, i, j0, v);
     else
-      finish_values<kOutF16>(a, i, j0, v);
+      finish_values<kOutF16, WHOLE>(a, i, j0, v);
   }
 }
 
@@ -281,8 +297,13 @@ __device__ __forceinline__ void mfma(i32x4& acc, const i32x4& b, const i32x4& a)
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
+// acc = b a^T.
+__device__ __forceinline__ void mfma_first(i32x4& acc, const i32x4& b, const i32x4& a) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(acc) : "v"(b), "v"(a));
+}
+
 // A row of accumulators, readable by other instructions (after at most 18
-// cycles) and, cleared, by the next products.
+// cycles).
 template <int N>
 __device__ __forceinline__ void settle(i32x4 (&acc)[N]) {
   static_assert(N == 8, "one operand for each");
@@ -424,6 +445,12 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
   const char* base_b = lds + TM * kBlockK + wn * kWaveN * kBlockK;
   i32x4 acc[FM][FN], fa[FM], fb[FN];
   uint32_t slot = 0;
+  // A tile's first bar waits for loads that were issued before the last
+  // epilogue's stores. Loads and stores are counted in order: where all of
+  // that epilogue's stores were made (a whole tile: one a piece at least), it
+  // lets that many be under way.
+  constexpr int kWholeStores = FM * 16 * (F == kGated ? kWaveN / 2 : kWaveN) / kPiece / 64;
+  bool whole_before = false;
   auto read_a = [&](uint32_t from, int st, int i) {
     fa[i] = *reinterpret_cast<const i32x4*>(base_a + from * P::kBlockBytes + lane_off[st] + i * 16 * kBlockK);
   };
@@ -434,7 +461,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
   // instruction behind it: first the reads of the quarter after, of stage st
   // of block `from`, then the loads of `part`, spread over the rest. In this
   // order, so that the matrix unit never waits for a row of others.
-  auto quarter = [&](int ha, int hb, bool reads_a, uint32_t from, int st, int half, int part) {
+  auto quarter = [&](int ha, int hb, bool reads_a, uint32_t from, int st, int half, int part, bool first = false) {
     const int reads = reads_a ? HM : HN;
     const int loads = part < kLoadQuarters ? kQuarter : 0;
     constexpr int kProducts = HM * HN, kOthers = (HM > HN ? HM : HN) + kQuarter;
@@ -443,7 +470,10 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
     for (int x = 0; x < (kProducts > kOthers ? kProducts : kOthers); ++x) {
       if (x < kProducts) {
         const int i = ha * HM + x / HN, j = hb * HN + x % HN;
-        mfma(acc[i][j], fb[j], fa[i]);
+        if (first)
+          mfma_first(acc[i][j], fb[j], fa[i]);
+        else
+          mfma(acc[i][j], fb[j], fa[i]);
       }
       if (x < reads) {
         if (reads_a)
@@ -457,20 +487,24 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
     }
   };
   constexpr int kNone = kLoadQuarters;
+  // `first`: the tile's first block, whose next block is all on its way.
   // `last_load`: the cursor's block is its tile's last.
-  auto block = [&](bool last_load) {
+  auto block = [&](bool first, bool last_load) {
     const uint32_t next = slot ^ 1;
-    quarter(0, 0, false, slot, 0, 1, 2);
-    quarter(0, 1, true, slot, 0, 1, 3);
-    quarter(1, 1, true, slot, 1, 0, kNone);
-    quarter(1, 0, false, slot, 1, 1, kNone);
+    quarter(0, 0, false, slot, 0, 1, first ? kNone : 2, first);
+    quarter(0, 1, true, slot, 0, 1, first ? kNone : 3, first);
+    quarter(1, 1, true, slot, 1, 0, kNone, first);
+    quarter(1, 0, false, slot, 1, 1, kNone, first);
     quarter(0, 1, false, slot, 1, 0, kNone);
     quarter(0, 0, true, slot, 1, 1, kNone);
     if (last_load)
       next_tile();
     else
       advance();
-    wait_loads_and_sync<0>();
+    if (first && whole_before)
+      wait_loads_and_sync<kWholeStores>();
+    else
+      wait_loads_and_sync<0>();
     quarter(1, 0, true, next, 0, 0, 0);
     quarter(1, 1, false, next, 0, 0, 1);
     slot = next;
@@ -481,59 +515,85 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
   for (int i = 0; i < HM; ++i) read_a(0, 0, i);
 #pragma unroll
   for (int j = 0; j < HN; ++j) read_b(0, 0, j);
-  auto clear = [&](int i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    settle(acc[i]);
-  };
-#pragma unroll
-  for (int i = 0; i < FM; ++i) clear(i);
+  for (int t = kEarly * kQuarter; t < P::kLoads; ++t) load(t);
   constexpr uint32_t out_n = F == kGated ? kWaveN / 2 : kWaveN;  // output channels of a wave
   constexpr uint32_t pieces = out_n / kPiece;
-  float* sums = reinterpret_cast<float*>(lds + 2 * P::kBlockBytes + wave * P::kSumsBytes);
+  int32_t* sums = reinterpret_cast<int32_t*>(lds + 2 * P::kBlockBytes + wave * P::kSumsBytes);
   for (; tile < end; tile += stride) {
     uint32_t tm, tn;
     order.at(tile, &tm, &tn);
     const uint32_t i0 = tm * TM + wm * WTM;
     const uint32_t j = tn * tile_n + wn * out_n + lane % pieces * kPiece;
-    float sa[FM];  // of token l % 16 of each fragment
-#pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = a.a_scales[min(i0 + 16 * i + lane % 16, a.m - 1)];
-    const PieceScales sb = piece_scales<F>(a, j);
     // At a block's bar the loads move on to the block after next: to the next
     // tile's first two in this tile's last two.
-    for (uint32_t b = 2; b < blocks; ++b) block(false);
-    block(true);
-    block(false);
-  // 16 tokens at a time through the wave's own part of LDS, as binary32
-    // times the token's scale; 16-byte units of a token's row are xored with
-    // the token, which keeps writes of one column off one bank.
+    if (blocks == 2) {
+      block(true, true);
+    } else {
+      block(true, false);
+      for (uint32_t b = 3; b < blocks; ++b) block(false, false);
+      block(false, true);
+    }
+    block(false, false);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    for (int t = kEarly * kQuarter; t < P::kLoads; ++t) load(t);
+
+    constexpr uint32_t kPass = 64 / pieces;  // tokens at a time
+    float sa[FM][16 / kPass];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (uint32_t t = 0; t < 16 / kPass; ++t)
+        sa[i][t] = a.a_scales[min(i0 + 16 * i + t * kPass + lane / pieces, a.m - 1)];
+    const PieceScales sb = piece_scales<F>(a, j);
+    // 16 tokens at a time through the wave's own part of LDS; 16-byte units
+    // of a token's row are xored with the token, which keeps writes of one
+    // column off one bank.
+    auto stage_sums = [&](int i) {
       __builtin_amdgcn_sched_barrier(0);  // one fragment's values in registers at a time
       settle(acc[i]);
 #pragma unroll
-      for (int g = 0; g < FN; ++g) {
-        // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16.
-        f32x4 v;
+      for (int g = 0; g < FN; ++g)  // lane l holds channels 4 (l / 16) .. + 3 of token l % 16
+        *reinterpret_cast<i32x4*>(sums + lane % 16 * kWaveN + ((4 * g + lane / 16) ^ (lane % 16)) * 4) = acc[i][g];
+    };
+    auto values = [&](uint32_t t, uint32_t unit, float scale, float* v) {
+      const i32x4* row = reinterpret_cast<const i32x4*>(sums + t * kWaveN);
+      const i32x4 lo = row[unit ^ t], hi = row[(unit + 1) ^ t];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][g][e]) * sa[i];
-        *reinterpret_cast<f32x4*>(sums + lane % 16 * kWaveN + ((4 * g + lane / 16) ^ (lane % 16)) * 4) = v;
+      for (int e = 0; e < 4; ++e) {
+        v[e] = static_cast<float>(lo[e]) * scale;
+        v[4 + e] = static_cast<float>(hi[e]) * scale;
       }
-      clear(i);
+    };
+    const uint32_t unit = lane % pieces * 2;
+    whole_before = tm * TM + TM <= a.m && (tn + 1) * tile_n <= a.n && (F == kCodes || a.out_vec);
+    if (whole_before) {
 #pragma unroll
-      for (uint32_t t0 = 0; t0 < 16; t0 += 64 / pieces) {
-        const uint32_t t = t0 + lane / pieces, u = lane % pieces * 2;
-        const f32x4* row = reinterpret_cast<const f32x4*>(sums + t * kWaveN);
-        float v[kPiece], up[kPiece];
-        *reinterpret_cast<f32x4*>(v) = row[u ^ t];
-        *reinterpret_cast<f32x4*>(v + 4) = row[(u + 1) ^ t];
-        if constexpr (F == kGated) {
-          *reinterpret_cast<f32x4*>(up) = row[(u + 2 * pieces) ^ t];
-          *reinterpret_cast<f32x4*>(up + 4) = row[(u + 2 * pieces + 1) ^ t];
+      for (int i = 0; i < FM; ++i) {
+        stage_sums(i);
+#pragma unroll
+        for (uint32_t p = 0; p < 16 / kPass; ++p) {
+          const uint32_t t = p * kPass + lane / pieces;
+          float v[kPiece], up[kPiece];
+          values(t, unit, sa[i][p], v);
+          if constexpr (F == kGated) values(t, unit + 2 * pieces, sa[i][p], up);
+          finish_piece<F, true>(a, i0 + 16 * i + t, j, true, sb, v, up);
         }
-        const uint32_t token = i0 + 16 * i + t;
-        finish_piece<F>(a, token, j, token < a.m && j < a.n, sb, v, up);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        stage_sums(i);
+#pragma unroll 1
+        for (uint32_t p = 0; p < 16 / kPass; ++p) {
+          const uint32_t t = p * kPass + lane / pieces;
+          const uint32_t token = i0 + 16 * i + t;
+          const float scale = a.a_scales[min(token, a.m - 1)];
+          float v[kPiece], up[kPiece];
+          values(t, unit, scale, v);
+          if constexpr (F == kGated) values(t, unit + 2 * pieces, scale, up);
+          finish_piece<F>(a, token, j, token < a.m && j < a.n, sb, v, up);
+        }
       }
     }
   }
