@@ -324,6 +324,7 @@ qrs_status matmul(qrs::MatmulLaunch* l, int64_t m, int64_t n, int64_t k, int gat
   l->gated = gated != 0;
   l->vec = k % 16 == 0 && in[0].rows_on(16) && in[1].rows_on(16);
   l->out_vec = out.rows_on(16);
+  l->out_near = out.stride * out.size < (int64_t{1} << 22) && scales.stride * scales.size < (int64_t{1} << 22);
   l->a = static_cast<const int8_t*>(a);
   l->a_stride = static_cast<uint64_t>(a_row_stride);
   l->a_scales = a_scales;

@@ -73,7 +73,8 @@ struct MatmulLaunch {
   bool gated;
   bool quantize;
   bool vec;      // k % 16 == 0, and every row of a and b starts on a 16-byte boundary
-  bool out_vec;  // quantize = false: every row of out starts on a 16-byte boundary
+  bool out_vec;   // quantize = false: every row of out starts on a 16-byte boundary
+  bool out_near;  // 256 rows of out, and of scales, span less than 2^30 bytes
   OutFormat out_format;      // quantize = false
   XFormat x_format;          // quantize = true
   ScaleLayout scale_layout;  // quantize = true

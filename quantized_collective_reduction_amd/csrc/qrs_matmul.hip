@@ -53,6 +53,13 @@ enum Finish : int { kValues = 0, kGated = 1, kCodes = 2 };
 // of its up channels.
 struct PieceScales {
   float b[kPiece], up[kPiece];
+
+  __device__ bool finite() const {
+    bool all = true;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) all = all && abs_bits(b[j]) < 0x7F800000u;
+    return all;
+  }
 };
 
 template <int F>
@@ -66,77 +73,87 @@ __device__ __forceinline__ PieceScales piece_scales(const MatmulLaunch& a, uint3
   return s;
 }
 
-// The codes of a piece and its group's scale, the mode chosen at run time: a
-// kernel's epilogue repeats this for every fragment, and a copy for each mode
-// would be five times the code.
-__device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, const float* v) {
-  const bool mx = a.scale_layout == kScaleE8M0Block32;
-  uint32_t amax = 0;
+// The codes of a piece and its group's scale (E8M0 code or binary32 bits),
+// the mode chosen at run time: a kernel's epilogue repeats this for every
+// fragment, and a copy for each mode would be five times the code. `finite`:
+// the scales that v was multiplied by are, so that v holds no NaN.
+__device__ __forceinline__ u32x2 encode_group(const MatmulLaunch& a, const float* v, bool finite, uint32_t* scale_bits) {
+  float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
 #pragma unroll
-  for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[j]));
-  amax = group_max<4>(amax);
-  float mul, scale = 0.0f;
-  uint32_t code = 0;
-  if (mx) {
-    mul = a.x_format == kXE4M3FN ? mx_multiplier<kXE4M3FN>(amax, &code) : mx_multiplier<kXE5M2>(amax, &code);
+  for (int j = 2; j < kPiece; ++j) m = __builtin_fmaxf(m, __builtin_fabsf(v[j]));
+  uint32_t amax = group_max<4>(finite ? __builtin_bit_cast(uint32_t, m) : 0x7FC00000u);
+  float mul;
+  if (a.scale_layout == kScaleE8M0Block32) {
+    mul = a.x_format == kXE4M3FN ? mx_multiplier<kXE4M3FN>(amax, scale_bits) : mx_multiplier<kXE5M2>(amax, scale_bits);
   } else {
     amax = max(amax, dpp<kDppHalfMirror>(amax));
     amax = max(amax, dpp<kDppMirror>(amax));
     const float top = a.x_format == kXE4M3FN ? CodeFormat<kXE4M3FN>::kMax
                       : a.x_format == kXE5M2 ? CodeFormat<kXE5M2>::kMax
                                              : CodeFormat<kXInt8>::kMax;
+    float scale;
     mul = f32_multiplier(amax, top, &scale);
+    *scale_bits = __builtin_bit_cast(uint32_t, scale);
   }
-  u32x2 w;
-  if (a.x_format == kXE4M3FN)
-    w = encode_piece<kXE4M3FN>(v, mul);
-  else if (a.x_format == kXE5M2)
-    w = encode_piece<kXE5M2>(v, mul);
-  else
-    w = encode_piece<kXInt8>(v, mul);
+  if (a.x_format == kXE4M3FN) return encode_piece<kXE4M3FN>(v, mul);
+  if (a.x_format == kXE5M2) return encode_piece<kXE5M2>(v, mul);
+  return encode_piece<kXInt8>(v, mul);
+}
+
+__device__ __forceinline__ bool is_finite(float v) { return abs_bits(v) < 0x7F800000u; }
+
+__device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, bool finite,
+                                             const float* v) {
+  uint32_t scale;
+  const u32x2 w = encode_group(a, v, finite, &scale);
   if (!active) return;
   *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + static_cast<uint64_t>(i) * a.out_stride + j0) = w;
-  if (mx) {
+  if (a.scale_layout == kScaleE8M0Block32) {
     if (j0 % 32 == 0)
-      static_cast<uint8_t*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 32) + j0 / 32] = static_cast<uint8_t>(code);
+      static_cast<uint8_t*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 32) + j0 / 32] = static_cast<uint8_t>(scale);
   } else {
-    if (j0 % 128 == 0) static_cast<float*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 128) + j0 / 128] = scale;
+    if (j0 % 128 == 0) static_cast<uint32_t*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 128) + j0 / 128] = scale;
   }
 }
 
-template <int OF, bool WHOLE>
+template <int OF>
 __device__ __forceinline__ void finish_values(const MatmulLaunch& a, uint32_t i, uint32_t j0, const float* v) {
   char* row = static_cast<char*>(a.out) + static_cast<uint64_t>(i) * a.out_stride * kOutSize<OF>;
-  if (WHOLE || (a.out_vec && j0 + kPiece <= a.n))
+  if (a.out_vec && j0 + kPiece <= a.n)
     store_piece<OF, true>(row, j0, a.n, v);
   else
     store_piece<OF, false>(row, j0, a.n, v);
 }
 
-// Eight outputs [j0, j0 + 8) of token i. v: the integer sums as binary32
-// times the token's scale (gated: of the gates; up: of the ups). `active`
-// says whether i and j0 are inside the output; where codes are written, all
-// lanes of a group (16 or 4 consecutive ones) call this together. WHOLE: every
-// piece of the tile is inside and may be stored 16 bytes at a time.
-template <int F, bool WHOLE = false>
-__device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active,
-                                             const PieceScales& s, float* v, const float* up) {
+// v: a piece's integer sums as binary32 times the token's scale sa (gated: of
+// the gates; up: of the ups) -> the outputs as binary32.
+template <int F>
+__device__ __forceinline__ void scale_piece(const PieceScales& s, float* v, const float* up) {
 #pragma unroll
   for (int j = 0; j < kPiece; ++j) v[j] *= s.b[j];
-  if constexpr (F == kCodes) {
-    finish_codes(a, i, j0, WHOLE || active, v);
-  } else {
-    if constexpr (F == kGated) {
+  if constexpr (F == kGated) {
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) v[j] = silu(v[j]) * (up[j] * s.up[j]);
-    }
-    if (!WHOLE && !active) return;
+    for (int j = 0; j < kPiece; ++j) v[j] = silu(v[j]) * (up[j] * s.up[j]);
+  }
+}
+
+// Eight outputs [j0, j0 + 8) of token i; v and up as for scale_piece. `active`
+// says whether i and j0 are inside the output; where codes are written, all
+// lanes of a group (16 or 4 consecutive ones) call this together.
+template <int F>
+__device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, float sa,
+                                             const PieceScales& s, float* v, const float* up) {
+  scale_piece<F>(s, v, up);
+  if constexpr (F == kCodes) {
+    finish_codes(a, i, j0, active, is_finite(sa) && s.finite(), v);
+  } else {
+    if (!active) return;
     if (a.out_format == kOutF32)
-      finish_values<kOutF32, WHOLE>(a, i, j0, v);
+      finish_values<kOutF32>(a, i, j0, v);
     else if (a.out_format == kOutBF16)
-      finish_values<kOutBF16, WHOLE>(a, i, j0, v);
+      finish_values<kOutBF16>(a, i, j0, v);
     else
-      finish_values<kOutF16, WHOLE>(a, i, j0, v);
+      finish_values<kOutF16>(a, i, j0, v);
   }
 }
 
@@ -233,7 +250,7 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulLaunch a) {
       v[e] = static_cast<float>(p[e]) * sa;
       if constexpr (F == kGated) up[e] = static_cast<float>(p[kTileN / 2 + e]) * sa;
     }
-    finish_piece<F>(a, i0 + i, j0 + j, i0 + i < a.m && j0 + j < a.n, piece_scales<F>(a, j0 + j), v, up);
+    finish_piece<F>(a, i0 + i, j0 + j, i0 + i < a.m && j0 + j < a.n, sa, piece_scales<F>(a, j0 + j), v, up);
   }
 }
 
@@ -342,6 +359,67 @@ struct TileOrder {
     *tn = in_group / group_m;
   }
 };
+
+#ifdef __HIP_DEVICE_COMPILE__
+// Stores of a wave's part of a tile that lies whole inside the output, from
+// token i0 and channel j0 on; this lane's are of token i0 + row + t and
+// channels j0 + col .. + 7. A uniform base, a lane's offset and the token in a
+// scalar, so that no address is computed for a store. They go past the caches
+// (16384 x 8192 bf16 values: 404 -> 379 us; they fill L2 otherwise).
+template <int F>
+struct WholeTile {
+  static constexpr int kStream = 2;
+  __amdgpu_buffer_rsrc_t out, scales;
+  uint32_t out_lane, out_row, scale_lane, scale_row;
+  bool has_scale;
+
+  __device__ __forceinline__ WholeTile(const MatmulLaunch& a, uint32_t i0, uint32_t j0, uint32_t row, uint32_t col) {
+    const uint32_t size = F == kCodes ? 1 : a.out_format == kOutF32 ? 4 : 2;
+    out_row = static_cast<uint32_t>(a.out_stride) * size;
+    out_lane = row * out_row + col * size;
+    out = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<char*>(a.out) + static_cast<uint64_t>(i0) * out_row + static_cast<uint64_t>(j0) * size, 0, kFar,
+        0x00020000);
+    if constexpr (F == kCodes) {
+      const bool mx = a.scale_layout == kScaleE8M0Block32;
+      const uint32_t g = mx ? 32 : 128, scale_size = mx ? 1 : 4;
+      scale_row = a.n / g * scale_size;
+      scale_lane = row * scale_row + col / g * scale_size;
+      has_scale = col % g == 0;
+      scales = __builtin_amdgcn_make_buffer_rsrc(
+          static_cast<char*>(a.scales) + static_cast<uint64_t>(i0) * scale_row + j0 / g * scale_size, 0, kFar,
+          0x00020000);
+    }
+  }
+
+  __device__ __forceinline__ void store(const MatmulLaunch& a, uint32_t t, const float* v, bool finite) const {
+    if constexpr (F == kCodes) {
+      uint32_t scale;
+      const u32x2 w = encode_group(a, v, finite, &scale);
+      __builtin_amdgcn_raw_buffer_store_b64(w, out, out_lane, t * out_row, kStream);
+      if (has_scale) {
+        if (a.scale_layout == kScaleE8M0Block32)
+          __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(scale), scales, scale_lane, t * scale_row, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b32(scale, scales, scale_lane, t * scale_row, 0);
+      }
+    } else if (a.out_format == kOutF32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), out, out_lane + 16 * h, t * out_row, kStream);
+      }
+    } else {
+      const bool bf = a.out_format == kOutBF16;
+      u32x4 w;
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        w[h] = bf ? pack2<kOutBF16>(v[2 * h], v[2 * h + 1]) : pack2<kOutF16>(v[2 * h], v[2 * h + 1]);
+      __builtin_amdgcn_raw_buffer_store_b128(w, out, out_lane, t * out_row, kStream);
+    }
+  }
+};
+#endif
 
 template <int TM, int TN, int WTM, int F>
 __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(const MatmulLaunch a) {
@@ -534,10 +612,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
       for (uint32_t b = 3; b < blocks; ++b) block(false, false);
       block(false, true);
     }
-    block(false, false);
-#pragma unroll
-    for (int t = kEarly * kQuarter; t < P::kLoads; ++t) load(t);
-
+    // Scales, asked for a block ahead of their use.
     constexpr uint32_t kPass = 64 / pieces;  // tokens at a time
     float sa[FM][16 / kPass];
 #pragma unroll
@@ -546,6 +621,10 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
       for (uint32_t t = 0; t < 16 / kPass; ++t)
         sa[i][t] = a.a_scales[min(i0 + 16 * i + t * kPass + lane / pieces, a.m - 1)];
     const PieceScales sb = piece_scales<F>(a, j);
+    block(false, false);
+#pragma unroll
+    for (int t = kEarly * kQuarter; t < P::kLoads; ++t) load(t);
+
     // 16 tokens at a time through the wave's own part of LDS; 16-byte units
     // of a token's row are xored with the token, which keeps writes of one
     // column off one bank.
@@ -566,8 +645,10 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
       }
     };
     const uint32_t unit = lane % pieces * 2;
-    whole_before = tm * TM + TM <= a.m && (tn + 1) * tile_n <= a.n && (F == kCodes || a.out_vec);
+    whole_before = tm * TM + TM <= a.m && (tn + 1) * tile_n <= a.n && (F == kCodes || a.out_vec) && a.out_near;
     if (whole_before) {
+      const WholeTile<F> whole(a, i0, tn * tile_n + wn * out_n, lane / pieces, lane % pieces * kPiece);
+      const bool sb_finite = F != kCodes || sb.finite();
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         stage_sums(i);
@@ -577,7 +658,8 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
           float v[kPiece], up[kPiece];
           values(t, unit, sa[i][p], v);
           if constexpr (F == kGated) values(t, unit + 2 * pieces, sa[i][p], up);
-          finish_piece<F, true>(a, i0 + 16 * i + t, j, true, sb, v, up);
+          scale_piece<F>(sb, v, up);
+          whole.store(a, 16 * i + p * kPass, v, sb_finite && is_finite(sa[i][p]));
         }
       }
     } else {
@@ -592,7 +674,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
           float v[kPiece], up[kPiece];
           values(t, unit, scale, v);
           if constexpr (F == kGated) values(t, unit + 2 * pieces, scale, up);
-          finish_piece<F>(a, token, j, token < a.m && j < a.n, sb, v, up);
+          finish_piece<F>(a, token, j, token < a.m && j < a.n, scale, sb, v, up);
         }
       }
     }
@@ -743,7 +825,7 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
       sb.up[e] = row_scale[r + RB / 2 + e];
     }
   }
-  finish_piece<F>(a, i, j0 + jj, i < a.m && j0 + jj < a.n, sb, v, up);
+  finish_piece<F>(a, i, j0 + jj, i < a.m && j0 + jj < a.n, token_scale[i], sb, v, up);
 #endif
 }
 
@@ -933,7 +1015,7 @@ __global__ __launch_bounds__(512, 1) void mid_kernel(const MatmulLaunch a) {
         sb.up[e] = scales[TM + r + 16 + e];
       }
     }
-    finish_piece<F>(a, i0 + i, j0 + jj, i0 + i < a.m && j0 + jj < a.n, sb, v, up);
+    finish_piece<F>(a, i0 + i, j0 + jj, i0 + i < a.m && j0 + jj < a.n, scales[i], sb, v, up);
   }
 #endif
 }
