@@ -332,13 +332,12 @@ qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scal
  * and y as codes and scales.
  *
  * s is rounded once to the activations' type and stored in sum_out; y is
- * computed from the stored s in binary32 and quantized without another
- * rounding, by qrs_quantize's rules for QRS_SCALE_F32_GROUP128 and
+ * computed from the stored s in binary64, rounded once to binary32 and
+ * quantized by qrs_quantize's rules for QRS_SCALE_F32_GROUP128 and
  * QRS_SCALE_E8M0_BLOCK32. QRS_SCALE_F32_ROW takes the whole row as one group
  * of the same rule. A group that holds a NaN or an infinity gets a NaN or
  * infinite scale (E8M0 code 255), so that it stays visible; its codes are
- * unspecified. Squares are summed in binary32: rows whose sum of squares
- * overflows it are taken as infinitely large (y = 0).
+ * unspecified.
  *
  *   tokens, h     rows of x; h in [1, 65536], a multiple of the layout's
  *                 group (128 or 32; any for QRS_SCALE_F32_ROW).

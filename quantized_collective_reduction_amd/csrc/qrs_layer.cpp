@@ -163,6 +163,7 @@ qrs_status qrs_add_rms_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype io
           (!residual || (in[2].rows_on(16) && out[2].rows_on(16)));
   l.h = static_cast<uint32_t>(h);
   l.eps = eps;
+  l.inv_h = 1.0 / static_cast<double>(h);
   l.rows = static_cast<uint64_t>(tokens);
   l.x = x;
   l.x_stride = static_cast<uint64_t>(x_row_stride);
@@ -213,7 +214,8 @@ qrs_status qrs_rms_norm_backward_workspace(int64_t tokens, int64_t h, size_t* by
   if (!bytes_out) return fail(QRS_ERR_INVALID_ARG, "null bytes_out");
   *bytes_out = 0;
   QRS_TRY(check_row_shape(tokens, h));
-  *bytes_out = static_cast<size_t>(qrs::norm_backward_parts(static_cast<uint64_t>(tokens))) * static_cast<size_t>(h) * 4;
+  *bytes_out = static_cast<size_t>(h) * 4 *
+               qrs::norm_backward_parts(static_cast<uint64_t>(tokens), static_cast<uint32_t>(h));
   return ok();
 }
 

@@ -23,6 +23,7 @@ struct RowsLaunch {
   bool vec;  // h % 8 == 0, and every row starts on a 16-byte boundary (codes: 8)
   uint32_t h;
   float eps;
+  double inv_h;  // 1 / h
   uint64_t rows;
   const void* x;
   uint64_t x_stride;
@@ -57,11 +58,11 @@ struct NormBackwardLaunch {
   void* grad_x;
   uint64_t grad_x_stride;
   float* grad_weight;
-  float* workspace;  // norm_backward_parts(rows) rows of h floats
+  float* workspace;  // norm_backward_parts(rows, h) rows of h floats
 };
 
 // Work-groups of the backward pass, and rows of its workspace.
-inline uint32_t norm_backward_parts(uint64_t rows) { return rows < 512 ? static_cast<uint32_t>(rows) : 512u; }
+uint32_t norm_backward_parts(uint64_t rows, uint32_t h);
 
 hipError_t launch_norm_backward(const NormBackwardLaunch& l, hipStream_t stream);
 

@@ -26,49 +26,106 @@ namespace {
 
 using namespace dev;
 
-// Sum (or maximum) over a work-group of NT lanes, in every lane, in a fixed
-// order. `part` holds one value per wave and is used once.
-template <int NT>
-__device__ __forceinline__ float block_sum(float v, float* part) {
-  v = wave_sum(v);
-  if constexpr (NT > 64) {
-    constexpr int kWaves = NT / 64;
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = v;
-    __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += part[w];
+// s_waitcnt for LDS and scalar loads alone (lgkmcnt 0, vmcnt and expcnt at most).
+constexpr int kWaitLds = 0xC07F;
+
+// A piece as it lies in memory (VEC), so that rows under way cost half the
+// registers for 16-bit types; otherwise as floats. STREAM: loads that leave no
+// copy in the caches.
+template <int IO, bool VEC>
+struct RawPiece {
+  float v[kPiece];
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const void* row, uint32_t c, uint32_t h) {
+    load_piece<IO, VEC>(row, c, h, v);
   }
-  return v;
+  __device__ __forceinline__ void get(float* to) const {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) to[j] = v[j];
+  }
+};
+template <int IO>
+struct RawPiece16 {
+  u32x4 w;
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const void* row, uint32_t c, uint32_t h) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+    w = u32x4{0u, 0u, 0u, 0u};
+    if (c < h) w = STREAM ? __builtin_nontemporal_load(p) : *p;
+  }
+  __device__ __forceinline__ void get(float* to) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack2<IO>(w[j], to + 2 * j);
+  }
+};
+template <>
+struct RawPiece<kOutF32, true> {
+  f32x4 w[2];
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const void* row, uint32_t c, uint32_t h) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (c < h) w[i] = STREAM ? __builtin_nontemporal_load(p + i) : p[i];
+    }
+  }
+  __device__ __forceinline__ void get(float* to) const {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) to[j] = w[j / 4][j % 4];
+  }
+};
+template <>
+struct RawPiece<kOutBF16, true> : RawPiece16<kOutBF16> {};
+template <>
+struct RawPiece<kOutF16, true> : RawPiece16<kOutF16> {};
+
+// Operands beyond this many bytes pass through the Infinity Cache (256 MB)
+// without being found there again: they are loaded as a stream (backward
+// pass, 1074 MB: 195 us, as a stream 174; 59 MB, found there: 20.2 and 21.6).
+constexpr uint64_t kStreamBytes = uint64_t{256} << 20;
+
+// Work-groups of a kernel that walks over rows: `per_row` / h, and one a CU at
+// least. More for narrow rows, whose operands under way would not fill the
+// memory's pipe; too many leave none to load ahead of (norm to codes, bf16:
+// 16384 x 1024 with 512, 1024, 2048 and 4096 work-groups 47.5, 36.2, 33.0 and
+// 30.2 us; 2048 x 8192 with 256, 512, 1024 and 2048 24.4, 23.7, 23.8 and 25.2).
+inline uint32_t rows_blocks(uint32_t per_row, uint32_t h) {
+  const uint32_t blocks = per_row / h;
+  return blocks > 256 ? blocks < 4096 ? blocks : 4096 : 256;
 }
 
-template <int NT>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
-  v = wave_max(v);
-  if constexpr (NT > 64) {
-    constexpr int kWaves = NT / 64;
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = v;
-    __syncthreads();
-    v = 0;
+// The wave's own barrier: LDS alone. A fence would also wait for the loads of
+// the next row.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(kWaitLds);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+  auto from = [](double x, auto f) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint64_t lo = f(static_cast<uint32_t>(b)), hi = f(static_cast<uint32_t>(b >> 32));
+    return __builtin_bit_cast(double, lo | hi << 32);
+  };
+  v += from(v, [](uint32_t x) { return dpp<kDppSwap1>(x); });
+  v += from(v, [](uint32_t x) { return dpp<kDppSwap2>(x); });
+  v += from(v, [](uint32_t x) { return dpp<kDppHalfMirror>(x); });
+  v += from(v, [](uint32_t x) { return dpp<kDppMirror>(x); });
+  double row[4];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v = max(v, part[w]);
-  }
-  return v;
+  for (int i = 0; i < 4; ++i) row[i] = from(v, [i](uint32_t x) { return lane_value(x, 16 * i); });
+  return (row[0] + row[1]) + (row[2] + row[3]);
 }
 
 // Codes of one row held as P pieces per lane, piece p at column
 // (p * NT + lane) * 8.
 template <int XF, int SL, int NT, int P, bool VEC>
 __device__ __forceinline__ void quantize_row(float (*v)[kPiece], const RowsLaunch& a, uint64_t row, int lane,
-                                             uint32_t* part) {
+                                             uint32_t amax) {
   uint8_t* codes_row = static_cast<uint8_t*>(a.codes) + row * a.codes_stride;
   if constexpr (SL == kScaleF32Row) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[p][j]));
-    amax = block_max<NT>(amax, part);
     float scale;
     const float mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
 #pragma unroll
@@ -86,99 +143,146 @@ __device__ __forceinline__ void quantize_row(float (*v)[kPiece], const RowsLaunc
 }
 
 // NORM: the residual sum and norm in front of the codes; otherwise x itself
-// is quantized. NT = 64 takes a row per wave and four rows per work-group;
-// larger NT a row per work-group.
-template <int IO, int SL, int NT, int P, bool VEC, bool NORM>
-__global__ __launch_bounds__(NT == 64 ? 256 : NT) void rows_kernel(const RowsLaunch a) {
-  __shared__ float sum_part[NT / 64];
-  __shared__ uint32_t max_part[NT / 64];
-  const int lane = NT == 64 ? threadIdx.x % 64 : threadIdx.x;
-  const uint64_t row = NT == 64 ? static_cast<uint64_t>(blockIdx.x) * 4 + threadIdx.x / 64 : blockIdx.x;
-  if (NT == 64 && row >= a.rows) return;  // whole waves; no barrier below for NT = 64
+// is quantized. Work-group b takes rows b, b + gridDim, ...; the next row's
+// operands are under way while a row is reduced and written.
+//
+// The sum of squares, r and y are taken in binary64 and y rounded once to
+// binary32: codes next to a border between two then fall on the side of the
+// exact value (in binary32, a few in 10^7 do not), and no sum of squares
+// overflows. It costs 3 us of vector time where the memory takes 19.
+template <int IO, int SL, int NT, int P, bool VEC, bool NORM, bool STREAM>
+__global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
+  constexpr int kWaves = NT / 64;
+  __shared__ double sum_part[2][kWaves];
+  __shared__ uint32_t max_part[2][kWaves];
+  const int lane = threadIdx.x;
   constexpr int kSize = kOutSize<IO>;
-  const char* x_row = static_cast<const char*>(a.x) + row * a.x_stride * kSize;
-
-  float v[P][kPiece];
+  typedef RawPiece<IO, VEC> Raw;
+  struct Operands {
+    Raw x[P], r[NORM ? P : 1];
+  };
+  Operands next;
+  Raw w[NORM ? P : 1];
+  const bool add = NORM && a.residual != nullptr;
+  auto load_row = [&](uint64_t row) {
+    const char* x_row = static_cast<const char*>(a.x) + row * a.x_stride * kSize;
 #pragma unroll
-  for (int p = 0; p < P; ++p) load_piece<IO, VEC>(x_row, (p * NT + lane) * kPiece, a.h, v[p]);
-
-  if constexpr (NORM) {
-    if (a.residual != nullptr) {
+    for (int p = 0; p < P; ++p) next.x[p].template load<STREAM>(x_row, (p * NT + lane) * kPiece, a.h);
+    if (add) {
       const char* r_row = static_cast<const char*>(a.residual) + row * a.residual_stride * kSize;
-      char* s_row = static_cast<char*>(a.sum) + row * a.sum_stride * kSize;
-      float r[P][kPiece];
 #pragma unroll
-      for (int p = 0; p < P; ++p) load_piece<IO, VEC>(r_row, (p * NT + lane) * kPiece, a.h, r[p]);
+      for (int p = 0; p < P; ++p) next.r[p].template load<STREAM>(r_row, (p * NT + lane) * kPiece, a.h);
+    }
+  };
+  constexpr bool kAhead = P <= 4;  // wider rows leave no registers for a second one
+  if (kAhead) load_row(blockIdx.x);
+  if constexpr (NORM) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) w[p].template load<false>(a.weight, (p * NT + lane) * kPiece, a.h);
+  }
+
+  // The parts of the reductions alternate between two halves: a wave that is
+  // a row ahead writes the other half, and the next barrier keeps it from
+  // going further.
+  int turn = 0;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    if (!kAhead) load_row(row);
+    const Operands now = next;
+    if (kAhead && row + gridDim.x < a.rows) load_row(row + gridDim.x);
+    float v[P][kPiece];
+#pragma unroll
+    for (int p = 0; p < P; ++p) now.x[p].get(v[p]);
+    if constexpr (NORM) {
+      if (add) {
+        char* s_row = static_cast<char*>(a.sum) + row * a.sum_stride * kSize;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float r[kPiece];
+          now.r[p].get(r);
+#pragma unroll
+          for (int j = 0; j < kPiece; ++j) v[p][j] = round_to<IO>(v[p][j] + r[j]);
+          store_piece<IO, VEC>(s_row, (p * NT + lane) * kPiece, a.h, v[p]);
+        }
+      }
+      double ss = 0.0;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          const double s = v[p][j];
+          ss = __builtin_fma(s, s, ss);
+        }
+      ss = wave_sum(ss);
+      if (lane % 64 == 0) sum_part[turn][lane / 64] = ss;
+      lds_barrier();
+      ss = 0.0;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) ss += sum_part[turn][i];
+      // The hardware's estimate (about 2^-24) and one Newton step.
+      const double m = ss * a.inv_h + static_cast<double>(a.eps);
+      const double q = __builtin_amdgcn_rsq(m);
+      const double r = __builtin_isinf(m) ? 0.0 : q * __builtin_fma(-0.5 * m * q, q, 1.5);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
+        float wv[kPiece];
+        w[p].get(wv);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) v[p][j] = round_to<IO>(v[p][j] + r[p][j]);
-        store_piece<IO, VEC>(s_row, (p * NT + lane) * kPiece, a.h, v[p]);
+        for (int j = 0; j < kPiece; ++j)
+          v[p][j] = static_cast<float>(static_cast<double>(v[p][j]) * r * static_cast<double>(wv[j]));
       }
     }
-    float ss = 0.0f;
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int j = 0; j < kPiece; ++j) ss += v[p][j] * v[p][j];
-    ss = block_sum<NT>(ss, sum_part);
-    const float rstd = 1.0f / __builtin_sqrtf(ss / static_cast<float>(a.h) + a.eps);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float w[kPiece];
-      load_piece<IO, VEC>(a.weight, (p * NT + lane) * kPiece, a.h, w);
-#pragma unroll
-      for (int j = 0; j < kPiece; ++j) v[p][j] = v[p][j] * rstd * w[j];
-    }
-  }
 
-  if (a.x_format == kXE4M3FN) {
-    quantize_row<kXE4M3FN, SL, NT, P, VEC>(v, a, row, lane, max_part);
-  } else if (a.x_format == kXE5M2) {
-    quantize_row<kXE5M2, SL, NT, P, VEC>(v, a, row, lane, max_part);
-  } else if constexpr (SL != kScaleE8M0Block32) {
-    quantize_row<kXInt8, SL, NT, P, VEC>(v, a, row, lane, max_part);
+    uint32_t amax = 0;
+    if constexpr (SL == kScaleF32Row) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[p][j]));
+      amax = wave_max(amax);
+      if (lane % 64 == 0) max_part[turn][lane / 64] = amax;
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) amax = max(amax, max_part[turn][i]);
+    }
+    if (a.x_format == kXE4M3FN) {
+      quantize_row<kXE4M3FN, SL, NT, P, VEC>(v, a, row, lane, amax);
+    } else if (a.x_format == kXE5M2) {
+      quantize_row<kXE5M2, SL, NT, P, VEC>(v, a, row, lane, amax);
+    } else if constexpr (SL != kScaleE8M0Block32) {
+      quantize_row<kXInt8, SL, NT, P, VEC>(v, a, row, lane, amax);
+    }
   }
 }
 
-// A HIP grid holds fewer than 2^32 work-items: at most 2^20 rows (2^30
-// lanes) a launch.
-constexpr uint64_t kMaxLaunchRows = uint64_t{1} << 20;
-
-template <int IO, int SL, int NT, int P, bool VEC, bool NORM>
+template <int IO, int SL, int NT, int P, bool VEC, bool NORM, bool STREAM>
 hipError_t launch_rows_as(const RowsLaunch& l, hipStream_t stream) {
-  constexpr uint64_t per_block = NT == 64 ? 4 : 1;
-  constexpr uint64_t size = kOutSize<IO>;
-  const uint64_t scales_per_row = SL == kScaleF32Row ? 1 : l.h / (SL == kScaleF32Group128 ? 128 : 32);
-  for (uint64_t r0 = 0; r0 < l.rows; r0 += kMaxLaunchRows) {
-    RowsLaunch q = l;
-    q.rows = l.rows - r0 < kMaxLaunchRows ? l.rows - r0 : kMaxLaunchRows;
-    q.x = static_cast<const char*>(l.x) + r0 * l.x_stride * size;
-    if (l.residual) {
-      q.residual = static_cast<const char*>(l.residual) + r0 * l.residual_stride * size;
-      q.sum = static_cast<char*>(l.sum) + r0 * l.sum_stride * size;
-    }
-    q.codes = static_cast<char*>(l.codes) + r0 * l.codes_stride;
-    q.scales = static_cast<char*>(l.scales) + r0 * scales_per_row * (SL == kScaleE8M0Block32 ? 1 : 4);
-    const hipError_t e =
-        launch_kernel(rows_kernel<IO, SL, NT, P, VEC, NORM>, dim3(static_cast<uint32_t>((q.rows + per_block - 1) / per_block)),
-                      dim3(NT == 64 ? 256 : NT), stream, q);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  const uint32_t blocks = rows_blocks(1u << 22, l.h);
+  return launch_kernel(rows_kernel<IO, SL, NT, P, VEC, NORM, STREAM>,
+                       dim3(static_cast<uint32_t>(l.rows < blocks ? l.rows : blocks)), dim3(NT), stream, l);
 }
 
-// The smallest shape that holds a row.
-template <int IO, int SL, bool VEC, bool NORM>
+// The smallest shape that holds a row; rows off 16-byte boundaries have two.
+template <int IO, int SL, bool VEC, bool NORM, bool STREAM>
 hipError_t launch_rows_sized(const RowsLaunch& l, hipStream_t stream) {
-  if (l.h <= 256 * 4 * kPiece) return launch_rows_as<IO, SL, 256, 4, VEC, NORM>(l, stream);
-  if (l.h <= 1024 * 8 * kPiece) return launch_rows_as<IO, SL, 1024, 8, VEC, NORM>(l, stream);
+  if constexpr (VEC) {
+    if (l.h <= 256 * 1 * kPiece) return launch_rows_as<IO, SL, 256, 1, VEC, NORM, STREAM>(l, stream);
+    if (l.h <= 512 * 1 * kPiece) return launch_rows_as<IO, SL, 512, 1, VEC, NORM, STREAM>(l, stream);
+  }
+  if (l.h <= 512 * 2 * kPiece) return launch_rows_as<IO, SL, 512, 2, VEC, NORM, STREAM>(l, stream);
+  if constexpr (VEC) {
+    if (l.h <= 1024 * 2 * kPiece) return launch_rows_as<IO, SL, 1024, 2, VEC, NORM, STREAM>(l, stream);
+    if (l.h <= 1024 * 4 * kPiece) return launch_rows_as<IO, SL, 1024, 4, VEC, NORM, STREAM>(l, stream);
+  }
+  if (l.h <= 1024 * 8 * kPiece) return launch_rows_as<IO, SL, 1024, 8, VEC, NORM, STREAM>(l, stream);
   return hipErrorInvalidValue;
 }
 
 template <int IO, int SL, bool NORM>
 hipError_t launch_rows_typed(const RowsLaunch& l, hipStream_t stream) {
-  return l.vec ? launch_rows_sized<IO, SL, true, NORM>(l, stream) : launch_rows_sized<IO, SL, false, NORM>(l, stream);
+  if (!l.vec) return launch_rows_sized<IO, SL, false, NORM, false>(l, stream);
+  const uint64_t bytes = l.rows * l.h * (kOutSize<IO> * (NORM ? 3 : 1) + 1);
+  return bytes > kStreamBytes ? launch_rows_sized<IO, SL, true, NORM, true>(l, stream)
+                              : launch_rows_sized<IO, SL, true, NORM, false>(l, stream);
 }
 
 template <int IO>
@@ -198,37 +302,59 @@ hipError_t launch_rows_io(const RowsLaunch& l, hipStream_t stream) {
 //   grad_x      = grad_sum + r * (d - s * (r^2 * mean(d * s)))
 //   grad_weight = sum over tokens of grad_y * s * r
 // Both row sums (s^2 and d * s) are taken in one reduction. Work-group b
-// takes rows b, b + gridDim, ... and keeps its columns' share of grad_weight
-// in registers; it leaves one row of partial sums in the workspace, and
+// takes rows b, b + gridDim, ...; the next row's operands are under way while
+// a row is reduced and written. It keeps its columns' share of grad_weight in
+// registers and leaves one row of partial sums in the workspace, and
 // grad_weight_kernel adds those rows in order: a fixed order without atomics.
-template <int IO, int NT, int P, bool VEC>
+template <int IO, int NT, int P, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLaunch a) {
   __shared__ float parts[2][2 * (NT / 64)];
   const int lane = threadIdx.x;
   constexpr int kSize = kOutSize<IO>;
+  typedef RawPiece<IO, VEC> Raw;
   float dw[P][kPiece];
+  Raw w[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int p = 0; p < P; ++p) {
+    w[p].template load<false>(a.weight, (p * NT + lane) * kPiece, a.h);
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) dw[p][j] = 0.0f;
-
-  int turn = 0;
-  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+  }
+  struct Operands {
+    Raw dy[P], s[P], g[P];
+  };
+  Operands next;
+  auto load_row = [&](uint64_t row) {
     const char* dy_row = static_cast<const char*>(a.grad_y) + row * a.grad_y_stride * kSize;
     const char* s_row = static_cast<const char*>(a.sum) + row * a.sum_stride * kSize;
-    float dy[P][kPiece], s[P][kPiece];
-    float ss = 0.0f, ds = 0.0f;
+    // Without a grad_sum, s stands in and is taken as zero below.
+    const char* g_row = a.grad_sum != nullptr ? static_cast<const char*>(a.grad_sum) + row * a.grad_sum_stride * kSize : s_row;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t c = (p * NT + lane) * kPiece;
-      float w[kPiece];
-      load_piece<IO, VEC>(dy_row, c, a.h, dy[p]);
-      load_piece<IO, VEC>(s_row, c, a.h, s[p]);
-      load_piece<IO, VEC>(a.weight, c, a.h, w);
+      next.dy[p].template load<STREAM>(dy_row, c, a.h);
+      next.s[p].template load<STREAM>(s_row, c, a.h);
+      next.g[p].template load<STREAM>(g_row, c, a.h);
+    }
+  };
+
+  load_row(blockIdx.x);
+  const float keep = a.grad_sum != nullptr ? 1.0f : 0.0f;
+  int turn = 0;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const Operands now = next;
+    if (row + gridDim.x < a.rows) load_row(row + gridDim.x);
+    float ss = 0.0f, ds = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float wv[kPiece], dy[kPiece], s[kPiece];
+      w[p].get(wv);
+      now.dy[p].get(dy);
+      now.s[p].get(s);
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) {
-        ss += s[p][j] * s[p][j];
-        ds += w[j] * dy[p][j] * s[p][j];
+        ss += s[j] * s[j];
+        ds += wv[j] * dy[j] * s[j];
       }
     }
     // Alternating halves of `parts`: a wave that is a row ahead writes the
@@ -240,12 +366,12 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
       parts[turn][lane / 64] = ss;
       parts[turn][kWaves + lane / 64] = ds;
     }
-    __syncthreads();
+    lds_barrier();
     ss = ds = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      ss += parts[turn][w];
-      ds += parts[turn][kWaves + w];
+    for (int i = 0; i < kWaves; ++i) {
+      ss += parts[turn][i];
+      ds += parts[turn][kWaves + i];
     }
     const float n = static_cast<float>(a.h);
     const float r = 1.0f / __builtin_sqrtf(ss / n + a.eps);
@@ -253,18 +379,15 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t c = (p * NT + lane) * kPiece;
-      float w[kPiece], g[kPiece];
-      load_piece<IO, VEC>(a.weight, c, a.h, w);
-      if (a.grad_sum != nullptr) {
-        load_piece<IO, VEC>(static_cast<const char*>(a.grad_sum) + row * a.grad_sum_stride * kSize, c, a.h, g);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPiece; ++j) g[j] = 0.0f;
-      }
+      float wv[kPiece], dy[kPiece], s[kPiece], g[kPiece];
+      w[p].get(wv);
+      now.dy[p].get(dy);
+      now.s[p].get(s);
+      now.g[p].get(g);
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) {
-        dw[p][j] += dy[p][j] * (s[p][j] * r);
-        g[j] += r * (w[j] * dy[p][j] - s[p][j] * along);
+        dw[p][j] += dy[j] * (s[j] * r);
+        g[j] = (keep != 0.0f ? g[j] : 0.0f) + r * (wv[j] * dy[j] - s[j] * along);
       }
       store_piece<IO, VEC>(static_cast<char*>(a.grad_x) + row * a.grad_x_stride * kSize, c, a.h, g);
     }
@@ -273,51 +396,68 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const uint32_t c = (p * NT + lane) * kPiece;
+    if (VEC && c < a.h) {
+      *reinterpret_cast<f32x4*>(part_row + c) = f32x4{dw[p][0], dw[p][1], dw[p][2], dw[p][3]};
+      *reinterpret_cast<f32x4*>(part_row + c + 4) = f32x4{dw[p][4], dw[p][5], dw[p][6], dw[p][7]};
+    } else {
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j)
-      if (c + j < a.h) part_row[c + j] = dw[p][j];
+      for (int j = 0; j < kPiece; ++j)
+        if (c + j < a.h) part_row[c + j] = dw[p][j];
+    }
   }
 }
 
-// grad_weight[c] = sum over the n_parts rows of the workspace: 64 columns a
-// work-group, its 16 waves taking every 16th row.
+// grad_weight[c] = sum over the n_parts rows of the workspace: 32 columns (a
+// line of each row) a work-group, its 32 half waves taking every 32nd row.
 __global__ __launch_bounds__(1024) void grad_weight_kernel(const float* parts, float* grad_weight, uint32_t n_parts,
                                                            uint32_t h) {
-  __shared__ float part[16][64];
-  const uint32_t c = blockIdx.x * 64 + threadIdx.x % 64;
-  const uint32_t w = threadIdx.x / 64;
+  __shared__ float part[32][33];
+  const uint32_t col = threadIdx.x % 32, c = blockIdx.x * 32 + col, w = threadIdx.x / 32;
   float v = 0.0f;
-  if (c < h)
-    for (uint32_t i = w; i < n_parts; i += 16) v += parts[static_cast<uint64_t>(i) * h + c];
-  part[w][threadIdx.x % 64] = v;
+  if (c < h) {
+#pragma unroll 4
+    for (uint32_t i = w; i < n_parts; i += 32) v += parts[static_cast<uint64_t>(i) * h + c];
+  }
+  part[w][col] = v;
   __syncthreads();
   if (w == 0 && c < h) {
     v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) v += part[i][col];
     grad_weight[c] = v;
   }
 }
 
-template <int IO, int NT, int P, bool VEC>
+template <int IO, int NT, int P, bool VEC, bool STREAM>
 hipError_t launch_backward_as(const NormBackwardLaunch& l, hipStream_t stream) {
-  const uint32_t parts = norm_backward_parts(l.rows);
-  const hipError_t e = launch_kernel(norm_backward_kernel<IO, NT, P, VEC>, dim3(parts), dim3(NT), stream, l);
+  const uint32_t parts = norm_backward_parts(l.rows, l.h);
+  const hipError_t e = launch_kernel(norm_backward_kernel<IO, NT, P, VEC, STREAM>, dim3(parts), dim3(NT), stream, l);
   if (e != hipSuccess) return e;
-  return launch_kernel(grad_weight_kernel, dim3((l.h + 63) / 64), dim3(1024), stream,
+  return launch_kernel(grad_weight_kernel, dim3((l.h + 31) / 32), dim3(1024), stream,
                        static_cast<const float*>(l.workspace), l.grad_weight, parts, l.h);
 }
 
-template <int IO, bool VEC>
+template <int IO, bool VEC, bool STREAM>
 hipError_t launch_backward_sized(const NormBackwardLaunch& l, hipStream_t stream) {
-  if (l.h <= 256 * 4 * kPiece) return launch_backward_as<IO, 256, 4, VEC>(l, stream);
-  if (l.h <= 1024 * 8 * kPiece) return launch_backward_as<IO, 1024, 8, VEC>(l, stream);
+  // The smallest shape that holds a row, as above. (1024 lanes leave 128
+  // registers a lane: rows past 16384 elements keep part of theirs in scratch
+  // memory.)
+  if constexpr (VEC) {
+    if (l.h <= 256 * 1 * kPiece) return launch_backward_as<IO, 256, 1, VEC, STREAM>(l, stream);
+    if (l.h <= 256 * 2 * kPiece) return launch_backward_as<IO, 256, 2, VEC, STREAM>(l, stream);
+  }
+  if (l.h <= 256 * 4 * kPiece) return launch_backward_as<IO, 256, 4, VEC, STREAM>(l, stream);
+  if constexpr (VEC)
+    if (l.h <= 1024 * 2 * kPiece) return launch_backward_as<IO, 1024, 2, VEC, STREAM>(l, stream);
+  if (l.h <= 1024 * 8 * kPiece) return launch_backward_as<IO, 1024, 8, VEC, STREAM>(l, stream);
   return hipErrorInvalidValue;
 }
 
 template <int IO>
 hipError_t launch_backward_io(const NormBackwardLaunch& l, hipStream_t stream) {
-  return l.vec ? launch_backward_sized<IO, true>(l, stream) : launch_backward_sized<IO, false>(l, stream);
+  if (!l.vec) return launch_backward_sized<IO, false, false>(l, stream);
+  return l.rows * l.h * kOutSize<IO> * 4 > kStreamBytes ? launch_backward_sized<IO, true, true>(l, stream)
+                                                        : launch_backward_sized<IO, true, false>(l, stream);
 }
 
 }  // namespace
@@ -329,6 +469,14 @@ hipError_t launch_rows(const RowsLaunch& l, hipStream_t stream) {
     case kOutF16: return launch_rows_io<kOutF16>(l, stream);
   }
   return hipErrorInvalidValue;
+}
+
+uint32_t norm_backward_parts(uint64_t rows, uint32_t h) {
+  // Fewer than for the forward pass: each leaves a row of partial sums
+  // (16384 x 8192 bf16: 256 work-groups 196 us, 512 207, 1024 214; 4096 x
+  // 4096 f16: 256 35.0 us, 512 32.3, 1024 35.5).
+  const uint32_t parts = rows_blocks(1u << 21, h);
+  return static_cast<uint32_t>(rows < parts ? rows : parts);
 }
 
 hipError_t launch_norm_backward(const NormBackwardLaunch& l, hipStream_t stream) {
