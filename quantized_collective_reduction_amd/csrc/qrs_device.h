@@ -29,6 +29,10 @@ constexpr int kPiece = 8;  // consecutive elements a lane owns
 template <int OF>
 constexpr int kOutSize = OF == kOutF32 ? 4 : 2;
 
+// The piece that is one 16-byte load or store.
+template <int OF>
+constexpr int kPiece16 = 16 / kOutSize<OF>;
+
 // Two floats -> one word of the 16-bit type, nearest-even.
 template <int OF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -75,66 +79,83 @@ __device__ __forceinline__ void store1(void* row, uint32_t c, float v) {
     static_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(pack2<OF>(v, 0.0f));
 }
 
-// Elements [c, c + 8) of a row, zeros from column h on. VEC: the row starts
+// Elements [c, c + E) of a row, zeros from column h on. VEC: the row starts
 // on a 16-byte boundary and h is a multiple of 8, so a piece is whole.
-template <int OF, bool VEC>
+template <int OF, bool VEC, int E>
 __device__ __forceinline__ void load_piece(const void* row, uint32_t c, uint32_t h, float* v) {
   if constexpr (VEC) {
     if (c < h) {
       if constexpr (OF == kOutF32) {
-        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
-        const f32x4 a = p[0], b = p[1];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = a[j];
-          v[4 + j] = b[j];
+        for (int i = 0; i < E; i += 4) {
+          const f32x4 a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c + i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i + j] = a[j];
         }
       } else {
+        static_assert(E == 8, "one 16-byte load");
         const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) unpack2<OF>(w[j], v + 2 * j);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) v[j] = 0.0f;
+      for (int j = 0; j < E; ++j) v[j] = 0.0f;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) v[j] = c + j < h ? load1<OF>(row, c + j) : 0.0f;
+    for (int j = 0; j < E; ++j) v[j] = c + j < h ? load1<OF>(row, c + j) : 0.0f;
   }
 }
 
-// 16-bit pieces are stored past the caches (norm of 2048 x 8192 bf16: 27.0 us
-// through them, 26.3 past them); a binary32 piece is two stores of half lines,
-// which the caches have to join (8192 x 5120 f32: 101 us, past them 112).
-template <int OF, bool VEC>
+// One 16-byte store is made past the caches (norm of 2048 x 8192 bf16: 27.0 us
+// through them, 26.3 past them); two of a lane (8 binary32 elements) cover
+// half lines each, which the caches have to join (8192 x 5120 f32: 101 us, past
+// them 112).
+template <int OF, bool VEC, int E>
 __device__ __forceinline__ void store_piece(void* row, uint32_t c, uint32_t h, const float* v) {
   if constexpr (VEC) {
     if (c < h) {
       if constexpr (OF == kOutF32) {
         f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(row) + c);
-        p[0] = f32x4{v[0], v[1], v[2], v[3]};
-        p[1] = f32x4{v[4], v[5], v[6], v[7]};
+        if constexpr (E == 4) {
+          __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, p);
+        } else {
+          p[0] = f32x4{v[0], v[1], v[2], v[3]};
+          p[1] = f32x4{v[4], v[5], v[6], v[7]};
+        }
       } else {
+        static_assert(E == 8, "one 16-byte store");
         const u32x4 w = {pack2<OF>(v[0], v[1]), pack2<OF>(v[2], v[3]), pack2<OF>(v[4], v[5]), pack2<OF>(v[6], v[7])};
         __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(row) + c));
       }
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j)
+    for (int j = 0; j < E; ++j)
       if (c + j < h) store1<OF>(row, c + j, v[j]);
   }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t c, uint32_t h, u32x2 w) {
+// E codes, four a word.
+template <int E>
+struct Codes {
+  uint32_t w[E / 4];
+};
+
+template <bool VEC, int E>
+__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t c, uint32_t h, const Codes<E>& codes) {
   if constexpr (VEC) {
-    if (c < h) *reinterpret_cast<u32x2*>(row + c) = w;
+    if (c < h) {
+      if constexpr (E == 8)
+        *reinterpret_cast<u32x2*>(row + c) = u32x2{codes.w[0], codes.w[1]};
+      else
+        *reinterpret_cast<uint32_t*>(row + c) = codes.w[0];
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j)
-      if (c + j < h) row[c + j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
+    for (int j = 0; j < E; ++j)
+      if (c + j < h) row[c + j] = static_cast<uint8_t>(codes.w[j / 4] >> (8 * (j % 4)));
   }
 }
 
@@ -154,16 +175,18 @@ __device__ __forceinline__ float dpp(float v) {
 // across the half row and the row of 16.
 constexpr int kDppSwap1 = 0xB1, kDppSwap2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
 
-// Largest v of each aligned group of L consecutive lanes (4 or 16), in every
-// lane of it. v holds the bits of a non-negative float, which order as
+// Largest v of each aligned group of L consecutive lanes (4, 8, 16 or 32), in
+// every lane of it. v holds the bits of a non-negative float, which order as
 // integers do; NaN is above infinity, so it wins.
 template <int L>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   v = max(v, dpp<kDppSwap1>(v));
   v = max(v, dpp<kDppSwap2>(v));
-  if constexpr (L == 16) {
-    v = max(v, dpp<kDppHalfMirror>(v));
-    v = max(v, dpp<kDppMirror>(v));
+  if constexpr (L >= 8) v = max(v, dpp<kDppHalfMirror>(v));
+  if constexpr (L >= 16) v = max(v, dpp<kDppMirror>(v));
+  if constexpr (L >= 32) {
+    constexpr int kXor16 = 0x401F;  // lane i <-> i ^ 16 of each half wave
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(v), kXor16)));
   }
   return v;
 }
@@ -235,55 +258,54 @@ __device__ __forceinline__ float mx_multiplier(uint32_t amax_bits, uint32_t* cod
   return exp2_int(-shared);
 }
 
-// Eight values times mul, clamped and rounded nearest-even to codes.
-template <int XF>
-__device__ __forceinline__ u32x2 encode_piece(const float* v, float mul) {
+// E values times mul, clamped and rounded nearest-even to codes.
+template <int XF, int E = kPiece>
+__device__ __forceinline__ Codes<E> encode_piece(const float* v, float mul) {
   constexpr float kMax = CodeFormat<XF>::kMax;
-  float q[kPiece];
+  float q[E];
 #pragma unroll
-  for (int j = 0; j < kPiece; ++j) q[j] = fminf(fmaxf(v[j] * mul, -kMax), kMax);
-  u32x2 w;
+  for (int j = 0; j < E; ++j) q[j] = fminf(fmaxf(v[j] * mul, -kMax), kMax);
+  Codes<E> codes;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < E / 4; ++k) {
     const float* p = q + 4 * k;
     if constexpr (XF == kXInt8) {
       uint32_t b[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         b[j] = static_cast<uint32_t>(static_cast<int32_t>(__builtin_rintf(p[j]))) & 0xFFu;
-      w[k] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+      codes.w[k] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
     } else if constexpr (XF == kXE4M3FN) {
       int t = __builtin_amdgcn_cvt_pk_fp8_f32(p[0], p[1], 0, false);
-      w[k] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(p[2], p[3], t, true));
+      codes.w[k] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(p[2], p[3], t, true));
     } else {
       int t = __builtin_amdgcn_cvt_pk_bf8_f32(p[0], p[1], 0, false);
-      w[k] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(p[2], p[3], t, true));
+      codes.w[k] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(p[2], p[3], t, true));
     }
   }
-  return w;
+  return codes;
 }
 
 // One piece of a row in a group layout: codes, and the group's scale from
 // its first lane. Lanes of a group are consecutive and all take part; `c` is
 // the piece's first column and `active` whether it is inside the row.
-template <int XF, int SL, bool VEC>
+template <int XF, int SL, bool VEC, int E>
 __device__ __forceinline__ void quantize_group_piece(const float* v, bool active, uint32_t c, uint32_t h,
                                                      uint8_t* codes_row, void* scales, uint64_t first_scale) {
   constexpr int G = SL == kScaleF32Group128 ? 128 : 32;
-  constexpr int L = G / kPiece;
   uint32_t amax = 0;
 #pragma unroll
-  for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[j]));
-  amax = group_max<L>(amax);
+  for (int j = 0; j < E; ++j) amax = max(amax, abs_bits(v[j]));
+  amax = group_max<G / E>(amax);
   float mul, scale = 0.0f;
   uint32_t code = 0;
   if constexpr (SL == kScaleF32Group128)
     mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
   else
     mul = mx_multiplier<XF>(amax, &code);
-  const u32x2 w = encode_piece<XF>(v, mul);
+  const Codes<E> codes = encode_piece<XF, E>(v, mul);
   if (!active) return;
-  store_codes<VEC>(codes_row, c, h, w);
+  store_codes<VEC, E>(codes_row, c, h, codes);
   if (c % G == 0) {
     if constexpr (SL == kScaleF32Group128)
       static_cast<float*>(scales)[first_scale + c / G] = scale;

@@ -77,7 +77,7 @@ __device__ __forceinline__ PieceScales piece_scales(const MatmulLaunch& a, uint3
 // the mode chosen at run time: a kernel's epilogue repeats this for every
 // fragment, and a copy for each mode would be five times the code. `finite`:
 // the scales that v was multiplied by are, so that v holds no NaN.
-__device__ __forceinline__ u32x2 encode_group(const MatmulLaunch& a, const float* v, bool finite, uint32_t* scale_bits) {
+__device__ __forceinline__ Codes<kPiece> encode_group(const MatmulLaunch& a, const float* v, bool finite, uint32_t* scale_bits) {
   float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
 #pragma unroll
   for (int j = 2; j < kPiece; ++j) m = __builtin_fmaxf(m, __builtin_fabsf(v[j]));
@@ -105,9 +105,9 @@ __device__ __forceinline__ bool is_finite(float v) { return abs_bits(v) < 0x7F80
 __device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, bool finite,
                                              const float* v) {
   uint32_t scale;
-  const u32x2 w = encode_group(a, v, finite, &scale);
+  const Codes<kPiece> codes = encode_group(a, v, finite, &scale);
   if (!active) return;
-  *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.out) + static_cast<uint64_t>(i) * a.out_stride + j0) = w;
+  store_codes<true, kPiece>(static_cast<uint8_t*>(a.out) + static_cast<uint64_t>(i) * a.out_stride, j0, a.n, codes);
   if (a.scale_layout == kScaleE8M0Block32) {
     if (j0 % 32 == 0)
       static_cast<uint8_t*>(a.scales)[static_cast<uint64_t>(i) * (a.n / 32) + j0 / 32] = static_cast<uint8_t>(scale);
@@ -120,9 +120,9 @@ template <int OF>
 __device__ __forceinline__ void finish_values(const MatmulLaunch& a, uint32_t i, uint32_t j0, const float* v) {
   char* row = static_cast<char*>(a.out) + static_cast<uint64_t>(i) * a.out_stride * kOutSize<OF>;
   if (a.out_vec && j0 + kPiece <= a.n)
-    store_piece<OF, true>(row, j0, a.n, v);
+    store_piece<OF, true, kPiece>(row, j0, a.n, v);
   else
-    store_piece<OF, false>(row, j0, a.n, v);
+    store_piece<OF, false, kPiece>(row, j0, a.n, v);
 }
 
 // v: a piece's integer sums as binary32 times the token's scale sa (gated: of
@@ -365,7 +365,8 @@ struct TileOrder {
 // token i0 and channel j0 on; this lane's are of token i0 + row + t and
 // channels j0 + col .. + 7. A uniform base, a lane's offset and the token in a
 // scalar, so that no address is computed for a store. They go past the caches
-// (16384 x 8192 bf16 values: 404 -> 379 us; they fill L2 otherwise).
+// (16384 x 8192 bf16 values: 404 -> 379 us; they fill L2 otherwise), but for
+// binary32, two stores of half lines a piece.
 template <int F>
 struct WholeTile {
   static constexpr int kStream = 2;
@@ -395,8 +396,8 @@ struct WholeTile {
   __device__ __forceinline__ void store(const MatmulLaunch& a, uint32_t t, const float* v, bool finite) const {
     if constexpr (F == kCodes) {
       uint32_t scale;
-      const u32x2 w = encode_group(a, v, finite, &scale);
-      __builtin_amdgcn_raw_buffer_store_b64(w, out, out_lane, t * out_row, kStream);
+      const Codes<kPiece> codes = encode_group(a, v, finite, &scale);
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes.w[0], codes.w[1]}, out, out_lane, t * out_row, kStream);
       if (has_scale) {
         if (a.scale_layout == kScaleE8M0Block32)
           __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(scale), scales, scale_lane, t * scale_row, 0);
@@ -407,7 +408,7 @@ struct WholeTile {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const f32x4 w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), out, out_lane + 16 * h, t * out_row, kStream);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), out, out_lane + 16 * h, t * out_row, 0);
       }
     } else {
       const bool bf = a.out_format == kOutBF16;

@@ -29,19 +29,19 @@ using namespace dev;
 // s_waitcnt for LDS and scalar loads alone (lgkmcnt 0, vmcnt and expcnt at most).
 constexpr int kWaitLds = 0xC07F;
 
-// A piece as it lies in memory (VEC), so that rows under way cost half the
+// A piece (16 bytes) as it lies in memory (VEC), so that rows under way cost half the
 // registers for 16-bit types; otherwise as floats. STREAM: loads that leave no
 // copy in the caches.
 template <int IO, bool VEC>
 struct RawPiece {
-  float v[kPiece];
+  float v[kPiece16<IO>];
   template <bool STREAM>
   __device__ __forceinline__ void load(const void* row, uint32_t c, uint32_t h) {
-    load_piece<IO, VEC>(row, c, h, v);
+    load_piece<IO, VEC, kPiece16<IO>>(row, c, h, v);
   }
   __device__ __forceinline__ void get(float* to) const {
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) to[j] = v[j];
+    for (int j = 0; j < kPiece16<IO>; ++j) to[j] = v[j];
   }
 };
 template <int IO>
@@ -60,19 +60,16 @@ struct RawPiece16 {
 };
 template <>
 struct RawPiece<kOutF32, true> {
-  f32x4 w[2];
+  f32x4 w;
   template <bool STREAM>
   __device__ __forceinline__ void load(const void* row, uint32_t c, uint32_t h) {
     const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (c < h) w[i] = STREAM ? __builtin_nontemporal_load(p + i) : p[i];
-    }
+    w = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < h) w = STREAM ? __builtin_nontemporal_load(p) : *p;
   }
   __device__ __forceinline__ void get(float* to) const {
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) to[j] = w[j / 4][j % 4];
+    for (int j = 0; j < 4; ++j) to[j] = w[j];
   }
 };
 template <>
@@ -120,9 +117,9 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // Codes of one row held as P pieces per lane, piece p at column
-// (p * NT + lane) * 8.
-template <int XF, int SL, int NT, int P, bool VEC>
-__device__ __forceinline__ void quantize_row(float (*v)[kPiece], const RowsLaunch& a, uint64_t row, int lane,
+// (p * NT + lane) * E.
+template <int XF, int SL, int NT, int P, bool VEC, int E>
+__device__ __forceinline__ void quantize_row(float (*v)[E], const RowsLaunch& a, uint64_t row, int lane,
                                              uint32_t amax) {
   uint8_t* codes_row = static_cast<uint8_t*>(a.codes) + row * a.codes_stride;
   if constexpr (SL == kScaleF32Row) {
@@ -130,14 +127,14 @@ __device__ __forceinline__ void quantize_row(float (*v)[kPiece], const RowsLaunc
     const float mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      store_codes<VEC>(codes_row, (p * NT + lane) * kPiece, a.h, encode_piece<XF>(v[p], mul));
+      store_codes<VEC, E>(codes_row, (p * NT + lane) * E, a.h, encode_piece<XF, E>(v[p], mul));
     if (lane == 0) static_cast<float*>(a.scales)[row] = scale;
   } else {
     const uint64_t first = row * (a.h / (SL == kScaleF32Group128 ? 128 : 32));
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t c = (p * NT + lane) * kPiece;
-      quantize_group_piece<XF, SL, VEC>(v[p], c < a.h, c, a.h, codes_row, a.scales, first);
+      const uint32_t c = (p * NT + lane) * E;
+      quantize_group_piece<XF, SL, VEC, E>(v[p], c < a.h, c, a.h, codes_row, a.scales, first);
     }
   }
 }
@@ -150,8 +147,9 @@ __device__ __forceinline__ void quantize_row(float (*v)[kPiece], const RowsLaunc
 // binary32: codes next to a border between two then fall on the side of the
 // exact value (in binary32, a few in 10^7 do not), and no sum of squares
 // overflows. It costs 3 us of vector time where the memory takes 19.
-template <int IO, int SL, int NT, int P, bool VEC, bool NORM, bool STREAM>
+template <int IO, int SL, int NT, int P8, bool VEC, bool NORM, bool STREAM>
 __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
+  constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
   constexpr int kWaves = NT / 64;
   __shared__ double sum_part[2][kWaves];
   __shared__ uint32_t max_part[2][kWaves];
@@ -167,18 +165,18 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   auto load_row = [&](uint64_t row) {
     const char* x_row = static_cast<const char*>(a.x) + row * a.x_stride * kSize;
 #pragma unroll
-    for (int p = 0; p < P; ++p) next.x[p].template load<STREAM>(x_row, (p * NT + lane) * kPiece, a.h);
+    for (int p = 0; p < P; ++p) next.x[p].template load<STREAM>(x_row, (p * NT + lane) * E, a.h);
     if (add) {
       const char* r_row = static_cast<const char*>(a.residual) + row * a.residual_stride * kSize;
 #pragma unroll
-      for (int p = 0; p < P; ++p) next.r[p].template load<STREAM>(r_row, (p * NT + lane) * kPiece, a.h);
+      for (int p = 0; p < P; ++p) next.r[p].template load<STREAM>(r_row, (p * NT + lane) * E, a.h);
     }
   };
-  constexpr bool kAhead = P <= 4;  // wider rows leave no registers for a second one
+  constexpr bool kAhead = P8 <= 4;  // wider rows leave no registers for a second one
   if (kAhead) load_row(blockIdx.x);
   if constexpr (NORM) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) w[p].template load<false>(a.weight, (p * NT + lane) * kPiece, a.h);
+    for (int p = 0; p < P; ++p) w[p].template load<false>(a.weight, (p * NT + lane) * E, a.h);
   }
 
   // The parts of the reductions alternate between two halves: a wave that is
@@ -189,7 +187,7 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
     if (!kAhead) load_row(row);
     const Operands now = next;
     if (kAhead && row + gridDim.x < a.rows) load_row(row + gridDim.x);
-    float v[P][kPiece];
+    float v[P][E];
 #pragma unroll
     for (int p = 0; p < P; ++p) now.x[p].get(v[p]);
     if constexpr (NORM) {
@@ -197,18 +195,18 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
         char* s_row = static_cast<char*>(a.sum) + row * a.sum_stride * kSize;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          float r[kPiece];
+          float r[E];
           now.r[p].get(r);
 #pragma unroll
-          for (int j = 0; j < kPiece; ++j) v[p][j] = round_to<IO>(v[p][j] + r[j]);
-          store_piece<IO, VEC>(s_row, (p * NT + lane) * kPiece, a.h, v[p]);
+          for (int j = 0; j < E; ++j) v[p][j] = round_to<IO>(v[p][j] + r[j]);
+          store_piece<IO, VEC, E>(s_row, (p * NT + lane) * E, a.h, v[p]);
         }
       }
       double ss = 0.0;
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
+        for (int j = 0; j < E; ++j) {
           const double s = v[p][j];
           ss = __builtin_fma(s, s, ss);
         }
@@ -224,10 +222,10 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
       const double r = __builtin_isinf(m) ? 0.0 : q * __builtin_fma(-0.5 * m * q, q, 1.5);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        float wv[kPiece];
+        float wv[E];
         w[p].get(wv);
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j)
+        for (int j = 0; j < E; ++j)
           v[p][j] = static_cast<float>(static_cast<double>(v[p][j]) * r * static_cast<double>(wv[j]));
       }
     }
@@ -237,7 +235,7 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) amax = max(amax, abs_bits(v[p][j]));
+        for (int j = 0; j < E; ++j) amax = max(amax, abs_bits(v[p][j]));
       amax = wave_max(amax);
       if (lane % 64 == 0) max_part[turn][lane / 64] = amax;
       lds_barrier();
@@ -245,11 +243,11 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
       for (int i = 0; i < kWaves; ++i) amax = max(amax, max_part[turn][i]);
     }
     if (a.x_format == kXE4M3FN) {
-      quantize_row<kXE4M3FN, SL, NT, P, VEC>(v, a, row, lane, amax);
+      quantize_row<kXE4M3FN, SL, NT, P, VEC, E>(v, a, row, lane, amax);
     } else if (a.x_format == kXE5M2) {
-      quantize_row<kXE5M2, SL, NT, P, VEC>(v, a, row, lane, amax);
+      quantize_row<kXE5M2, SL, NT, P, VEC, E>(v, a, row, lane, amax);
     } else if constexpr (SL != kScaleE8M0Block32) {
-      quantize_row<kXInt8, SL, NT, P, VEC>(v, a, row, lane, amax);
+      quantize_row<kXInt8, SL, NT, P, VEC, E>(v, a, row, lane, amax);
     }
   }
 }
@@ -306,19 +304,20 @@ hipError_t launch_rows_io(const RowsLaunch& l, hipStream_t stream) {
 // a row is reduced and written. It keeps its columns' share of grad_weight in
 // registers and leaves one row of partial sums in the workspace, and
 // grad_weight_kernel adds those rows in order: a fixed order without atomics.
-template <int IO, int NT, int P, bool VEC, bool STREAM>
+template <int IO, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLaunch a) {
   __shared__ float parts[2][2 * (NT / 64)];
+  constexpr int E = kPiece16<IO>, P = P8 * 8 / E;
   const int lane = threadIdx.x;
   constexpr int kSize = kOutSize<IO>;
   typedef RawPiece<IO, VEC> Raw;
-  float dw[P][kPiece];
+  float dw[P][E];
   Raw w[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    w[p].template load<false>(a.weight, (p * NT + lane) * kPiece, a.h);
+    w[p].template load<false>(a.weight, (p * NT + lane) * E, a.h);
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) dw[p][j] = 0.0f;
+    for (int j = 0; j < E; ++j) dw[p][j] = 0.0f;
   }
   struct Operands {
     Raw dy[P], s[P], g[P];
@@ -331,7 +330,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     const char* g_row = a.grad_sum != nullptr ? static_cast<const char*>(a.grad_sum) + row * a.grad_sum_stride * kSize : s_row;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t c = (p * NT + lane) * kPiece;
+      const uint32_t c = (p * NT + lane) * E;
       next.dy[p].template load<STREAM>(dy_row, c, a.h);
       next.s[p].template load<STREAM>(s_row, c, a.h);
       next.g[p].template load<STREAM>(g_row, c, a.h);
@@ -347,12 +346,12 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     float ss = 0.0f, ds = 0.0f;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      float wv[kPiece], dy[kPiece], s[kPiece];
+      float wv[E], dy[E], s[E];
       w[p].get(wv);
       now.dy[p].get(dy);
       now.s[p].get(s);
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) {
+      for (int j = 0; j < E; ++j) {
         ss += s[j] * s[j];
         ds += wv[j] * dy[j] * s[j];
       }
@@ -378,30 +377,31 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     const float along = r * r * (ds / n);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const uint32_t c = (p * NT + lane) * kPiece;
-      float wv[kPiece], dy[kPiece], s[kPiece], g[kPiece];
+      const uint32_t c = (p * NT + lane) * E;
+      float wv[E], dy[E], s[E], g[E];
       w[p].get(wv);
       now.dy[p].get(dy);
       now.s[p].get(s);
       now.g[p].get(g);
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j) {
+      for (int j = 0; j < E; ++j) {
         dw[p][j] += dy[j] * (s[j] * r);
         g[j] = (keep != 0.0f ? g[j] : 0.0f) + r * (wv[j] * dy[j] - s[j] * along);
       }
-      store_piece<IO, VEC>(static_cast<char*>(a.grad_x) + row * a.grad_x_stride * kSize, c, a.h, g);
+      store_piece<IO, VEC, E>(static_cast<char*>(a.grad_x) + row * a.grad_x_stride * kSize, c, a.h, g);
     }
   }
   float* part_row = a.workspace + static_cast<uint64_t>(blockIdx.x) * a.h;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const uint32_t c = (p * NT + lane) * kPiece;
+    const uint32_t c = (p * NT + lane) * E;
     if (VEC && c < a.h) {
-      *reinterpret_cast<f32x4*>(part_row + c) = f32x4{dw[p][0], dw[p][1], dw[p][2], dw[p][3]};
-      *reinterpret_cast<f32x4*>(part_row + c + 4) = f32x4{dw[p][4], dw[p][5], dw[p][6], dw[p][7]};
+#pragma unroll
+      for (int j = 0; j < E; j += 4)
+        *reinterpret_cast<f32x4*>(part_row + c + j) = f32x4{dw[p][j], dw[p][j + 1], dw[p][j + 2], dw[p][j + 3]};
     } else {
 #pragma unroll
-      for (int j = 0; j < kPiece; ++j)
+      for (int j = 0; j < E; ++j)
         if (c + j < a.h) part_row[c + j] = dw[p][j];
     }
   }
