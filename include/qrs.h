@@ -403,15 +403,10 @@ qrs_status qrs_quantize_rows(int64_t rows, int64_t cols, qrs_out_dtype in_dtype,
  *              silu(g) = g / (1 + exp(-g)) in binary32.
  *   k          in [1, 131071]; m, n below 2^31.
  *   a_scales   float32 [m]; b_scales float32 [n], or [2n] if gated.
- *   workspace  DEVICE memory of at least qrs_matmul_int_workspace bytes (the
- *              same for both calls), 16-byte aligned, for this call alone
- *              until it ends; may be NULL where that size is 0.
  */
-qrs_status qrs_matmul_int_workspace(int64_t m, int64_t n, int64_t k, int gated, size_t* bytes_out);
 qrs_status qrs_matmul_int(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype, const void* a,
                           int64_t a_row_stride, const float* a_scales, const void* b, int64_t b_row_stride,
-                          const float* b_scales, void* out, int64_t out_row_stride, void* workspace,
-                          size_t workspace_bytes, void* stream);
+                          const float* b_scales, void* out, int64_t out_row_stride, void* stream);
 
 /*
  * The same product (not gated), quantized in binary32 by qrs_quantize's
@@ -423,8 +418,7 @@ qrs_status qrs_matmul_int(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dt
 qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype x_dtype,
                                    qrs_scale_layout scale_layout, const void* a, int64_t a_row_stride,
                                    const float* a_scales, const void* b, int64_t b_row_stride, const float* b_scales,
-                                   void* codes, int64_t codes_row_stride, void* scales, void* workspace,
-                                   size_t workspace_bytes, void* stream);
+                                   void* codes, int64_t codes_row_stride, void* scales, void* stream);
 
 /* Free a plan. NULL is accepted. Plans in use by queued runs may be freed:
  * qrs_run copies what the kernel needs into its launch arguments. */

@@ -22,6 +22,7 @@ What a layer computes between one share and the next, with 8-bit weights:
 """
 
 import ctypes
+import functools
 import os
 from enum import IntEnum
 
@@ -113,7 +114,6 @@ EXPORTED_SYMBOLS = (
     "qrs_quantize_rows",
     "qrs_matmul_int",
     "qrs_matmul_int_quantize",
-    "qrs_matmul_int_workspace",
 )
 
 
@@ -197,13 +197,10 @@ def load_library(path: str = LIB_PATH):
     lib.qrs_rms_norm_backward.restype = c_int
     lib.qrs_quantize_rows.argtypes = [c_i64, c_i64, c_int, c_int, vp, c_i64, vp, c_i64, vp, vp]
     lib.qrs_quantize_rows.restype = c_int
-    lib.qrs_matmul_int_workspace.argtypes = [c_i64, c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]
-    lib.qrs_matmul_int_workspace.restype = c_int
-    lib.qrs_matmul_int.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, vp, c_i64, vp, vp, c_i64, vp, vp, c_i64, vp,
-                                   c_sz, vp]
+    lib.qrs_matmul_int.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, vp, c_i64, vp, vp, c_i64, vp, vp, c_i64, vp]
     lib.qrs_matmul_int.restype = c_int
     lib.qrs_matmul_int_quantize.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, vp, c_i64, vp, vp, c_i64, vp, vp,
-                                            c_i64, vp, vp, c_sz, vp]
+                                            c_i64, vp, vp]
     lib.qrs_matmul_int_quantize.restype = c_int
     _lib = lib
     return lib
@@ -295,6 +292,7 @@ def alloc_slices(p: Plan, device="cuda", full_inputs=False):
     return xs, ss
 
 
+@functools.lru_cache(maxsize=None)
 def _element_dtypes():
     """torch element types of the codes, scales and outputs each mode names."""
     import torch
@@ -341,7 +339,8 @@ def _stream_handle(stream):
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream, without the Stream object (2.7 us -> 0.3 us a call).
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -612,13 +611,22 @@ class QuantizeLaunch:
 # ---- between two shares -----------------------------------------------------
 
 
-def _act_dtype(t, what):
+# The checks below run in front of kernels of a few microseconds: each tensor
+# attribute is read once, and messages are made only for refusals.
+
+
+@functools.lru_cache(maxsize=None)
+def _activation_types():
     import torch
 
-    kinds = {torch.float32: OutDtype.F32, torch.bfloat16: OutDtype.BF16, torch.float16: OutDtype.F16}
-    if t.dtype not in kinds:
+    return {torch.float32: int(OutDtype.F32), torch.bfloat16: int(OutDtype.BF16), torch.float16: int(OutDtype.F16)}
+
+
+def _act_dtype(t, what):
+    kind = _activation_types().get(t.dtype)
+    if kind is None:
         raise ValueError(f"{what}: float32, bfloat16 or float16 expected, got {t.dtype}")
-    return int(kinds[t.dtype])
+    return kind
 
 
 def _matrix(t, what, shape=None, dtype=None):
@@ -626,39 +634,44 @@ def _matrix(t, what, shape=None, dtype=None):
     adjacent, after checking its shape and element type."""
     if not t.is_cuda:
         raise ValueError(f"{what}: device tensors only (there is no CPU path)")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
+    got = t.shape
+    if len(got) != 2 or (shape is not None and got != shape):
         want = "two dimensions" if shape is None else f"shape {list(shape)}"
-        raise ValueError(f"{what}: expected {want}, got {list(t.shape)}")
+        raise ValueError(f"{what}: expected {want}, got {list(got)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    rows, cols = got
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}: elements within a row must be adjacent")
-    return t.stride(0) if rows > 1 else cols
+    return ld if rows > 1 else cols
 
 
 def _vector(t, what, n, dtype):
     if not t.is_cuda:
         raise ValueError(f"{what}: device tensors only (there is no CPU path)")
-    if t.numel() != n or not t.is_contiguous() or t.dtype != dtype:
+    if t.numel() != n or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous {dtype} elements expected, got {list(t.shape)} {t.dtype}")
 
 
-def _codes_and_scales(codes, scales, rows, h, xd, sl):
-    """Checks codes and scales of a mode; the codes' row stride."""
-    import torch
+_GROUP_OF = {ScaleLayout.F32_GROUP128: 128, ScaleLayout.E8M0_BLOCK32: 32}
 
+
+def _codes_and_scales(codes, scales, shape, xd, sl):
+    """Checks codes and scales of a mode; the codes' row stride."""
     x_dt, s_dt, _ = _element_dtypes()
-    ld = _matrix(codes, "codes", (rows, h))
+    ld = _matrix(codes, "codes", shape)
     if codes.element_size() != 1:
         raise ValueError(f"codes: 1-byte elements expected, got {codes.dtype}")
     _check_dtype(codes, x_dt.get(xd), "codes")
-    n = rows if sl == ScaleLayout.F32_ROW else rows * h // (128 if sl == ScaleLayout.F32_GROUP128 else 32)
+    rows, h = shape
+    n = rows if sl == ScaleLayout.F32_ROW else rows * h // _GROUP_OF.get(sl, 32)
     if sl == ScaleLayout.E8M0_BLOCK32:
         _check_tensor(scales, n, "scales")
         _check_dtype(scales, s_dt[sl], "scales")
+        _ptr(scales)
     else:
-        _vector(scales, "scales", n, torch.float32)
+        _vector(scales, "scales", n, s_dt[ScaleLayout.F32_GROUP128])
     return ld
 
 
@@ -669,8 +682,6 @@ def _workspace(workspace, nbytes, like, stream):
 
     if workspace is not None:
         return _ptr(workspace), workspace.numel() * workspace.element_size()
-    if nbytes == 0:
-        return None, 0
     ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     if stream is not None:
         ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
@@ -696,11 +707,11 @@ def add_rms_norm_quantize(x, residual, weight, eps, sum_out, codes, scales, x_dt
         ld_r = _matrix(residual, "residual", x.shape, x.dtype)
         ld_s = _matrix(sum_out, "sum_out", x.shape, x.dtype)
     xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
-    ld_c = _codes_and_scales(codes, scales, tokens, h, xd, sl)
+    ld_c = _codes_and_scales(codes, scales, x.shape, xd, sl)
     _check(lib.qrs_add_rms_norm_quantize(
         tokens, h, io, int(xd), int(sl), eps, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(),
         ld_r, weight.data_ptr(), None if residual is None else sum_out.data_ptr(), ld_s, codes.data_ptr(), ld_c,
-        _ptr(scales), _stream_handle(stream)))
+        scales.data_ptr(), _stream_handle(stream)))
 
 
 def rms_norm_backward(grad_y, sum, weight, eps, grad_sum, grad_x, grad_weight, workspace=None, stream=None):
@@ -740,56 +751,51 @@ def quantize_rows(x, codes, scales, x_dtype="int8", stream=None):
     ld_x = _matrix(x, "x")
     rows, cols = x.shape
     xd = _enum(x_dtype, _X_NAMES, XDtype)
-    ld_c = _codes_and_scales(codes, scales, rows, cols, xd, ScaleLayout.F32_ROW)
+    ld_c = _codes_and_scales(codes, scales, x.shape, xd, ScaleLayout.F32_ROW)
     _check(lib.qrs_quantize_rows(rows, cols, kind, int(xd), x.data_ptr(), ld_x, codes.data_ptr(), ld_c,
                                  scales.data_ptr(), _stream_handle(stream)))
 
 
-def _matmul_operands(lib, a, a_scales, b, b_scales, gated, workspace, stream):
+def _matmul_operands(a, a_scales, b, b_scales, gated):
     import torch
 
     ld_a = _matrix(a, "a", None, torch.int8)
     ld_b = _matrix(b, "b", None, torch.int8)
     m, k = a.shape
-    wide = b.shape[0]
-    if b.shape[1] != k or (gated and wide % 2):
+    wide, kb = b.shape
+    if kb != k or (gated and wide % 2):
         raise ValueError(f"b: expected [{'2 n' if gated else 'n'}, {k}], got {list(b.shape)}")
     _vector(a_scales, "a_scales", m, torch.float32)
     _vector(b_scales, "b_scales", wide, torch.float32)
-    n = wide // 2 if gated else wide
-    need = ctypes.c_size_t()
-    _check(lib.qrs_matmul_int_workspace(m, n, k, 1 if gated else 0, ctypes.byref(need)))
-    ws, nbytes = _workspace(workspace, need.value, a, stream)
-    return m, n, k, ld_a, ld_b, ws, nbytes
+    return m, wide // 2 if gated else wide, k, ld_a, ld_b
 
 
-def matmul_int8(a, a_scales, b, b_scales, out, gated=False, workspace=None, stream=None):
+def matmul_int8(a, a_scales, b, b_scales, out, gated=False, stream=None):
     """``out = (a @ b.T) * a_scales[:, None] * b_scales`` of int8 ``a [m, k]``
     (tokens) and ``b [n, k]`` (channels), float32 scales, summed exactly
     (qrs_matmul_int). ``out [m, n]``: float32, bfloat16 or float16.
 
     ``gated``: ``b`` is ``[2 n, k]``, n gate and then n up channels, and
-    ``out = silu(gate product) * up product``. ``workspace``: device memory of
-    qrs_matmul_int_workspace bytes, by default taken from torch's allocator."""
+    ``out = silu(gate product) * up product``."""
     lib = load_library()
-    m, n, k, ld_a, ld_b, ws, nbytes = _matmul_operands(lib, a, a_scales, b, b_scales, gated, workspace, stream)
+    m, n, k, ld_a, ld_b = _matmul_operands(a, a_scales, b, b_scales, gated)
     kind = _act_dtype(out, "out")
     ld_o = _matrix(out, "out", (m, n))
     _check(lib.qrs_matmul_int(m, n, k, 1 if gated else 0, kind, a.data_ptr(), ld_a, a_scales.data_ptr(), b.data_ptr(),
-                              ld_b, b_scales.data_ptr(), out.data_ptr(), ld_o, ws, nbytes, _stream_handle(stream)))
+                              ld_b, b_scales.data_ptr(), out.data_ptr(), ld_o, _stream_handle(stream)))
 
 
-def matmul_int8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_layout, workspace=None, stream=None):
+def matmul_int8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_layout, stream=None):
     """``matmul_int8``'s product, quantized in float32 into the codes
     ``[m, n]`` and scales that ``run`` and ``run_all_shares`` read
     (qrs_matmul_int_quantize): one rank's partial sums. n is a multiple of 128."""
     lib = load_library()
-    m, n, k, ld_a, ld_b, ws, nbytes = _matmul_operands(lib, a, a_scales, b, b_scales, False, workspace, stream)
+    m, n, k, ld_a, ld_b = _matmul_operands(a, a_scales, b, b_scales, False)
     xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
-    ld_c = _codes_and_scales(codes, scales, m, n, xd, sl)
+    ld_c = _codes_and_scales(codes, scales, (m, n), xd, sl)
     _check(lib.qrs_matmul_int_quantize(m, n, k, int(xd), int(sl), a.data_ptr(), ld_a, a_scales.data_ptr(),
-                                       b.data_ptr(), ld_b, b_scales.data_ptr(), codes.data_ptr(), ld_c, _ptr(scales),
-                                       ws, nbytes, _stream_handle(stream)))
+                                       b.data_ptr(), ld_b, b_scales.data_ptr(), codes.data_ptr(), ld_c,
+                                       scales.data_ptr(), _stream_handle(stream)))
 
 
 def run_launch_info(p: Plan, stream=None) -> dict:

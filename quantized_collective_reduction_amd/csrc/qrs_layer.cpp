@@ -293,8 +293,7 @@ qrs_status check_matmul_shape(int64_t m, int64_t n, int64_t k, int gated) {
 // the caller describes them (scales.p NULL: no scales).
 qrs_status matmul(qrs::MatmulLaunch* l, int64_t m, int64_t n, int64_t k, int gated, const void* a,
                   int64_t a_row_stride, const float* a_scales, const void* b, int64_t b_row_stride,
-                  const float* b_scales, const Rows& out, const Rows& scales, void* workspace, size_t workspace_bytes,
-                  void* stream) {
+                  const float* b_scales, const Rows& out, const Rows& scales, void* stream) {
   const int64_t wide = gated ? 2 * n : n;
   const Rows in[4] = {{"a", a, m, k, a_row_stride, 1},
                       {"b", b, wide, k, b_row_stride, 1},
@@ -307,18 +306,6 @@ qrs_status matmul(qrs::MatmulLaunch* l, int64_t m, int64_t n, int64_t k, int gat
     QRS_TRY(check_rows(scales));
     QRS_TRY(check_apart(scales, in, 4, false));
     QRS_TRY(check_apart(scales, &out, 1, false));
-  }
-  const uint64_t need = qrs::matmul_workspace_bytes(static_cast<uint32_t>(m), static_cast<uint32_t>(n),
-                                                    static_cast<uint32_t>(k), gated != 0);
-  if (need != 0) {
-    if (!workspace || workspace_bytes < need)
-      return fail(QRS_ERR_INVALID_ARG, "the workspace must hold %llu bytes", static_cast<unsigned long long>(need));
-    if (!aligned(workspace, 16)) return fail(QRS_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
-    const int64_t words = static_cast<int64_t>(need / 4);
-    const Rows ws = {"workspace", workspace, 1, words, words, 4};
-    QRS_TRY(check_apart(ws, in, 4, false));
-    QRS_TRY(check_apart(ws, &out, 1, false));
-    if (l->quantize) QRS_TRY(check_apart(ws, &scales, 1, false));
   }
   l->m = static_cast<uint32_t>(m);
   l->n = static_cast<uint32_t>(n);
@@ -336,7 +323,6 @@ qrs_status matmul(qrs::MatmulLaunch* l, int64_t m, int64_t n, int64_t k, int gat
   l->out = const_cast<void*>(out.p);
   l->out_stride = static_cast<uint64_t>(out.stride);
   l->scales = const_cast<void*>(scales.p);
-  l->workspace = static_cast<int32_t*>(workspace);
   return launched(qrs::launch_matmul(*l, static_cast<hipStream_t>(stream)));
 }
 
@@ -344,19 +330,9 @@ qrs_status matmul(qrs::MatmulLaunch* l, int64_t m, int64_t n, int64_t k, int gat
 
 extern "C" {
 
-qrs_status qrs_matmul_int_workspace(int64_t m, int64_t n, int64_t k, int gated, size_t* bytes_out) {
-  if (!bytes_out) return fail(QRS_ERR_INVALID_ARG, "null bytes_out");
-  *bytes_out = 0;
-  QRS_TRY(check_matmul_shape(m, n, k, gated));
-  *bytes_out = static_cast<size_t>(qrs::matmul_workspace_bytes(static_cast<uint32_t>(m), static_cast<uint32_t>(n),
-                                                               static_cast<uint32_t>(k), gated != 0));
-  return ok();
-}
-
 qrs_status qrs_matmul_int(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype, const void* a,
                           int64_t a_row_stride, const float* a_scales, const void* b, int64_t b_row_stride,
-                          const float* b_scales, void* out, int64_t out_row_stride, void* workspace,
-                          size_t workspace_bytes, void* stream) {
+                          const float* b_scales, void* out, int64_t out_row_stride, void* stream) {
   QRS_TRY(check_matmul_shape(m, n, k, gated));
   QRS_TRY(check_float_type(out_dtype, "out_dtype"));
   qrs::MatmulLaunch l;
@@ -365,15 +341,14 @@ qrs_status qrs_matmul_int(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dt
   l.out_format = to_format(out_dtype);
   const Rows o = {"out", out, m, n, out_row_stride, type_size(out_dtype)};
   const Rows none = {"scales", nullptr, 1, 1, 1, 1};
-  return matmul(&l, m, n, k, gated, a, a_row_stride, a_scales, b, b_row_stride, b_scales, o, none, workspace,
-                workspace_bytes, stream);
+  return matmul(&l, m, n, k, gated, a, a_row_stride, a_scales, b, b_row_stride, b_scales, o, none,
+                stream);
 }
 
 qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype x_dtype,
                                    qrs_scale_layout scale_layout, const void* a, int64_t a_row_stride,
                                    const float* a_scales, const void* b, int64_t b_row_stride, const float* b_scales,
-                                   void* codes, int64_t codes_row_stride, void* scales, void* workspace,
-                                   size_t workspace_bytes, void* stream) {
+                                   void* codes, int64_t codes_row_stride, void* scales, void* stream) {
   QRS_TRY(check_matmul_shape(m, n, k, 0));
   QRS_TRY(check_codes(x_dtype, scale_layout, false));
   if (n % 128 != 0) return fail(QRS_ERR_INVALID_ARG, "n %lld is not a multiple of 128", static_cast<long long>(n));
@@ -387,8 +362,7 @@ qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype 
   const Rows o = {"codes", codes, m, n, codes_row_stride, 1};
   if (codes && !o.rows_on(16)) return fail(QRS_ERR_INVALID_ARG, "rows of codes are not on 16-byte boundaries");
   const Rows s = {"scales", scales, m, n / g, n / g, e8m0 ? 1 : 4};
-  return matmul(&l, m, n, k, 0, a, a_row_stride, a_scales, b, b_row_stride, b_scales, o, s, workspace, workspace_bytes,
-                stream);
+  return matmul(&l, m, n, k, 0, a, a_row_stride, a_scales, b, b_row_stride, b_scales, o, s, stream);
 }
 
 }  // extern "C"

@@ -88,13 +88,11 @@ struct MatmulLaunch {
   void* out;  // values, or codes
   uint64_t out_stride;
   void* scales;
-  int32_t* workspace;
 };
 
 // The largest k whose sums of products (each at most 2^14) fit 32 bits.
 constexpr int64_t kMaxMatmulK = 131071;
 
-uint64_t matmul_workspace_bytes(uint32_t m, uint32_t n, uint32_t k, bool gated);
 // Fails with hipErrorInvalidValue where m * n needs more work-items than a
 // grid holds (2^24 tiles of 64 x 128 outputs, or 64 x 64 gated).
 hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream);

@@ -1086,8 +1086,6 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
 
 }  // namespace
 
-uint64_t matmul_workspace_bytes(uint32_t, uint32_t, uint32_t, bool) { return 0; }
-
 hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream) {
   if (l.quantize) return launch_as<kCodes>(l, stream);
   return l.gated ? launch_as<kGated>(l, stream) : launch_as<kValues>(l, stream);

@@ -33,9 +33,9 @@ BACK = dict(tokens=4, h=1024, io=BF16, eps=1e-5, dy=_at(0), ldy=1024, s=_at(1), 
             dx=_at(4), ldx=1024, dw=_at(5), ws=_at(6), wsb=1 << 20)
 QROWS = dict(rows=4, cols=1000, kind=BF16, xd=INT8, x=_at(0), ldx=1000, c=_at(1), ldc=1000, sc=_at(2))
 MM = dict(m=4, n=256, k=512, gated=0, kind=BF16, a=_at(0), lda=512, sa=_at(1), b=_at(2), ldb=512, sb=_at(3), o=_at(4),
-          ldo=256, ws=_at(5), wsb=1 << 40)
+          ldo=256)
 MMQ = dict(m=4, n=256, k=512, xd=E4M3, sl=MX, a=_at(0), lda=512, sa=_at(1), b=_at(2), ldb=512, sb=_at(3), c=_at(4),
-           ldc=256, sc=_at(6), ws=_at(5), wsb=1 << 31)
+           ldc=256, sc=_at(6))
 
 
 def _norm(lib, **kw):
@@ -59,13 +59,13 @@ def _qrows(lib, **kw):
 def _mm(lib, **kw):
     d = {**MM, **kw}
     return lib.qrs_matmul_int(d["m"], d["n"], d["k"], d["gated"], d["kind"], d["a"], d["lda"], d["sa"], d["b"],
-                              d["ldb"], d["sb"], d["o"], d["ldo"], d["ws"], d["wsb"], None)
+                              d["ldb"], d["sb"], d["o"], d["ldo"], None)
 
 
 def _mmq(lib, **kw):
     d = {**MMQ, **kw}
     return lib.qrs_matmul_int_quantize(d["m"], d["n"], d["k"], d["xd"], d["sl"], d["a"], d["lda"], d["sa"], d["b"],
-                                       d["ldb"], d["sb"], d["c"], d["ldc"], d["sc"], d["ws"], d["wsb"], None)
+                                       d["ldb"], d["sb"], d["c"], d["ldc"], d["sc"], None)
 
 
 NORM_BAD = [
@@ -127,7 +127,7 @@ def test_hifloat8_is_unsupported(lib, call):
     assert call(lib, xd=HIF8) == UNSUPPORTED
 
 
-def test_workspace_queries(lib):
+def test_workspace_query(lib):
     n = ctypes.c_size_t(7)
     assert lib.qrs_rms_norm_backward_workspace(4, 1024, ctypes.byref(n)) == 0
     assert n.value == 4 * 1024 * 4  # a row of sums for each of the four rows
@@ -135,9 +135,6 @@ def test_workspace_queries(lib):
     assert 0 < n.value <= 1 << 23  # bounded whatever the number of tokens
     assert lib.qrs_rms_norm_backward_workspace(0, 1024, ctypes.byref(n)) == INVALID and n.value == 0
     assert lib.qrs_rms_norm_backward_workspace(4, 1024, None) == INVALID
-    assert lib.qrs_matmul_int_workspace(4, 256, 512, 0, ctypes.byref(n)) == 0
-    assert lib.qrs_matmul_int_workspace(4, 256, 0, 0, ctypes.byref(n)) == INVALID and n.value == 0
-    assert lib.qrs_matmul_int_workspace(4, 256, 512, 0, None) == INVALID
 
 
 def test_row_scales_are_no_mode_of_the_reduce_scatter(lib):
