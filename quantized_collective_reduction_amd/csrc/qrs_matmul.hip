@@ -915,11 +915,12 @@ __global__ __launch_bounds__(512, 1) void mid_kernel(const MatmulLaunch a) {
     offset[t] = (r < TM ? (min(i0 + r, a.m - 1) - i0) * static_cast<uint32_t>(a.a_stride)
                         : (row_of(r - TM) - j0) * static_cast<uint32_t>(a.b_stride)) + in_k[t];
   }
-  auto load = [&](uint32_t st, int t) {
+  // Load t of stage st, to `slot`; `full`: the stage ends inside k.
+  auto load = [&](uint32_t st, uint32_t slot, int t, bool full) {
     const uint32_t k = __builtin_amdgcn_readfirstlane(st * P::kStageK);
     const uint32_t at = wave * P::kLoads + t;
-    char* to = lds + st % S * P::kStageBytes + at * 1024;
-    const uint32_t far = k + in_k[t] < a.k ? 0 : kFar;  // past the end of k: zeros
+    char* to = lds + slot * P::kStageBytes + at * 1024;
+    const uint32_t far = full || k + in_k[t] < a.k ? 0 : kFar;  // past the end of k: zeros
     __builtin_amdgcn_raw_ptr_buffer_load_lds(at % (P::kRows / 8) * 8 < TM ? ra : rb, (lds_ptr)to, 16, offset[t] + far, k,
                                              0, 0);
   };
@@ -927,33 +928,34 @@ __global__ __launch_bounds__(512, 1) void mid_kernel(const MatmulLaunch a) {
   float scale = 0.0f;
   if (threadIdx.x < P::kRows)
     scale = threadIdx.x < TM ? a.a_scales[min(i0 + threadIdx.x, a.m - 1)] : a.b_scales[row_of(threadIdx.x - TM)];
-  const uint32_t stages = (a.k + P::kStageK - 1) / P::kStageK;
+  const uint32_t stages = (a.k + P::kStageK - 1) / P::kStageK, full_stages = a.k / P::kStageK;
 #pragma unroll
   for (uint32_t st = 0; st < S; ++st)  // past the last stage: zeros
 #pragma unroll
-    for (int t = 0; t < P::kLoads; ++t) load(st, t);
+    for (int t = 0; t < P::kLoads; ++t) load(st, st, t, false);
 
   i32x4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  const uint32_t slot = ((4 * (g % 2) + lane / 16) ^ (lane % 16 / 2)) * 16;
-  const char* frag = lds + g / 2 * P::kRows * 128 + lane % 16 * 128 + slot;
+  const uint32_t chunk_slot = ((4 * (g % 2) + lane / 16) ^ (lane % 16 / 2)) * 16;
+  const char* frag = lds + g / 2 * P::kRows * 128 + lane % 16 * 128 + chunk_slot;
   const char* frag_b = frag + (TM + wn * P::WTN) * 128;
   i32x4 fa[2][FM], fb[2][FN];  // of even and odd stages
-  auto read = [&](int set, uint32_t st, int x) {
-    const uint32_t base = st % S * P::kStageBytes;
+  auto read = [&](int set, uint32_t slot, int x) {
+    const uint32_t base = slot * P::kStageBytes;
     if (x < FN)
       fb[set][x] = *reinterpret_cast<const i32x4*>(frag_b + base + x * 16 * 128);
     else
       fa[set][x - FN] = *reinterpret_cast<const i32x4*>(frag + base + (x - FN) * 16 * 128);
   };
-  // Multiplies stage st, in registers, while stage st + 1 is read and stage
-  // st + S loaded into st's place in LDS.
-  auto stage = [&](uint32_t st, int set) {
+  // Multiplies stage st (in registers, its LDS `slot`) while stage st + 1 is
+  // read and stage st + S loaded into st's place in LDS.
+  auto stage = [&](uint32_t st, uint32_t slot, int set, bool full) {
     wait_loads_and_sync<P::kLoads * (S - 2)>();
     constexpr int kProducts = FM * FN, kReads = FM + FN, kOthers = kReads + P::kLoads;
+    const uint32_t next = slot + 1 == S ? 0 : slot + 1;
 #pragma unroll
     for (int x = 0; x < (kProducts > kOthers ? kProducts : kOthers); ++x) {
       if (x < kProducts) {
@@ -961,19 +963,26 @@ __global__ __launch_bounds__(512, 1) void mid_kernel(const MatmulLaunch a) {
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
       }
       if (x < kReads)
-        read(1 - set, st + 1, x);
+        read(1 - set, next, x);
       else if (x < kOthers)
-        load(st + S, x - kReads);
+        load(st + S, slot, x - kReads, full);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   wait_loads_and_sync<P::kLoads * (S - 1)>();
 #pragma unroll
   for (int x = 0; x < FM + FN; ++x) read(0, 0, x);
-  // Two stages a round; an odd last one is followed by zeros.
-  for (uint32_t st = 0; st < stages; st += 2) {
-    stage(st, 0);
-    stage(st + 1, 1);
+  // Rounds with fixed slots and nothing to check, while all that they load is
+  // inside k; then two stages a round (an odd last one is followed by zeros).
+  constexpr uint32_t kRound = S % 2 == 0 ? S : 2 * S;
+  uint32_t st = 0;
+  for (; st + S + kRound <= full_stages; st += kRound) {
+#pragma unroll
+    for (uint32_t r = 0; r < kRound; ++r) stage(st + r, r % S, r % 2, true);
+  }
+  for (; st < stages; st += 2) {
+    stage(st, st % S, 0, false);
+    stage(st + 1, (st + 1) % S, 1, false);
   }
 
   // The KG partial sums meet in LDS: one wave of each column writes, the
