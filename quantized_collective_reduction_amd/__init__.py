@@ -676,16 +676,18 @@ def _codes_and_scales(codes, scales, shape, xd, sl):
 
 
 def _workspace(workspace, nbytes, like, stream):
-    """The caller's workspace, or one from torch's allocator, which keeps it
-    until the work enqueued on ``stream`` so far has ended."""
+    """The caller's workspace, or one that torch's allocator gives ``stream``:
+    memory that only work of that stream used before and will use next."""
     import torch
 
     if workspace is not None:
-        return _ptr(workspace), workspace.numel() * workspace.element_size()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return ws.data_ptr(), nbytes
+        return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return ws.data_ptr(), nbytes, ws
 
 
 def add_rms_norm_quantize(x, residual, weight, eps, sum_out, codes, scales, x_dtype, scale_layout, stream=None):
@@ -736,7 +738,7 @@ def rms_norm_backward(grad_y, sum, weight, eps, grad_sum, grad_x, grad_weight, w
     _vector(grad_weight, "grad_weight", h, torch.float32)
     need = ctypes.c_size_t()
     _check(lib.qrs_rms_norm_backward_workspace(tokens, h, ctypes.byref(need)))
-    ws, nbytes = _workspace(workspace, need.value, sum, stream)
+    ws, nbytes, _keep = _workspace(workspace, need.value, sum, stream)  # _keep: until it is enqueued
     _check(lib.qrs_rms_norm_backward(
         tokens, h, io, eps, grad_y.data_ptr(), ld_y, sum.data_ptr(), ld_s, weight.data_ptr(),
         None if grad_sum is None else grad_sum.data_ptr(), ld_g, grad_x.data_ptr(), ld_x, grad_weight.data_ptr(), ws,
