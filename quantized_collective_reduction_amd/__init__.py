@@ -207,7 +207,7 @@ def load_library(path: str = LIB_PATH):
 
 
 def _check(status):
-    if status != Status.OK:
+    if status:  # Status.OK is 0
         msg = _lib.qrs_last_error().decode(errors="replace")
         raise QrsError(status, msg)
 
@@ -654,24 +654,34 @@ def _vector(t, what, n, dtype):
         raise ValueError(f"{what}: {n} contiguous {dtype} elements expected, got {list(t.shape)} {t.dtype}")
 
 
-_GROUP_OF = {ScaleLayout.F32_GROUP128: 128, ScaleLayout.E8M0_BLOCK32: 32}
+@functools.lru_cache(maxsize=None)
+def _mode(x_dtype, scale_layout):
+    """(x_dtype, scale_layout) as the library's ints, with the element types
+    of codes and scales and the scales' group (0: the row)."""
+    import torch
 
-
-def _codes_and_scales(codes, scales, shape, xd, sl):
-    """Checks codes and scales of a mode; the codes' row stride."""
+    xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
     x_dt, s_dt, _ = _element_dtypes()
+    group = {ScaleLayout.F32_GROUP128: 128, ScaleLayout.E8M0_BLOCK32: 32}.get(sl, 0)
+    return int(xd), int(sl), x_dt.get(xd), s_dt.get(sl, torch.float32), group
+
+
+def _codes_and_scales(codes, scales, shape, mode):
+    """Checks codes and scales of a mode; the codes' row stride."""
+    _, _, x_dt, s_dt, group = mode
     ld = _matrix(codes, "codes", shape)
-    if codes.element_size() != 1:
-        raise ValueError(f"codes: 1-byte elements expected, got {codes.dtype}")
-    _check_dtype(codes, x_dt.get(xd), "codes")
+    if codes.dtype != x_dt:
+        if codes.element_size() != 1:
+            raise ValueError(f"codes: 1-byte elements expected, got {codes.dtype}")
+        _check_dtype(codes, x_dt, "codes")
     rows, h = shape
-    n = rows if sl == ScaleLayout.F32_ROW else rows * h // _GROUP_OF.get(sl, 32)
-    if sl == ScaleLayout.E8M0_BLOCK32:
+    n = rows * h // group if group else rows
+    if group == 32 and scales.dtype != s_dt:  # E8M0 codes also as raw bytes
         _check_tensor(scales, n, "scales")
-        _check_dtype(scales, s_dt[sl], "scales")
+        _check_dtype(scales, s_dt, "scales")
         _ptr(scales)
     else:
-        _vector(scales, "scales", n, s_dt[ScaleLayout.F32_GROUP128])
+        _vector(scales, "scales", n, s_dt)
     return ld
 
 
@@ -708,10 +718,10 @@ def add_rms_norm_quantize(x, residual, weight, eps, sum_out, codes, scales, x_dt
     if residual is not None:
         ld_r = _matrix(residual, "residual", x.shape, x.dtype)
         ld_s = _matrix(sum_out, "sum_out", x.shape, x.dtype)
-    xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
-    ld_c = _codes_and_scales(codes, scales, x.shape, xd, sl)
+    mode = _mode(x_dtype, scale_layout)
+    ld_c = _codes_and_scales(codes, scales, x.shape, mode)
     _check(lib.qrs_add_rms_norm_quantize(
-        tokens, h, io, int(xd), int(sl), eps, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(),
+        tokens, h, io, mode[0], mode[1], eps, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(),
         ld_r, weight.data_ptr(), None if residual is None else sum_out.data_ptr(), ld_s, codes.data_ptr(), ld_c,
         scales.data_ptr(), _stream_handle(stream)))
 
@@ -752,9 +762,9 @@ def quantize_rows(x, codes, scales, x_dtype="int8", stream=None):
     kind = _act_dtype(x, "x")
     ld_x = _matrix(x, "x")
     rows, cols = x.shape
-    xd = _enum(x_dtype, _X_NAMES, XDtype)
-    ld_c = _codes_and_scales(codes, scales, x.shape, xd, ScaleLayout.F32_ROW)
-    _check(lib.qrs_quantize_rows(rows, cols, kind, int(xd), x.data_ptr(), ld_x, codes.data_ptr(), ld_c,
+    mode = _mode(x_dtype, "f32_row")
+    ld_c = _codes_and_scales(codes, scales, x.shape, mode)
+    _check(lib.qrs_quantize_rows(rows, cols, kind, mode[0], x.data_ptr(), ld_x, codes.data_ptr(), ld_c,
                                  scales.data_ptr(), _stream_handle(stream)))
 
 
@@ -793,9 +803,9 @@ def matmul_int8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale
     (qrs_matmul_int_quantize): one rank's partial sums. n is a multiple of 128."""
     lib = load_library()
     m, n, k, ld_a, ld_b = _matmul_operands(a, a_scales, b, b_scales, False)
-    xd, sl = _enum(x_dtype, _X_NAMES, XDtype), _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
-    ld_c = _codes_and_scales(codes, scales, (m, n), xd, sl)
-    _check(lib.qrs_matmul_int_quantize(m, n, k, int(xd), int(sl), a.data_ptr(), ld_a, a_scales.data_ptr(),
+    mode = _mode(x_dtype, scale_layout)
+    ld_c = _codes_and_scales(codes, scales, (m, n), mode)
+    _check(lib.qrs_matmul_int_quantize(m, n, k, mode[0], mode[1], a.data_ptr(), ld_a, a_scales.data_ptr(),
                                        b.data_ptr(), ld_b, b_scales.data_ptr(), codes.data_ptr(), ld_c,
                                        scales.data_ptr(), _stream_handle(stream)))
 
