@@ -14,7 +14,6 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "qrs_device.h"
 #include "qrs_layer.h"
@@ -34,16 +33,18 @@ constexpr uint32_t kCus = 256;
 // g / (1 + exp(-g)). exp as a power of two whose exponent's rounding error is
 // put back as a factor, 1 / d as the hardware's estimate and one Newton step:
 // each within a few units of the last place, for a third of the instructions
-// of the library's exp and divide (a gated tile's epilogue 9 us -> 4 us). The
-// power is kept below 2^126, so that its reciprocal is a normal number.
+// of the library's exp and divide (512 tokens by 5120 ups, k = 1024: 17.5 us
+// -> 16.5). Beyond 87 the quotient is 1, beyond -87 (there less than 2^-125)
+// it is 0, so that nothing between overflows.
 __device__ __forceinline__ float silu(float g) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
-  const float p = -g * kLog2e;
-  const float low = __builtin_fmaf(-g, kLog2eLow, __builtin_fmaf(-g, kLog2e, -p));
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f, kLimit = 87.0f;
+  const float x = __builtin_amdgcn_fmed3f(g, -kLimit, kLimit);
+  const float p = -x * kLog2e;
+  const float low = __builtin_fmaf(-x, kLog2eLow, __builtin_fmaf(-x, kLog2e, -p));
   const float e = __builtin_amdgcn_exp2f(p);
-  const float d = 1.0f + __builtin_fminf(__builtin_fmaf(e, low * kLn2, e), 0x1p126f);
+  const float d = 1.0f + __builtin_fmaf(e, low * kLn2, e);
   const float r = __builtin_amdgcn_rcpf(d);
-  return g * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  return g * (g < -kLimit ? 0.0f : __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r));
 }
 
 // What a kernel instance writes.
@@ -1062,8 +1063,12 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   if (l.m <= 16) return launch_few_sized<1, F>(l, stream);
   if (l.m <= 32) return launch_few_sized<2, F>(l, stream);
   // The tile whose busiest CU loads least. The pipelined kernel's rows count
-  // half as much again: its CU takes 36 GB/s (the matrix units and the power
-  // limit bound it), the others' 50 to 58.
+  // a quarter more: its CU takes 33 to 39 GB/s (the matrix units and the
+  // power limit bound it), the others' 39 to 47 once most CUs have a tile.
+  // k = 5120, rows of a CU and time of <256, 256> and of the best other:
+  // 1536 tokens by 8192, 512 rows 75 us and 768 rows 87; 1024 by 5120, 512
+  // rows 74 us and 384 rows 48; 4096 by 9472, 1536 rows 204 us and 1920 rows
+  // 221.
   const bool narrow = F != kCodes || l.scale_layout == kScaleE8M0Block32;  // less than 128 channels a tile
   uint32_t best = ~0u;
   hipError_t (*launch)(const MatmulLaunch&, hipStream_t) = nullptr;
@@ -1073,22 +1078,13 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
       launch = f;
     }
   };
-  if (l.k > kBlockK) offer(rows_a_cu<256, 256, F>(l) * 3 / 2, launch_pipe<256, 256, 128, F>);
+  if (l.k > kBlockK) offer(rows_a_cu<256, 256, F>(l) * 5 / 4, launch_pipe<256, 256, 128, F>);
   offer(rows_a_cu<128, 256, F>(l), launch_mid<128, 256, 2, 3, F>);
   offer(rows_a_cu<128, 128, F>(l), launch_mid<128, 128, 2, 4, F>);
   offer(rows_a_cu<64, 128, F>(l), launch_mid<64, 128, 2, 6, F>);
   if (narrow) {
     offer(rows_a_cu<64, 64, F>(l), launch_mid<64, 64, 4, 4, F>);
     offer(rows_a_cu<64, 32, F>(l), launch_mid<64, 32, 8, 3, F>);
-  }
-  const char* e = getenv("QRS_MID");
-  if (e) switch (atoi(e)) {
-    case 0: return launch_pipe<256, 256, 128, F>(l, stream);
-    case 1: return launch_mid<128, 256, 2, 3, F>(l, stream);
-    case 2: return launch_mid<128, 128, 2, 4, F>(l, stream);
-    case 3: return launch_mid<64, 128, 2, 6, F>(l, stream);
-    case 4: return launch_mid<64, 64, 4, 4, F>(l, stream);
-    case 5: return launch_mid<64, 32, 8, 3, F>(l, stream);
   }
   return launch(l, stream);
 }

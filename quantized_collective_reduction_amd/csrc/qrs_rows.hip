@@ -146,7 +146,7 @@ __device__ __forceinline__ void quantize_row(float (*v)[E], const RowsLaunch& a,
 // The sum of squares, r and y are taken in binary64 and y rounded once to
 // binary32: codes next to a border between two then fall on the side of the
 // exact value (in binary32, a few in 10^7 do not), and no sum of squares
-// overflows. It costs 3 us of vector time where the memory takes 19.
+// overflows.
 template <int IO, int SL, int NT, int P8, bool VEC, bool NORM, bool STREAM>
 __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane

@@ -142,6 +142,25 @@ def test_gated_at_large_gates(gpu):
     assert np.all(np.abs(host(out) - want) <= np.abs(want) * 16 * STEP + 2.0 ** -100)
 
 
+def test_gated_at_gates_of_any_size(gpu):
+    """silu(g) is 0 for large negative gates, however large, and g / (1 +
+    exp(-g)) of an infinity or NaN is what the formula gives."""
+    g = np.array([-3e38, -1e30, -1e4, -104, -89, -88, -87, 0, 1e30, 3e38, np.inf, -np.inf, np.nan], np.float32)
+    n = len(g)
+    a, b = np.zeros((40, 16), np.int8), np.zeros((2 * n, 16), np.int8)
+    a[:, 0] = b[:, 0] = 1
+    sb = np.concatenate([g, np.ones(n, np.float32)])
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = g.astype(np.float64) / (1.0 + np.exp(-g.astype(np.float64)))
+    bound = np.where(np.isfinite(want), np.abs(want) * 16 * STEP + 2.0 ** -100, 0.0)
+    for m in (1, 20, 40):
+        out = torch.empty(m, n, device="cuda")
+        qrs.matmul_int8(device(a[:m]), device(np.ones(m, np.float32)), device(b), device(sb), out, gated=True)
+        got = host(out)
+        with np.errstate(invalid="ignore"):
+            assert np.all((np.abs(got - want) <= bound) | (got == want) | (np.isnan(got) & np.isnan(want))), got[0]
+
+
 MODES = [("int8", "f32_group128"), ("e4m3fn", "f32_group128"), ("e5m2", "f32_group128"), ("e4m3fn", "e8m0_block32"),
          ("e5m2", "e8m0_block32")]
 
