@@ -76,13 +76,21 @@ __device__ __forceinline__ PieceScales piece_scales(const MatmulLaunch& a, uint3
 
 // The codes of a piece and its group's scale (E8M0 code or binary32 bits),
 // the mode chosen at run time: a kernel's epilogue repeats this for every
-// fragment, and a copy for each mode would be five times the code. `finite`:
-// the scales that v was multiplied by are, so that v holds no NaN.
-__device__ __forceinline__ Codes<kPiece> encode_group(const MatmulLaunch& a, const float* v, bool finite, uint32_t* scale_bits) {
+// fragment, and a copy for each mode would be five times the code.
+// `no_nan`: the scales that v was multiplied by leave no NaN in it, and the
+// maximum may be one of numbers; else it is one of bits, where NaN stands
+// above infinity.
+__device__ __forceinline__ Codes<kPiece> encode_group(const MatmulLaunch& a, const float* v, bool no_nan,
+                                                       uint32_t* scale_bits) {
   float m = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
 #pragma unroll
   for (int j = 2; j < kPiece; ++j) m = __builtin_fmaxf(m, __builtin_fabsf(v[j]));
-  uint32_t amax = group_max<4>(finite ? __builtin_bit_cast(uint32_t, m) : 0x7FC00000u);
+  uint32_t bits = __builtin_bit_cast(uint32_t, m);
+  if (!no_nan) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) bits = max(bits, abs_bits(v[j]));
+  }
+  uint32_t amax = group_max<4>(bits);
   float mul;
   if (a.scale_layout == kScaleE8M0Block32) {
     mul = a.x_format == kXE4M3FN ? mx_multiplier<kXE4M3FN>(amax, scale_bits) : mx_multiplier<kXE5M2>(amax, scale_bits);
@@ -101,12 +109,14 @@ __device__ __forceinline__ Codes<kPiece> encode_group(const MatmulLaunch& a, con
   return encode_piece<kXInt8>(v, mul);
 }
 
-__device__ __forceinline__ bool is_finite(float v) { return abs_bits(v) < 0x7F800000u; }
+// Whether an integer sum times a token's scale is finite for certain: the
+// scale is below 2^95.
+__device__ __forceinline__ bool keeps_finite(float token_scale) { return abs_bits(token_scale) < 0x6F000000u; }
 
-__device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, bool finite,
+__device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, uint32_t j0, bool active, bool no_nan,
                                              const float* v) {
   uint32_t scale;
-  const Codes<kPiece> codes = encode_group(a, v, finite, &scale);
+  const Codes<kPiece> codes = encode_group(a, v, no_nan, &scale);
   if (!active) return;
   store_codes<true, kPiece>(static_cast<uint8_t*>(a.out) + static_cast<uint64_t>(i) * a.out_stride, j0, a.n, codes);
   if (a.scale_layout == kScaleE8M0Block32) {
@@ -146,7 +156,7 @@ __device__ __forceinline__ void finish_piece(const MatmulLaunch& a, uint32_t i, 
                                              const PieceScales& s, float* v, const float* up) {
   scale_piece<F>(s, v, up);
   if constexpr (F == kCodes) {
-    finish_codes(a, i, j0, active, is_finite(sa) && s.finite(), v);
+    finish_codes(a, i, j0, active, keeps_finite(sa) && s.finite(), v);
   } else {
     if (!active) return;
     if (a.out_format == kOutF32)
@@ -394,10 +404,10 @@ struct WholeTile {
     }
   }
 
-  __device__ __forceinline__ void store(const MatmulLaunch& a, uint32_t t, const float* v, bool finite) const {
+  __device__ __forceinline__ void store(const MatmulLaunch& a, uint32_t t, const float* v, bool no_nan) const {
     if constexpr (F == kCodes) {
       uint32_t scale;
-      const Codes<kPiece> codes = encode_group(a, v, finite, &scale);
+      const Codes<kPiece> codes = encode_group(a, v, no_nan, &scale);
       __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes.w[0], codes.w[1]}, out, out_lane, t * out_row, kStream);
       if (has_scale) {
         if (a.scale_layout == kScaleE8M0Block32)
@@ -661,7 +671,7 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
           values(t, unit, sa[i][p], v);
           if constexpr (F == kGated) values(t, unit + 2 * pieces, sa[i][p], up);
           scale_piece<F>(sb, v, up);
-          whole.store(a, 16 * i + p * kPass, v, sb_finite && is_finite(sa[i][p]));
+          whole.store(a, 16 * i + p * kPass, v, sb_finite && keeps_finite(sa[i][p]));
         }
       }
     } else {

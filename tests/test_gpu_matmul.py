@@ -96,6 +96,33 @@ def test_product_at_the_largest_sums(gpu, m):
         _check(a, np.ones(m, np.float32), b, np.ones(3, np.float32), "f32")
 
 
+@pytest.mark.parametrize("far", ["a", "b", "out"])
+@pytest.mark.parametrize("m,n,k", [(12, 300, 80), (140, 200, 144)])
+def test_product_of_far_rows(gpu, m, n, k, far):
+    """Rows 4 MiB and more apart: a tile's rows span more than 2^30 bytes."""
+    rng = np.random.default_rng([m, n, k, 5])
+    a, sa, b, sb = _operands(rng, m, n, k)
+    spread = lambda t, stride: torch.empty_strided(t.shape, (stride, 1), dtype=t.dtype, device="cuda").copy_(t)
+    da, db = device(a), device(b)
+    if far == "a":
+        da = spread(da, (1 << 22) + 16)
+    if far == "b":
+        db = spread(db, (1 << 22) + 32)
+    out = spread(torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda"), (1 << 22) + 8 if far == "out" else n)
+    qrs.matmul_int8(da, device(sa), db, device(sb), out)
+    assert np.array_equal(out_bits(out.contiguous()), _bits(scaled_product(a, sa, b, sb), "bf16"))
+
+
+def test_whole_tiles_of_far_rows(gpu):
+    """Whole tiles of the largest size, whose output rows lie 4 MiB apart."""
+    rng = np.random.default_rng(6)
+    m, n, k = 2048, 5120, 144
+    a, sa, b, sb = _operands(rng, m, n, k)
+    out = torch.empty_strided((m, n), ((1 << 21) + 8, 1), dtype=torch.bfloat16, device="cuda")
+    qrs.matmul_int8(device(a), device(sa), device(b), device(sb), out)
+    assert np.array_equal(out_bits(out.contiguous()), _bits(scaled_product(a, sa, b, sb), "bf16"))
+
+
 def test_scales_that_are_not_finite_propagate(gpu):
     rng = np.random.default_rng(2)
     a, sa, b, sb = _operands(rng, 40, 200, 64)
@@ -182,6 +209,39 @@ def test_quantized_product(gpu, m, n, k, x_format, layout):
     # Zero rows may keep the sign of zero in floating codes.
     bad = (got != c) & ((got & 0x7F) != 0) if x_format != "int8" else got != c
     assert not bad.any(), np.argwhere(bad)[:4]
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 256, 64), (30, 256, 64), (200, 512, 128), (2048, 5120, 144), (3, 256, 17)])
+@pytest.mark.parametrize("x_format,layout", [("int8", "f32_group128"), ("e4m3fn", "e8m0_block32")])
+def test_quantized_product_that_is_not_finite(gpu, m, n, k, x_format, layout):
+    """NaN and infinite scales, and sums that overflow, show in the scales of
+    their groups; the other groups are the oracle's."""
+    rng = np.random.default_rng([m, n, k, 4])
+    a, sa, b, sb = _operands(rng, m, n, k)
+    clean, clean_scales = quantize_values(scaled_product(a, sa, b, sb), x_format, layout)
+    a[1], b[5], b[37] = 127, 127, 0
+    a[m - 1] = b[n - 1] = b[70]
+    sa[m - 1], sb[n - 1], sb[140] = np.nan, np.inf, np.nan
+    # Row 1: infinite where a sum is not 0, NaN where its b scale is 0 then.
+    sa[1], sb[5], sb[6] = 2.0 ** 127, 0, 2.0 ** -10
+    # Channels 32 .. 63 of row 1: a NaN beside finite numbers.
+    b[32:64] = 0
+    b[40], sb[40] = 1, 0
+    codes, scales = empty_codes(m, n, layout)
+    qrs.matmul_int8_quantize(device(a), device(sa), device(b), device(sb), codes, scales, x_format, layout)
+    with np.errstate(all="ignore"):
+        v = scaled_product(a, sa, b, sb)
+    g = 128 if layout == "f32_group128" else 32
+    good = np.isfinite(v.reshape(m, n // g, g)).all(axis=2)
+    if g == 32:
+        assert not good[1, 1] and np.isnan(v[1, 40]) and np.isfinite(v[1, 41:64]).all()
+    assert not good[m - 1].any() and not good[:, n // g - 1].all() and not good[:, 140 // g].any() and good.any()
+    got = scales.cpu().numpy().reshape(good.shape)
+    assert np.array_equal(got != 255 if layout == "e8m0_block32" else np.isfinite(got), good)
+    c, s = quantize_values(np.where(np.repeat(good, g, axis=1), v, 0), x_format, layout)
+    assert np.array_equal(got[good], s.reshape(good.shape)[good])
+    where = np.repeat(good, g, axis=1) & (np.abs(v) > 0)
+    assert np.array_equal(codes.cpu().numpy()[where], c[where])
 
 
 def test_quantized_product_feeds_a_share(gpu):
