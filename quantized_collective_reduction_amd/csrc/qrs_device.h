@@ -286,33 +286,5 @@ __device__ __forceinline__ Codes<E> encode_piece(const float* v, float mul) {
   return codes;
 }
 
-// One piece of a row in a group layout: codes, and the group's scale from
-// its first lane. Lanes of a group are consecutive and all take part; `c` is
-// the piece's first column and `active` whether it is inside the row.
-template <int XF, int SL, bool VEC, int E>
-__device__ __forceinline__ void quantize_group_piece(const float* v, bool active, uint32_t c, uint32_t h,
-                                                     uint8_t* codes_row, void* scales, uint64_t first_scale) {
-  constexpr int G = SL == kScaleF32Group128 ? 128 : 32;
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < E; ++j) amax = max(amax, abs_bits(v[j]));
-  amax = group_max<G / E>(amax);
-  float mul, scale = 0.0f;
-  uint32_t code = 0;
-  if constexpr (SL == kScaleF32Group128)
-    mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
-  else
-    mul = mx_multiplier<XF>(amax, &code);
-  const Codes<E> codes = encode_piece<XF, E>(v, mul);
-  if (!active) return;
-  store_codes<VEC, E>(codes_row, c, h, codes);
-  if (c % G == 0) {
-    if constexpr (SL == kScaleF32Group128)
-      static_cast<float*>(scales)[first_scale + c / G] = scale;
-    else
-      static_cast<uint8_t*>(scales)[first_scale + c / G] = static_cast<uint8_t>(code);
-  }
-}
-
 }  // namespace dev
 }  // namespace qrs

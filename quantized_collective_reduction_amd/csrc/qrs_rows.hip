@@ -82,16 +82,6 @@ struct RawPiece<kOutF16, true> : RawPiece16<kOutF16> {};
 // pass, 1074 MB: 195 us, as a stream 174; 59 MB, found there: 20.2 and 21.6).
 constexpr uint64_t kStreamBytes = uint64_t{256} << 20;
 
-// Work-groups of a kernel that walks over rows: `per_row` / h, and one a CU at
-// least. More for narrow rows, whose operands under way would not fill the
-// memory's pipe; too many leave none to load ahead of (norm to codes, bf16:
-// 16384 x 1024 with 512, 1024, 2048 and 4096 work-groups 47.5, 36.2, 33.0 and
-// 30.2 us; 2048 x 8192 with 256, 512, 1024 and 2048 24.4, 23.7, 23.8 and 25.2).
-inline uint32_t rows_blocks(uint32_t per_row, uint32_t h) {
-  const uint32_t blocks = per_row / h;
-  return blocks > 256 ? blocks < 4096 ? blocks : 4096 : 256;
-}
-
 // The wave's own barrier: LDS alone. A fence would also wait for the loads of
 // the next row.
 __device__ __forceinline__ void lds_barrier() {
@@ -116,25 +106,150 @@ __device__ __forceinline__ double wave_sum(double v) {
   return (row[0] + row[1]) + (row[2] + row[3]);
 }
 
+// Values that are to be taken as new ones: what is made of them is not kept
+// over rows, or made ahead of the branch that needs it, at the cost of the
+// registers that let more waves run.
+template <int E>
+__device__ __forceinline__ void as_new(float (&v)[E]) {
+#pragma unroll
+  for (int j = 0; j < E; ++j) asm volatile("" : "+v"(v[j]));
+}
+
+// y * 2^896 rounded to odd: toward zero, the last bit set if that was inexact.
+// A second rounding, to fewer bits, then gives what it would give for y. The
+// factor puts the exponent of a binary64 where a binary32 has it, subnormal
+// numbers included, so that a shift truncates; values that binary32 does not
+// hold become NaN.
+__device__ __forceinline__ float round_to_odd(double y) {
+  const uint64_t bits = __builtin_bit_cast(uint64_t, y);
+  const uint32_t low = static_cast<uint32_t>(bits), sign = static_cast<uint32_t>(bits >> 32) & 0x80000000u;
+  const uint32_t magnitude = min(static_cast<uint32_t>(bits >> 29), 0x7FC00000u) | min(low & 0x1FFFFFFFu, 1u);
+  return __builtin_bit_cast(float, magnitude | sign);
+}
+
+// One lane's pieces of a row and what makes values for codes of them.
+//
+// y = s * r * weight is taken in binary32, within 1.5 * 2^-24 of itself, and in
+// binary64 where that does not do: in rows whose squares leave binary32's
+// range, and, with E8M0 scales, where y is so close to a border between two
+// codes that the error could decide which one it gets. (In binary64 always, it
+// takes the registers of a second work-group: 8192 x 5120 fp32 117 us.)
+template <int IO, bool VEC, bool NORM, int P>
+struct RowValues {
+  static constexpr int E = kPiece16<IO>;
+  float v[P][E];  // s, or without a norm the values themselves
+  double r;
+  bool wide;  // y in binary64
+  const RawPiece<IO, VEC>* w;
+
+  // TO_F32: in binary64 where the row is wide.
+  template <bool TO_F32>
+  __device__ __forceinline__ void piece(int p, float* y) const {
+    if constexpr (NORM) {
+      float s[E], wv[E];
+      operands(p, s, wv);
+#pragma unroll
+      for (int j = 0; j < E; ++j) y[j] = s[j] * static_cast<float>(r) * wv[j];
+      if (TO_F32 && wide) {
+        operands(p, s, wv);
+#pragma unroll
+        for (int j = 0; j < E; ++j) y[j] = static_cast<float>(static_cast<double>(s[j]) * r * static_cast<double>(wv[j]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) y[j] = v[p][j];
+    }
+  }
+
+  __device__ __forceinline__ void piece_to_odd(int p, float* y) const {
+    float s[E], wv[E];
+    operands(p, s, wv);
+    const double factor = r * 0x1p-896;
+#pragma unroll
+    for (int j = 0; j < E; ++j) y[j] = round_to_odd(static_cast<double>(s[j]) * factor * static_cast<double>(wv[j]));
+  }
+
+ private:
+  __device__ __forceinline__ void operands(int p, float (&s)[E], float (&wv)[E]) const {
+    w[p].get(wv);
+#pragma unroll
+    for (int j = 0; j < E; ++j) s[j] = v[p][j];
+    as_new(s);
+    as_new(wv);
+  }
+};
+
+template <int E>
+__device__ __forceinline__ uint32_t piece_max(const float* y) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < E; ++j) amax = max(amax, abs_bits(y[j]));
+  return amax;
+}
+
+// Codes and E8M0 scales of a lane's pieces: those of y in binary32 if both
+// ends of the interval y * (1 -+ 2^-22) have them in every lane of the wave,
+// else (one wave's row in about 100) those of y rounded to odd.
+template <int XF, int P, typename Values>
+__device__ __forceinline__ void mx_codes(const Values& row, Codes<Values::E>* codes, uint32_t* scales) {
+  constexpr int E = Values::E, G = 32;
+  bool sure = !row.wide;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    float y[E];
+    row.template piece<false>(p, y);
+    const uint32_t amax = group_max<G / E>(piece_max<E>(y));
+    const float mul = mx_multiplier<XF>(amax, &scales[p]);
+    codes[p] = encode_piece<XF, E>(y, mul * (1.0f + 0x1p-22f));
+    const Codes<E> low = encode_piece<XF, E>(y, mul * (1.0f - 0x1p-22f));
+    sure = sure && (amax + 8) >> 23 == (max(amax, 8u) - 8) >> 23;
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) sure = sure && codes[p].w[k] == low.w[k];
+  }
+  if (__builtin_amdgcn_ballot_w64(!sure) == 0) return;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    float y[E];
+    row.piece_to_odd(p, y);
+    const uint32_t amax = group_max<G / E>(piece_max<E>(y));
+    codes[p] = encode_piece<XF, E>(y, mx_multiplier<XF>(amax, &scales[p]));
+  }
+}
+
 // Codes of one row held as P pieces per lane, piece p at column
 // (p * NT + lane) * E.
-template <int XF, int SL, int NT, int P, bool VEC, int E>
-__device__ __forceinline__ void quantize_row(float (*v)[E], const RowsLaunch& a, uint64_t row, int lane,
+template <int XF, int SL, int NT, int P, bool VEC, typename Values>
+__device__ __forceinline__ void quantize_row(const Values& values, const RowsLaunch& a, uint64_t row, int lane,
                                              uint32_t amax) {
+  constexpr int E = Values::E;
   uint8_t* codes_row = static_cast<uint8_t*>(a.codes) + row * a.codes_stride;
-  if constexpr (SL == kScaleF32Row) {
-    float scale;
-    const float mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-      store_codes<VEC, E>(codes_row, (p * NT + lane) * E, a.h, encode_piece<XF, E>(v[p], mul));
-    if (lane == 0) static_cast<float*>(a.scales)[row] = scale;
-  } else {
-    const uint64_t first = row * (a.h / (SL == kScaleF32Group128 ? 128 : 32));
+  if constexpr (SL == kScaleE8M0Block32) {
+    Codes<E> codes[P];
+    uint32_t scales[P];
+    mx_codes<XF, P>(values, codes, scales);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t c = (p * NT + lane) * E;
-      quantize_group_piece<XF, SL, VEC, E>(v[p], c < a.h, c, a.h, codes_row, a.scales, first);
+      store_codes<VEC, E>(codes_row, c, a.h, codes[p]);
+      if (c < a.h && c % 32 == 0)
+        static_cast<uint8_t*>(a.scales)[row * (a.h / 32) + c / 32] = static_cast<uint8_t>(scales[p]);
+    }
+  } else {
+    float mul = 0.0f, scale = 0.0f;
+    if constexpr (SL == kScaleF32Row) {
+      mul = f32_multiplier(amax, CodeFormat<XF>::kMax, &scale);
+      if (lane == 0) static_cast<float*>(a.scales)[row] = scale;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t c = (p * NT + lane) * E;
+      float y[E];
+      values.template piece<true>(p, y);
+      if constexpr (SL == kScaleF32Group128)
+        mul = f32_multiplier(group_max<128 / E>(piece_max<E>(y)), CodeFormat<XF>::kMax, &scale);
+      store_codes<VEC, E>(codes_row, c, a.h, encode_piece<XF, E>(y, mul));
+      if (SL == kScaleF32Group128 && c < a.h && c % 128 == 0)
+        static_cast<float*>(a.scales)[row * (a.h / 128) + c / 128] = scale;
     }
   }
 }
@@ -143,10 +258,8 @@ __device__ __forceinline__ void quantize_row(float (*v)[E], const RowsLaunch& a,
 // is quantized. Work-group b takes rows b, b + gridDim, ...; the next row's
 // operands are under way while a row is reduced and written.
 //
-// The sum of squares, r and y are taken in binary64 and y rounded once to
-// binary32: codes next to a border between two then fall on the side of the
-// exact value (in binary32, a few in 10^7 do not), and no sum of squares
-// overflows.
+// The squares of a piece are added in binary32, the pieces in binary64. If
+// the sum is not well inside binary32's range, it is taken again in binary64.
 template <int IO, int SL, int NT, int P8, bool VEC, bool NORM, bool STREAM>
 __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
@@ -183,11 +296,23 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   // a row ahead writes the other half, and the next barrier keeps it from
   // going further.
   int turn = 0;
+  RowValues<IO, VEC, NORM, P> values;
+  auto& v = values.v;
+  values.w = w;
+  values.wide = false;
+  auto row_sum = [&](double ss) {
+    ss = wave_sum(ss);
+    if (lane % 64 == 0) sum_part[turn][lane / 64] = ss;
+    lds_barrier();
+    ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) ss += sum_part[turn][i];
+    return ss;
+  };
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     if (!kAhead) load_row(row);
     const Operands now = next;
     if (kAhead && row + gridDim.x < a.rows) load_row(row + gridDim.x);
-    float v[P][E];
 #pragma unroll
     for (int p = 0; p < P; ++p) now.x[p].get(v[p]);
     if constexpr (NORM) {
@@ -204,38 +329,39 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
       }
       double ss = 0.0;
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+      for (int p = 0; p < P; ++p) {
+        float q = v[p][0] * v[p][0];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const double s = v[p][j];
-          ss = __builtin_fma(s, s, ss);
+        for (int j = 1; j < E; ++j) q = __builtin_fmaf(v[p][j], v[p][j], q);
+        ss += q;
+      }
+      ss = row_sum(ss);
+      values.wide = !(ss > 0x1p-70 && ss < 0x1p120);  // the same in every lane
+      if (values.wide) {
+        turn ^= 1;
+        ss = 0.0;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          as_new(v[p]);
+#pragma unroll
+          for (int j = 0; j < E; ++j) ss = __builtin_fma(v[p][j], static_cast<double>(v[p][j]), ss);
         }
-      ss = wave_sum(ss);
-      if (lane % 64 == 0) sum_part[turn][lane / 64] = ss;
-      lds_barrier();
-      ss = 0.0;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) ss += sum_part[turn][i];
+        ss = row_sum(ss);
+      }
       // The hardware's estimate (about 2^-24) and one Newton step.
       const double m = ss * a.inv_h + static_cast<double>(a.eps);
       const double q = __builtin_amdgcn_rsq(m);
-      const double r = __builtin_isinf(m) ? 0.0 : q * __builtin_fma(-0.5 * m * q, q, 1.5);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float wv[E];
-        w[p].get(wv);
-#pragma unroll
-        for (int j = 0; j < E; ++j)
-          v[p][j] = static_cast<float>(static_cast<double>(v[p][j]) * r * static_cast<double>(wv[j]));
-      }
+      values.r = __builtin_isinf(m) ? 0.0 : q * __builtin_fma(-0.5 * m * q, q, 1.5);
     }
 
     uint32_t amax = 0;
     if constexpr (SL == kScaleF32Row) {
 #pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < E; ++j) amax = max(amax, abs_bits(v[p][j]));
+      for (int p = 0; p < P; ++p) {
+        float y[E];
+        values.template piece<true>(p, y);
+        amax = max(amax, piece_max<E>(y));
+      }
       amax = wave_max(amax);
       if (lane % 64 == 0) max_part[turn][lane / 64] = amax;
       lds_barrier();
@@ -243,18 +369,26 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
       for (int i = 0; i < kWaves; ++i) amax = max(amax, max_part[turn][i]);
     }
     if (a.x_format == kXE4M3FN) {
-      quantize_row<kXE4M3FN, SL, NT, P, VEC, E>(v, a, row, lane, amax);
+      quantize_row<kXE4M3FN, SL, NT, P, VEC>(values, a, row, lane, amax);
     } else if (a.x_format == kXE5M2) {
-      quantize_row<kXE5M2, SL, NT, P, VEC, E>(v, a, row, lane, amax);
+      quantize_row<kXE5M2, SL, NT, P, VEC>(values, a, row, lane, amax);
     } else if constexpr (SL != kScaleE8M0Block32) {
-      quantize_row<kXInt8, SL, NT, P, VEC, E>(v, a, row, lane, amax);
+      quantize_row<kXInt8, SL, NT, P, VEC>(values, a, row, lane, amax);
     }
   }
 }
 
 template <int IO, int SL, int NT, int P, bool VEC, bool NORM, bool STREAM>
 hipError_t launch_rows_as(const RowsLaunch& l, hipStream_t stream) {
-  const uint32_t blocks = rows_blocks(1u << 22, l.h);
+  // Where registers leave two work-groups a CU (one of 1024 lanes), as many as
+  // run at once: each loads ahead, and none is left over for a second round.
+  // Else many, which even out by themselves. Norm of bf16 rows, us with 512
+  // and 4096 work-groups: 2048 x 8192 23.8 and 24.5, 16384 x 8192 148 and 151,
+  // 8192 x 4096 42.4 and 40.4, 16384 x 1024 48.2 and 29.8; with 256 and 4096:
+  // 2048 x 16384 44.1 and 53.1. 8192 x 5120 fp32 rows with 512, 819 and 4096:
+  // 94.4, 103 and 94.0. Codes of 16384 x 8192 alone with 512 and 4096: 75.7 and
+  // 68.7.
+  const uint32_t blocks = !NORM || NT * P <= 512 ? 4096 : NT == 512 ? 512 : 256;
   return launch_kernel(rows_kernel<IO, SL, NT, P, VEC, NORM, STREAM>,
                        dim3(static_cast<uint32_t>(l.rows < blocks ? l.rows : blocks)), dim3(NT), stream, l);
 }
@@ -472,10 +606,12 @@ hipError_t launch_rows(const RowsLaunch& l, hipStream_t stream) {
 }
 
 uint32_t norm_backward_parts(uint64_t rows, uint32_t h) {
-  // Fewer than for the forward pass: each leaves a row of partial sums
-  // (16384 x 8192 bf16: 256 work-groups 196 us, 512 207, 1024 214; 4096 x
-  // 4096 f16: 256 35.0 us, 512 32.3, 1024 35.5).
-  const uint32_t parts = rows_blocks(1u << 21, h);
+  // One a CU: each leaves a row of partial sums, and holds half of a CU's
+  // registers. Two for narrow rows, if they then have rows to load ahead. us
+  // with 256, 512 and 1024: 16384 x 8192 bf16 179, 190 and 192; 1021 x 7168
+  // bf16 17.5, 19.7 and 26.1; 4096 x 4096 f16 28.3, 29.6 and 33.3; 8192 x 2048
+  // bf16 37.0, 29.2 and 31.9; 500 x 2048 bf16 8.0 and 9.7.
+  const uint32_t parts = h <= 256 * kPiece && rows >= 4 * 512 ? 512 : 256;
   return static_cast<uint32_t>(rows < parts ? rows : parts);
 }
 

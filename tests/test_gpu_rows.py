@@ -51,6 +51,43 @@ def test_norm(gpu, t, h, x_format, layout, kind):
     _check_norm(x, r, w, kind, x_format, layout, total, codes, scales, "norm")
 
 
+@pytest.mark.parametrize("kind,x_format", [("f32", "e5m2"), ("f32", "e4m3fn"), ("bf16", "e4m3fn"), ("f16", "e5m2")])
+def test_norm_rounds_once_to_codes_of_e8m0_scales(gpu, kind, x_format):
+    """Of 2^22 values, none falls on the far side of a border between two
+    codes: y is exact to far more than binary32 when its code is chosen."""
+    t, h = 1024, 4096
+    rng = np.random.default_rng([t, h, len(kind)])
+    x, r, w = _norm_case(rng, t, h, kind)
+    codes, scales = empty_codes(t, h, "e8m0_block32")
+    total = torch.empty(t, h, dtype=TORCH[kind], device="cuda")
+    qrs.add_rms_norm_quantize(device(x, kind), device(r, kind), device(w, kind), EPS, total, codes, scales, x_format,
+                              "e8m0_block32")
+    y = rms_norm(rounded_sum(x, r, kind), w, EPS)
+    assert_codes(codes.cpu().numpy(), scales.cpu().numpy(), y, 2.0 ** -40, x_format, "e8m0_block32")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("x_format,layout", [("int8", "f32_row"), ("e4m3fn", "f32_group128"), ("e5m2", "e8m0_block32")])
+@pytest.mark.parametrize("h", [1024, 5120, 16384])
+def test_norm_of_rows_whose_squares_leave_binary32(gpu, h, x_format, layout, kind):
+    """Rows of about 2^100 and 2^-100 between rows of ordinary size."""
+    t = 1700  # several rows a work-group at any width
+    rng = np.random.default_rng([t, h, 3])
+    x, r, w = values(rng, (t, h), kind), values(rng, (t, h), kind), values(rng, h, kind, 0.1) + np.float32(1)
+    w = round_to(w, kind)
+    size = np.exp2(rng.choice([0, 0, 100, -100, 62, -62], t)).astype(np.float32)
+    x, r = (round_to(v * size[:, None], kind) for v in (x, r))
+    x[5] = r[5] = 0
+    codes, scales = empty_codes(t, h, layout)
+    total = torch.empty(t, h, dtype=TORCH[kind], device="cuda")
+    eps = 2.0 ** -126
+    qrs.add_rms_norm_quantize(device(x, kind), device(r, kind), device(w, kind), eps, total, codes, scales, x_format,
+                              layout)
+    s = rounded_sum(x, r, kind)
+    assert np.array_equal(host(total), s)
+    assert_codes(codes.cpu().numpy(), scales.cpu().numpy(), rms_norm(s, w, eps), norm_rel(h), x_format, layout)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("t,h", [(1, 1), (5, 7), (3, 100), (4, 1001), (2, 8200), (9, 4100), (2, 65535), (66, 33)])
 def test_norm_with_row_scales_at_any_width(gpu, t, h, kind):
