@@ -26,10 +26,11 @@
  * here are this library's own.
  *
  * Ownership: the caller owns every device buffer and the stream; the library
- * owns only the plan. No call allocates device memory; the workspace size is
- * always 0. A plan is immutable and may be used by any number of concurrent
- * qrs_run calls on different streams. The launching calls (qrs_run,
- * qrs_run_all_shares, qrs_run_strided, qrs_quantize) enqueue kernels only --
+ * owns only the plan. No call allocates device memory; the workspace size of
+ * a plan is always 0. A plan is immutable and may be used by any number of
+ * concurrent qrs_run calls on different streams. The launching calls (qrs_run,
+ * qrs_run_all_shares, qrs_run_strided, qrs_quantize and the operators between
+ * two shares) enqueue kernels only --
  * no allocation, memset or synchronisation -- so they may be captured in a
  * HIP graph.
  *
@@ -332,10 +333,12 @@ qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scal
  * and y as codes and scales.
  *
  * s is rounded once to the activations' type and stored in sum_out; y is
- * computed from the stored s in binary64, rounded once to binary32 and
- * quantized by qrs_quantize's rules for QRS_SCALE_F32_GROUP128 and
- * QRS_SCALE_E8M0_BLOCK32. QRS_SCALE_F32_ROW takes the whole row as one group
- * of the same rule. A group that holds a NaN or an infinity gets a NaN or
+ * computed from the stored s in binary32 (the sum of squares mostly in
+ * binary64) to within 5 * 2^-24 of itself, also where squares leave binary32's
+ * range, and quantized by qrs_quantize's rules for QRS_SCALE_F32_GROUP128 and
+ * QRS_SCALE_E8M0_BLOCK32. With the latter, a y too close to the border between
+ * two codes to tell is taken again in binary64. QRS_SCALE_F32_ROW takes the
+ * whole row as one group of the same rule. A group that holds a NaN or an infinity gets a NaN or
  * infinite scale (E8M0 code 255), so that it stays visible; its codes are
  * unspecified.
  *

@@ -129,8 +129,8 @@ __device__ __forceinline__ float round_to_odd(double y) {
 
 // One lane's pieces of a row and what makes values for codes of them.
 //
-// y = s * r * weight is taken in binary32, within 1.5 * 2^-24 of itself, and in
-// binary64 where that does not do: in rows whose squares leave binary32's
+// y = s * r * weight is taken in binary32, within 1.5 * 2^-24 of the product of
+// its operands, and in binary64 where that does not do: in rows whose squares leave binary32's
 // range, and, with E8M0 scales, where y is so close to a border between two
 // codes that the error could decide which one it gets. (In binary64 always, it
 // takes the registers of a second work-group: 8192 x 5120 fp32 117 us.)
@@ -258,8 +258,10 @@ __device__ __forceinline__ void quantize_row(const Values& values, const RowsLau
 // is quantized. Work-group b takes rows b, b + gridDim, ...; the next row's
 // operands are under way while a row is reduced and written.
 //
-// The squares of a piece are added in binary32, the pieces in binary64. If
-// the sum is not well inside binary32's range, it is taken again in binary64.
+// The squares of a piece are added in binary32 (at most 7 roundings, so r is
+// within 3.5 * 2^-24; their signs differ from piece to piece, which leaves far
+// less of a row), the pieces in binary64. If the sum is not well inside
+// binary32's range, it is taken again in binary64.
 template <int IO, int SL, int NT, int P8, bool VEC, bool NORM, bool STREAM>
 __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
