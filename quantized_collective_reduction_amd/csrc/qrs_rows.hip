@@ -387,10 +387,10 @@ hipError_t launch_rows_as(const RowsLaunch& l, hipStream_t stream) {
   // Else many, which even out by themselves. Norm of bf16 rows, us with 512
   // and 4096 work-groups: 2048 x 8192 23.8 and 24.5, 16384 x 8192 148 and 151,
   // 8192 x 4096 42.4 and 40.4, 16384 x 1024 48.2 and 29.8; with 256 and 4096:
-  // 2048 x 16384 44.1 and 53.1. 8192 x 5120 fp32 rows with 512, 819 and 4096:
+  // 2048 x 16384 44.1 and 53.1. 8192 x 5120 fp32 (512 x 2) with 512, 819 and 4096:
   // 94.4, 103 and 94.0. Codes of 16384 x 8192 alone with 512 and 4096: 75.7 and
   // 68.7.
-  const uint32_t blocks = !NORM || NT * P <= 512 ? 4096 : NT == 512 ? 512 : 256;
+  const uint32_t blocks = !NORM || NT * P <= 512 ? 4096 : NT < 1024 ? 512 : 256;
   return launch_kernel(rows_kernel<IO, SL, NT, P, VEC, NORM, STREAM>,
                        dim3(static_cast<uint32_t>(l.rows < blocks ? l.rows : blocks)), dim3(NT), stream, l);
 }
@@ -401,6 +401,11 @@ hipError_t launch_rows_sized(const RowsLaunch& l, hipStream_t stream) {
   if constexpr (VEC) {
     if (l.h <= 256 * 1 * kPiece) return launch_rows_as<IO, SL, 256, 1, VEC, NORM, STREAM>(l, stream);
     if (l.h <= 512 * 1 * kPiece) return launch_rows_as<IO, SL, 512, 1, VEC, NORM, STREAM>(l, stream);
+    // E8M0 codes of 4096 x 4224 and 4096 x 6144 bf16: 31.2 and 34.4 us with
+    // 512 x 2, 27.0 and 32.2 with 768 x 1; fp32 scales 32.0 and 31.7, row
+    // scales (4096 x 6144) 33.0 and 34.5.
+    if constexpr (SL == kScaleE8M0Block32)
+      if (l.h <= 768 * 1 * kPiece) return launch_rows_as<IO, SL, 768, 1, VEC, NORM, STREAM>(l, stream);
   }
   if (l.h <= 512 * 2 * kPiece) return launch_rows_as<IO, SL, 512, 2, VEC, NORM, STREAM>(l, stream);
   if constexpr (VEC) {
