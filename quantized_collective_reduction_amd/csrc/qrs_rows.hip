@@ -258,10 +258,11 @@ __device__ __forceinline__ void quantize_row(const Values& values, const RowsLau
 // is quantized. Work-group b takes rows b, b + gridDim, ...; the next row's
 // operands are under way while a row is reduced and written.
 //
-// The squares of a piece are added in binary32 (at most 7 roundings, so r is
+// The squares are added in binary64 where codes go by more than binary32 (E8M0
+// scales); otherwise those of a piece in binary32 (at most 7 roundings, so r is
 // within 3.5 * 2^-24; their signs differ from piece to piece, which leaves far
-// less of a row), the pieces in binary64. If the sum is not well inside
-// binary32's range, it is taken again in binary64.
+// less of a row) and the pieces in binary64. If the sum is not well inside
+// binary32's range, the row is taken in binary64.
 template <int IO, int SL, int NT, int P8, bool VEC, bool NORM, bool STREAM>
 __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
@@ -332,10 +333,15 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
       double ss = 0.0;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        float q = v[p][0] * v[p][0];
+        if constexpr (SL == kScaleE8M0Block32) {
 #pragma unroll
-        for (int j = 1; j < E; ++j) q = __builtin_fmaf(v[p][j], v[p][j], q);
-        ss += q;
+          for (int j = 0; j < E; ++j) ss = __builtin_fma(v[p][j], static_cast<double>(v[p][j]), ss);
+        } else {
+          float q = v[p][0] * v[p][0];
+#pragma unroll
+          for (int j = 1; j < E; ++j) q = __builtin_fmaf(v[p][j], v[p][j], q);
+          ss += q;
+        }
       }
       ss = row_sum(ss);
       values.wide = !(ss > 0x1p-70 && ss < 0x1p120);  // the same in every lane
