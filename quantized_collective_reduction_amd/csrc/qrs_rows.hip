@@ -345,7 +345,7 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
       }
       ss = row_sum(ss);
       values.wide = !(ss > 0x1p-70 && ss < 0x1p120);  // the same in every lane
-      if (values.wide) {
+      if (SL != kScaleE8M0Block32 && values.wide) {
         turn ^= 1;
         ss = 0.0;
 #pragma unroll
