@@ -211,6 +211,16 @@ __device__ __forceinline__ float wave_sum(float v) {
          (__builtin_bit_cast(float, lane_value(b, 32)) + __builtin_bit_cast(float, lane_value(b, 48)));
 }
 
+// Between writes to LDS and reads of them by other lanes of the same wave, and
+// between such reads and the next writes. LDS serves a wave's accesses in
+// order, so this costs no instruction; it keeps the compiler from moving one
+// across the other where a single lane's addresses differ.
+__device__ __forceinline__ void lds_wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
 
 template <int XF>

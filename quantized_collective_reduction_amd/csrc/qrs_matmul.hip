@@ -642,10 +642,12 @@ __global__ __launch_bounds__((Pipe<TM, TN, WTM>::kThreads), 1) void pipe_kernel(
     // column off one bank.
     auto stage_sums = [&](int i) {
       __builtin_amdgcn_sched_barrier(0);  // one fragment's values in registers at a time
+      lds_wave_order();
       settle(acc[i]);
 #pragma unroll
       for (int g = 0; g < FN; ++g)  // lane l holds channels 4 (l / 16) .. + 3 of token l % 16
         *reinterpret_cast<i32x4*>(sums + lane % 16 * kWaveN + ((4 * g + lane / 16) ^ (lane % 16)) * 4) = acc[i][g];
+      lds_wave_order();
     };
     auto values = [&](uint32_t t, uint32_t unit, float scale, float* v) {
       const i32x4* row = reinterpret_cast<const i32x4*>(sums + t * kWaveN);
@@ -789,6 +791,7 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
       for (int t = 0; t < kLinesB; ++t) put(t, lb[q][t]);
 #pragma unroll
       for (int t = 0; t < 2 * MT; ++t) put(kLinesB + t, la[q][t]);
+      lds_wave_order();
 #pragma unroll
       for (int unit = 0; unit < 2; ++unit) {
         i32x4 fb[FB];
@@ -801,6 +804,7 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
           for (int h = 0; h < FB; ++h) acc[i][h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h], fa, acc[i][h], 0, 0, 0);
         }
       }
+      lds_wave_order();
     }
   }
 

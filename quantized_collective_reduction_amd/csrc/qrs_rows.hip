@@ -26,9 +26,6 @@ namespace {
 
 using namespace dev;
 
-// s_waitcnt for LDS and scalar loads alone (lgkmcnt 0, vmcnt and expcnt at most).
-constexpr int kWaitLds = 0xC07F;
-
 // A piece (16 bytes) as it lies in memory (VEC), so that rows under way cost half the
 // registers for 16-bit types; otherwise as floats. STREAM: loads that leave no
 // copy in the caches.
@@ -82,12 +79,12 @@ struct RawPiece<kOutF16, true> : RawPiece16<kOutF16> {};
 // pass, 1074 MB: 195 us, as a stream 174; 59 MB, found there: 20.2 and 21.6).
 constexpr uint64_t kStreamBytes = uint64_t{256} << 20;
 
-// The wave's own barrier: LDS alone. A fence would also wait for the loads of
-// the next row.
+// A work-group barrier that orders LDS accesses alone: __syncthreads would also
+// wait for the loads of the next row.
 __device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_s_waitcnt(kWaitLds);
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
