@@ -369,8 +369,10 @@ qrs_status qrs_add_rms_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype io
  *   grad_weight = sum over tokens of grad_y * s * r
  *
  * grad_x is the gradient of s, and so of x and of residual alike. grad_sum
- * is what reaches s by the residual stream; NULL = zero. All arithmetic is
- * binary32; grad_x is rounded once to io_dtype, grad_weight is binary32.
+ * is what reaches s by the residual stream; NULL = zero. The arithmetic is
+ * binary32 (the two sums along a row mostly binary64), and binary64 for rows
+ * whose sums leave binary32's range, before one rounding to binary32; then
+ * grad_x is rounded once to io_dtype. grad_weight is added in binary32.
  *
  *   grad_x      may be grad_y or grad_sum themselves (same pointer and
  *               stride).

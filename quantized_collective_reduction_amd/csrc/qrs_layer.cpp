@@ -255,6 +255,7 @@ qrs_status qrs_rms_norm_backward(int64_t tokens, int64_t h, qrs_out_dtype io_dty
   for (int i = 0; i < n; ++i) l.vec = l.vec && in[i].rows_on(16);
   l.h = static_cast<uint32_t>(h);
   l.eps = eps;
+  l.inv_h = 1.0 / static_cast<double>(h);
   l.rows = static_cast<uint64_t>(tokens);
   l.grad_y = grad_y;
   l.grad_y_stride = static_cast<uint64_t>(grad_y_row_stride);

@@ -47,6 +47,7 @@ struct NormBackwardLaunch {
   bool vec;  // h % 8 == 0, and every row starts on a 16-byte boundary
   uint32_t h;
   float eps;
+  double inv_h;  // 1 / h
   uint64_t rows;
   const void* grad_y;
   uint64_t grad_y_stride;

@@ -28,7 +28,8 @@ using namespace dev;
 
 // A piece (16 bytes) as it lies in memory (VEC), so that rows under way cost half the
 // registers for 16-bit types; otherwise as floats. STREAM: loads that leave no
-// copy in the caches.
+// copy in the caches. renew(): from here on the values are to be taken as new
+// ones, so that what was unpacked from them is not kept in registers.
 template <int IO, bool VEC>
 struct RawPiece {
   float v[kPiece16<IO>];
@@ -39,6 +40,14 @@ struct RawPiece {
   __device__ __forceinline__ void get(float* to) const {
 #pragma unroll
     for (int j = 0; j < kPiece16<IO>; ++j) to[j] = v[j];
+  }
+  __device__ __forceinline__ void put(const float* from) {
+#pragma unroll
+    for (int j = 0; j < kPiece16<IO>; ++j) v[j] = from[j];
+  }
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int j = 0; j < kPiece16<IO>; ++j) asm volatile("" : "+v"(v[j]));
   }
 };
 template <int IO>
@@ -54,6 +63,11 @@ struct RawPiece16 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) unpack2<IO>(w[j], to + 2 * j);
   }
+  __device__ __forceinline__ void put(const float* from) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack2<IO>(from[2 * j], from[2 * j + 1]);
+  }
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(w)); }
 };
 template <>
 struct RawPiece<kOutF32, true> {
@@ -68,6 +82,8 @@ struct RawPiece<kOutF32, true> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) to[j] = w[j];
   }
+  __device__ __forceinline__ void put(const float* from) { w = f32x4{from[0], from[1], from[2], from[3]}; }
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(w)); }
 };
 template <>
 struct RawPiece<kOutBF16, true> : RawPiece16<kOutBF16> {};
@@ -101,6 +117,12 @@ __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) row[i] = from(v, [i](uint32_t x) { return lane_value(x, 16 * i); });
   return (row[0] + row[1]) + (row[2] + row[3]);
+}
+
+// 1 / sqrt(m): the hardware's estimate (about 2^-24) and one Newton step.
+__device__ __forceinline__ double inverse_root(double m) {
+  const double q = __builtin_amdgcn_rsq(m);
+  return __builtin_isinf(m) ? 0.0 : q * __builtin_fma(-0.5 * m * q, q, 1.5);
 }
 
 // Values that are to be taken as new ones: what is made of them is not kept
@@ -353,10 +375,7 @@ __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
         }
         ss = row_sum(ss);
       }
-      // The hardware's estimate (about 2^-24) and one Newton step.
-      const double m = ss * a.inv_h + static_cast<double>(a.eps);
-      const double q = __builtin_amdgcn_rsq(m);
-      values.r = __builtin_isinf(m) ? 0.0 : q * __builtin_fma(-0.5 * m * q, q, 1.5);
+      values.r = inverse_root(ss * a.inv_h + static_cast<double>(a.eps));
     }
 
     uint32_t amax = 0;
@@ -440,17 +459,34 @@ hipError_t launch_rows_io(const RowsLaunch& l, hipStream_t stream) {
 
 // ---- backward ----------------------------------------------------------
 
-// With r = 1 / sqrt(mean(s^2) + eps) and d = weight * grad_y:
-//   grad_x      = grad_sum + r * (d - s * (r^2 * mean(d * s)))
-//   grad_weight = sum over tokens of grad_y * s * r
-// Both row sums (s^2 and d * s) are taken in one reduction. Work-group b
-// takes rows b, b + gridDim, ...; the next row's operands are under way while
-// a row is reduced and written. It keeps its columns' share of grad_weight in
-// registers and leaves one row of partial sums in the workspace, and
-// grad_weight_kernel adds those rows in order: a fixed order without atomics.
+// With r = 1 / sqrt(mean(s^2) + eps), u = s * r and d = weight * grad_y:
+//   grad_x      = grad_sum + r * (d - u * mean(d * u))
+//   grad_weight = sum over tokens of grad_y * u
+// Both row sums (s^2 and d * s) are taken in one reduction: those of a piece
+// in binary32, the pieces in binary64. |u| is at most sqrt(h) and |u * mean|
+// at most the largest |d * u|, so apart from these sums and d itself nothing
+// leaves binary32's range before the result does. Where a sum is not well
+// inside it, the row is taken again in binary64.
+//
+// d is held times 2^64 (kGradScale, in the weight; r takes it back), which is
+// exact: then the products of an ordinary row have room on both sides, and a
+// sum of d * s that is zero means that there are no gradients (as in rows of
+// padding), or none that the result could show. Binary16 products need no room.
+// A weight of 2^60 or more leaves none: its lane keeps its weights as they are
+// and makes the sum NaN, so that every row is taken in binary64.
+//
+// Work-group b takes rows b, b + gridDim, ...; the next row's operands are
+// under way while a row is reduced and written. It keeps its columns' share of
+// grad_weight in registers and leaves one row of partial sums in the workspace,
+// and grad_weight_kernel adds those rows in order: a fixed order without
+// atomics.
+template <int IO>
+constexpr float kGradScale = IO == kOutF16 ? 1.0f : 0x1p64f;
+
 template <int IO, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLaunch a) {
-  __shared__ float parts[2][2 * (NT / 64)];
+  constexpr int kWaves = NT / 64;
+  __shared__ double parts[2][2 * kWaves];
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;
   const int lane = threadIdx.x;
   constexpr int kSize = kOutSize<IO>;
@@ -462,6 +498,25 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     w[p].template load<false>(a.weight, (p * NT + lane) * E, a.h);
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[p][j] = 0.0f;
+  }
+  float no_sum = 0.0f;  // NaN if the lane's weights are not scaled
+  if constexpr (kGradScale<IO> != 1.0f) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float wv[E];
+      w[p].get(wv);
+#pragma unroll
+      for (int j = 0; j < E; ++j) no_sum = __builtin_fabsf(wv[j]) < 0x1p60f ? no_sum : __builtin_nanf("");
+    }
+    const float scale = no_sum == 0.0f ? kGradScale<IO> : 1.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float wv[E];
+      w[p].get(wv);
+#pragma unroll
+      for (int j = 0; j < E; ++j) wv[j] *= scale;
+      w[p].put(wv);
+    }
   }
   struct Operands {
     Raw dy[P], s[P], g[P];
@@ -483,54 +538,112 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
 
   load_row(blockIdx.x);
   const float keep = a.grad_sum != nullptr ? 1.0f : 0.0f;
+  // Alternating halves of `parts`: a wave that is a row ahead writes the
+  // other half, and the next barrier keeps it from going further.
   int turn = 0;
-  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-    const Operands now = next;
-    if (row + gridDim.x < a.rows) load_row(row + gridDim.x);
-    float ss = 0.0f, ds = 0.0f;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float wv[E], dy[E], s[E];
-      w[p].get(wv);
-      now.dy[p].get(dy);
-      now.s[p].get(s);
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        ss += s[j] * s[j];
-        ds += wv[j] * dy[j] * s[j];
-      }
-    }
-    // Alternating halves of `parts`: a wave that is a row ahead writes the
-    // other half, and the next barrier keeps it from going further.
+  auto row_sums = [&](double& ss, double& ds) {
     ss = wave_sum(ss);
     ds = wave_sum(ds);
-    constexpr int kWaves = NT / 64;
     if (lane % 64 == 0) {
       parts[turn][lane / 64] = ss;
       parts[turn][kWaves + lane / 64] = ds;
     }
     lds_barrier();
-    ss = ds = 0.0f;
+    ss = ds = 0.0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
       ss += parts[turn][i];
       ds += parts[turn][kWaves + i];
     }
-    const float n = static_cast<float>(a.h);
-    const float r = 1.0f / __builtin_sqrtf(ss / n + a.eps);
-    const float along = r * r * (ds / n);
+  };
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    Operands now = next;
+    if (row + gridDim.x < a.rows) load_row(row + gridDim.x);
+    auto operands = [&](int p, float (&wv)[E], float (&dy)[E], float (&s)[E]) {
+      w[p].get(wv);
+      now.dy[p].get(dy);
+      now.s[p].get(s);
+    };
+    auto renew = [&]() {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        w[p].renew();
+        now.dy[p].renew();
+        now.s[p].renew();
+      }
+    };
+    // 1024 lanes leave 128 registers each, which unpacked values kept for the
+    // second pass overflow (4096 x 16384 bf16 161 us, renewed 101); with fewer
+    // lanes unpacking twice costs more (16384 x 8192 bf16 176 us, renewed 186).
+    constexpr bool kRenew = NT == 1024;
+    double ss = 0.0, ds = no_sum;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float wv[E], dy[E], s[E];
+      operands(p, wv, dy, s);
+      float q = s[0] * s[0], t = wv[0] * dy[0] * s[0];
+#pragma unroll
+      for (int j = 1; j < E; ++j) {
+        q = __builtin_fmaf(s[j], s[j], q);
+        t = __builtin_fmaf(wv[j] * dy[j], s[j], t);
+      }
+      ss += q;
+      ds += t;
+    }
+    row_sums(ss, ds);
+    if (kRenew) renew();
+    double r = inverse_root(ss * a.inv_h + static_cast<double>(a.eps)), mean = r * (ds * a.inv_h);
+    // The same in every lane.
+    const bool wide = !(ss > 0x1p-70 && ss < 0x1p120 && __builtin_fabs(mean) < 0x1p110 &&
+                        (ds == 0.0 || __builtin_fabs(ds) > 0x1p-100));
+    const double unscale = no_sum == 0.0f ? 1.0 / kGradScale<IO> : 1.0;
+    if (wide) {
+      turn ^= 1;
+      ss = ds = 0.0;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float wv[E], dy[E], s[E];
+        operands(p, wv, dy, s);
+        as_new(wv);
+        as_new(dy);
+        as_new(s);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          ss = __builtin_fma(s[j], static_cast<double>(s[j]), ss);
+          ds = __builtin_fma(wv[j] * unscale * dy[j], static_cast<double>(s[j]), ds);
+        }
+      }
+      row_sums(ss, ds);
+      if (kRenew) renew();
+      r = inverse_root(ss * a.inv_h + static_cast<double>(a.eps));
+      mean = r * (ds * a.inv_h);
+    }
+    const float r32 = static_cast<float>(r), mean32 = static_cast<float>(mean), back = r32 * (1.0f / kGradScale<IO>);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t c = (p * NT + lane) * E;
       float wv[E], dy[E], s[E], g[E];
-      w[p].get(wv);
-      now.dy[p].get(dy);
-      now.s[p].get(s);
+      operands(p, wv, dy, s);
       now.g[p].get(g);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        dw[p][j] += dy[j] * (s[j] * r);
-        g[j] = (keep != 0.0f ? g[j] : 0.0f) + r * (wv[j] * dy[j] - s[j] * along);
+      for (int j = 0; j < E; ++j) g[j] = keep != 0.0f ? g[j] : 0.0f;
+      if (wide) {
+        as_new(wv);
+        as_new(dy);
+        as_new(s);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const double u = s[j] * r;
+          dw[p][j] += static_cast<float>(dy[j] * u);
+          g[j] = static_cast<float>(g[j] + r * (wv[j] * unscale * dy[j] - u * mean));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const float u = s[j] * r32;
+          dw[p][j] += dy[j] * u;
+          g[j] += back * (wv[j] * dy[j] - u * mean32);
+        }
       }
       store_piece<IO, VEC, E>(static_cast<char*>(a.grad_x) + row * a.grad_x_stride * kSize, c, a.h, g);
     }
