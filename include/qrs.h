@@ -405,7 +405,8 @@ qrs_status qrs_quantize_rows(int64_t rows, int64_t cols, qrs_out_dtype in_dtype,
  *
  *   gated      1: b is [2n, k], n gate channels and then n up channels, and
  *              out = silu(g) * u of the two scaled products, with
- *              silu(g) = g / (1 + exp(-g)) in binary32.
+ *              silu(g) = g / (1 + exp(-g)) in binary32, within five half
+ *              units of its last place for every finite g.
  *   k          in [1, 131071]; m, n below 2^31.
  *   a_scales   float32 [m]; b_scales float32 [n], or [2n] if gated.
  */

@@ -30,21 +30,25 @@ constexpr uint32_t kCus = 256;
 
 // ---- epilogue ----------------------------------------------------------
 
-// g / (1 + exp(-g)). exp as a power of two whose exponent's rounding error is
-// put back as a factor, 1 / d as the hardware's estimate and one Newton step:
-// each within a few units of the last place, for a third of the instructions
-// of the library's exp and divide (512 tokens by 5120 ups, k = 1024: 17.5 us
-// -> 16.5). Beyond 87 the quotient is 1, beyond -87 (there less than 2^-125)
-// it is 0, so that nothing between overflows.
+// g / (1 + exp(-g)) as g * n / (1 + e) with e = exp(-|g|) and n = 1, or e for
+// negative g: nothing overflows, and where e would be subnormal (g < -64) it is
+// held times 2^64 and g times 2^-64. exp as a power of two whose exponent's
+// rounding error is put back as a factor, 1 / d as the hardware's estimate and
+// one Newton step: each within a few units of the last place, for a third of
+// the instructions of the library's exp and divide (512 tokens by 5120 ups,
+// k = 1024: 17.5 us -> 16.5). Beyond 200, e is 0 whatever its scale.
 __device__ __forceinline__ float silu(float g) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f, kLimit = 87.0f;
-  const float x = __builtin_amdgcn_fmed3f(g, -kLimit, kLimit);
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+  const float x = __builtin_fminf(__builtin_fabsf(g), 200.0f);
+  const bool far = g < -64.0f;
   const float p = -x * kLog2e;
   const float low = __builtin_fmaf(-x, kLog2eLow, __builtin_fmaf(-x, kLog2e, -p));
-  const float e = __builtin_amdgcn_exp2f(p);
-  const float d = 1.0f + __builtin_fmaf(e, low * kLn2, e);
+  const float e0 = __builtin_amdgcn_exp2f(far ? p + 64.0f : p);  // this sum is exact: |p| is at least 92
+  const float e = __builtin_fmaf(e0, low * kLn2, e0);
+  const float d = 1.0f + e;  // far: e, 2^-28 at most even so, has no part in it
   const float r = __builtin_amdgcn_rcpf(d);
-  return g * (g < -kLimit ? 0.0f : __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r));
+  const float inverse = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  return (far ? g * 0x1p-64f : g) * (g < 0.0f ? e * inverse : inverse);
 }
 
 // What a kernel instance writes.
