@@ -701,7 +701,11 @@ def _workspace(workspace, nbytes, like, stream):
     if stream is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        if isinstance(stream, int):
+            # ExternalStream takes the default stream's handle, 0, for none given and answers with one of its own.
+            stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+                      else torch.cuda.default_stream(like.device))
+        with torch.cuda.stream(stream):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     return ws.data_ptr(), nbytes, ws
 
