@@ -46,3 +46,14 @@ def test_the_workspace_is_allocated_under_the_stream_that_uses_it(recorded):
         assert nbytes == 64 and ws.numel() == 64
     # 0 is the handle of the default stream, not of a stream of its own.
     assert recorded == [None, given, ("external", 0x7F00, "cuda:3"), ("default", "cuda:3")]
+
+
+@pytest.mark.parametrize("missing", [(), ("_cuda_getCurrentRawStream",), ("_cuda_getDevice",)])
+def test_the_current_stream_without_torchs_own_functions(monkeypatch, missing):
+    given = {"_cuda_getCurrentRawStream": lambda device: 1000 + device, "_cuda_getDevice": lambda: 5}
+    monkeypatch.setattr(torch, "_C", types.SimpleNamespace(**{k: f for k, f in given.items() if k not in missing}))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 5)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=1005))
+    monkeypatch.setattr(qrs, "_current_stream_call", qrs._current_stream_call.__wrapped__)
+    assert qrs._stream_handle(None) == 1005
+    assert qrs._stream_handle(0) == 0 and qrs._stream_handle(_Given()) == 77
