@@ -407,7 +407,8 @@ qrs_status qrs_quantize_rows(int64_t rows, int64_t cols, qrs_out_dtype in_dtype,
  *              out = silu(g) * u of the two scaled products, with
  *              silu(g) = g / (1 + exp(-g)) in binary32, within five half
  *              units of its last place for every finite g.
- *   k          in [1, 131071]; m, n below 2^31.
+ *   k          in [1, 131071].
+ *   m, n       below 2^31, and ceil(m / 64) * ceil(n / 64) below 2^24.
  *   a_scales   float32 [m]; b_scales float32 [n], or [2n] if gated.
  */
 qrs_status qrs_matmul_int(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype, const void* a,
@@ -425,6 +426,29 @@ qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype 
                                    qrs_scale_layout scale_layout, const void* a, int64_t a_row_stride,
                                    const float* a_scales, const void* b, int64_t b_row_stride, const float* b_scales,
                                    void* codes, int64_t codes_row_stride, void* scales, void* stream);
+
+/*
+ * The kernel and grid that qrs_matmul_int (quantize = 0; scale_layout unused)
+ * or qrs_matmul_int_quantize (quantize = 1; not gated) takes for contiguous
+ * operands of this shape on 16-byte boundaries, reported without launching
+ * anything. Host only.
+ *
+ *   blocks, threads_per_block  the grid; their product is below 2^32.
+ *   kernel                     0: general tiles; 1: up to 32 tokens; 2: waves
+ *                              that share k; 3: pipelined tiles, whose
+ *                              work-groups walk over them.
+ *   tile_m, tile_n             tokens and rows of b of a work-group's tile.
+ */
+typedef struct qrs_matmul_info {
+  uint64_t blocks;
+  uint32_t threads_per_block;
+  uint32_t kernel;
+  uint32_t tile_m;
+  uint32_t tile_n;
+} qrs_matmul_info;
+
+qrs_status qrs_matmul_launch_info(int64_t m, int64_t n, int64_t k, int gated, int quantize,
+                                  qrs_scale_layout scale_layout, qrs_matmul_info* info_out);
 
 /* Free a plan. NULL is accepted. Plans in use by queued runs may be freed:
  * qrs_run copies what the kernel needs into its launch arguments. */

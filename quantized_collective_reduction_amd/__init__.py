@@ -55,6 +55,7 @@ __all__ = [
     "stream_copy",
     "run_launch_info",
     "LaunchInfo",
+    "matmul_launch_info",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -114,6 +115,7 @@ EXPORTED_SYMBOLS = (
     "qrs_quantize_rows",
     "qrs_matmul_int",
     "qrs_matmul_int_quantize",
+    "qrs_matmul_launch_info",
 )
 
 
@@ -133,6 +135,18 @@ class LaunchInfo(ctypes.Structure):
 
     def as_dict(self):
         return {name: int(getattr(self, name)) for name, _ in self._fields_}
+
+
+class MatmulInfo(ctypes.Structure):
+    """qrs_matmul_info: the kernel a product takes (see matmul_launch_info)."""
+
+    _fields_ = [
+        ("blocks", ctypes.c_uint64),
+        ("threads_per_block", ctypes.c_uint32),
+        ("kernel", ctypes.c_uint32),
+        ("tile_m", ctypes.c_uint32),
+        ("tile_n", ctypes.c_uint32),
+    ]
 
 
 class QrsError(RuntimeError):
@@ -202,6 +216,8 @@ def load_library(path: str = LIB_PATH):
     lib.qrs_matmul_int_quantize.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, vp, c_i64, vp, vp, c_i64, vp, vp,
                                             c_i64, vp, vp]
     lib.qrs_matmul_int_quantize.restype = c_int
+    lib.qrs_matmul_launch_info.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, ctypes.POINTER(MatmulInfo)]
+    lib.qrs_matmul_launch_info.restype = c_int
     _lib = lib
     return lib
 
@@ -837,6 +853,20 @@ def run_launch_info(p: Plan, stream=None) -> dict:
     info = LaunchInfo()
     _check(lib.qrs_run_launch_info(p.handle, _stream_handle(stream), ctypes.byref(info)))
     return info.as_dict()
+
+
+def matmul_launch_info(m, n, k, gated=False, scale_layout=None) -> dict:
+    """The kernel ("tiles", "few_tokens", "mid" or "pipe"), its tile and its
+    grid that ``matmul_int8`` takes for contiguous operands of this shape, or
+    ``matmul_int8_quantize`` with a ``scale_layout`` (qrs_matmul_launch_info);
+    launches nothing."""
+    lib = load_library()
+    info = MatmulInfo()
+    layout = ScaleLayout.F32_GROUP128 if scale_layout is None else _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
+    _check(lib.qrs_matmul_launch_info(m, n, k, 1 if gated else 0, 0 if scale_layout is None else 1, layout,
+                                      ctypes.byref(info)))
+    return {"kernel": ("tiles", "few_tokens", "mid", "pipe")[info.kernel], "tile": (info.tile_m, info.tile_n),
+            "blocks": info.blocks, "threads_per_block": info.threads_per_block}
 
 
 def stream_copy(src, dst, nbytes=None, stream=None):

@@ -290,6 +290,12 @@ qrs_status check_matmul_shape(int64_t m, int64_t n, int64_t k, int gated) {
   return QRS_OK;
 }
 
+qrs_status check_quantized_shape(int64_t n, int gated) {
+  if (gated) return fail(QRS_ERR_INVALID_ARG, "the gated product is not written as codes");
+  if (n % 128 != 0) return fail(QRS_ERR_INVALID_ARG, "n %lld is not a multiple of 128", static_cast<long long>(n));
+  return QRS_OK;
+}
+
 // The checks of both products but for the output's type; out and scales as
 // the caller describes them (scales.p NULL: no scales).
 qrs_status matmul(qrs::MatmulLaunch* l, int64_t m, int64_t n, int64_t k, int gated, const void* a,
@@ -352,7 +358,7 @@ qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype 
                                    void* codes, int64_t codes_row_stride, void* scales, void* stream) {
   QRS_TRY(check_matmul_shape(m, n, k, 0));
   QRS_TRY(check_codes(x_dtype, scale_layout, false));
-  if (n % 128 != 0) return fail(QRS_ERR_INVALID_ARG, "n %lld is not a multiple of 128", static_cast<long long>(n));
+  QRS_TRY(check_quantized_shape(n, 0));
   const bool e8m0 = scale_layout == QRS_SCALE_E8M0_BLOCK32;
   const int64_t g = e8m0 ? 32 : 128;
   qrs::MatmulLaunch l;
@@ -364,6 +370,34 @@ qrs_status qrs_matmul_int_quantize(int64_t m, int64_t n, int64_t k, qrs_x_dtype 
   if (codes && !o.rows_on(16)) return fail(QRS_ERR_INVALID_ARG, "rows of codes are not on 16-byte boundaries");
   const Rows s = {"scales", scales, m, n / g, n / g, e8m0 ? 1 : 4};
   return matmul(&l, m, n, k, 0, a, a_row_stride, a_scales, b, b_row_stride, b_scales, o, s, stream);
+}
+
+qrs_status qrs_matmul_launch_info(int64_t m, int64_t n, int64_t k, int gated, int quantize,
+                                  qrs_scale_layout scale_layout, qrs_matmul_info* info_out) {
+  if (!info_out) return fail(QRS_ERR_INVALID_ARG, "null info pointer");
+  QRS_TRY(check_matmul_shape(m, n, k, gated));
+  if (quantize != 0 && quantize != 1) return fail(QRS_ERR_INVALID_ARG, "quantize must be 0 or 1");
+  if (quantize) {
+    QRS_TRY(check_codes(QRS_X_FP8_E4M3FN, scale_layout, false));
+    QRS_TRY(check_quantized_shape(n, gated));
+  }
+  qrs::MatmulLaunch l;
+  std::memset(&l, 0, sizeof(l));
+  l.m = static_cast<uint32_t>(m);
+  l.n = static_cast<uint32_t>(n);
+  l.k = static_cast<uint32_t>(k);
+  l.gated = gated != 0;
+  l.quantize = quantize != 0;
+  l.scale_layout = scale_layout == QRS_SCALE_E8M0_BLOCK32 ? qrs::kScaleE8M0Block32 : qrs::kScaleF32Group128;
+  l.vec = k % 16 == 0;
+  l.a_stride = l.b_stride = static_cast<uint64_t>(k);
+  const qrs::MatmulShape shape = qrs::matmul_shape(l);
+  info_out->blocks = shape.blocks;
+  info_out->threads_per_block = shape.threads;
+  info_out->kernel = static_cast<uint32_t>(shape.kernel.family);
+  info_out->tile_m = shape.kernel.tile_m;
+  info_out->tile_n = shape.kernel.tile_n;
+  return ok();
 }
 
 }  // extern "C"

@@ -94,8 +94,23 @@ struct MatmulLaunch {
 // The largest k whose sums of products (each at most 2^14) fit 32 bits.
 constexpr int64_t kMaxMatmulK = 131071;
 
-// Fails with hipErrorInvalidValue where m * n needs more work-items than a
-// grid holds (2^24 tiles of 64 x 128 outputs, or 64 x 64 gated).
+// Every shape of fewer than 2^24 tiles of 64 x 64 outputs has a kernel whose
+// grid a launch holds (fewer than 2^32 work-items); hipErrorInvalidValue,
+// launching nothing, beyond that.
 hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream);
+
+// The kernel that launch_matmul takes: its family, and its tile in tokens and
+// rows of b.
+enum MatmulFamily : uint32_t { kMatmulTiles = 0, kMatmulFewTokens = 1, kMatmulMid = 2, kMatmulPipe = 3 };
+struct MatmulKernel {
+  MatmulFamily family;
+  uint32_t tile_m, tile_n;
+};
+struct MatmulShape {
+  MatmulKernel kernel;
+  uint64_t blocks;
+  uint32_t threads;
+};
+MatmulShape matmul_shape(const MatmulLaunch& l);
 
 }  // namespace qrs

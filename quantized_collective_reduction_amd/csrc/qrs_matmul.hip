@@ -269,12 +269,25 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulLaunch a) {
   }
 }
 
+// A kernel and its grid for a call.
+struct Choice {
+  MatmulKernel id;
+  void (*kernel)(MatmulLaunch);
+  uint64_t blocks;
+  uint32_t threads;
+
+  // A HIP grid holds fewer than 2^32 work-items.
+  bool fits() const { return blocks * threads < uint64_t{1} << 32; }
+};
+
+uint64_t tiles_of(const MatmulLaunch& l, uint32_t tile_m, uint32_t tile_n) {
+  return static_cast<uint64_t>((l.m + tile_m - 1) / tile_m) * ((l.n + tile_n - 1) / tile_n);
+}
+
 template <bool VEC, int F>
-hipError_t launch_tiles(const MatmulLaunch& l, hipStream_t stream) {
-  const uint32_t tile_n = l.gated ? kTileN / 2 : kTileN;
-  const uint64_t tiles = static_cast<uint64_t>((l.m + kTileM - 1) / kTileM) * ((l.n + tile_n - 1) / tile_n);
-  if (tiles >= uint64_t{1} << 24) return hipErrorInvalidValue;  // 2^32 work-items
-  return launch_kernel(tile_kernel<VEC, F>, dim3(static_cast<uint32_t>(tiles)), dim3(256), stream, l);
+Choice general_tiles(const MatmulLaunch& l) {
+  constexpr uint32_t tile_n = F == kGated ? kTileN / 2 : kTileN;
+  return {{kMatmulTiles, kTileM, kTileN}, tile_kernel<VEC, F>, tiles_of(l, kTileM, tile_n), 256};
 }
 
 // ---- pipelined tile kernel ---------------------------------------------
@@ -850,21 +863,21 @@ __global__ __launch_bounds__(1024) void few_tokens_kernel(const MatmulLaunch a) 
 }
 
 template <int MT, int GW, int RB, int F>
-hipError_t launch_few(const MatmulLaunch& l, hipStream_t stream) {
+Choice few(const MatmulLaunch& l) {
   constexpr uint32_t out = (F == kGated ? RB / 2 : RB) * GW;
-  return launch_kernel(few_tokens_kernel<MT, GW, RB, F>, dim3((l.n + out - 1) / out), dim3(1024), stream, l);
+  return {{kMatmulFewTokens, 16 * MT, RB * GW}, few_tokens_kernel<MT, GW, RB, F>, tiles_of(l, 16 * MT, out), 1024};
 }
 
 template <int MT, int F>
-hipError_t launch_few_sized(const MatmulLaunch& l, hipStream_t stream) {
+Choice few_sized(const MatmulLaunch& l) {
   if constexpr (F == kCodes) {
     // Codes need a whole group of 128 or 32 channels in one work-group.
-    if (l.scale_layout == kScaleF32Group128) return launch_few<MT, 4, 32, F>(l, stream);
-    return launch_few<MT, 1, 32, F>(l, stream);
+    if (l.scale_layout == kScaleF32Group128) return few<MT, 4, 32, F>(l);
+    return few<MT, 1, 32, F>(l);
   } else {
     // Narrow work-groups where wide ones would leave half of the CUs idle.
     const uint32_t rows = F == kGated ? 2 * l.n : l.n;
-    return rows <= 16 * kCus ? launch_few<MT, 1, 16, F>(l, stream) : launch_few<MT, 1, 32, F>(l, stream);
+    return rows <= 16 * kCus ? few<MT, 1, 16, F>(l) : few<MT, 1, 32, F>(l);
   }
 }
 
@@ -1050,36 +1063,34 @@ __global__ __launch_bounds__(512, 1) void mid_kernel(const MatmulLaunch a) {
 }
 
 template <int TM, int TN, int KG, int S, int F>
-hipError_t launch_mid(const MatmulLaunch& l, hipStream_t stream) {
-  constexpr uint32_t out = F == kGated ? TN / 2 : TN;
-  const uint32_t tiles = ((l.m + TM - 1) / TM) * ((l.n + out - 1) / out);
-  return launch_kernel(mid_kernel<TM, TN, KG, S, F>, dim3(tiles), dim3(512), stream, l);
+Choice mid(const MatmulLaunch& l) {
+  return {{kMatmulMid, TM, TN}, mid_kernel<TM, TN, KG, S, F>, tiles_of(l, TM, F == kGated ? TN / 2 : TN), 512};
 }
 
 template <int TM, int TN, int WTM, int F>
-hipError_t launch_pipe(const MatmulLaunch& l, hipStream_t stream) {
+Choice pipe(const MatmulLaunch&) {
   using P = Pipe<TM, TN, WTM>;
-  return launch_kernel(pipe_kernel<TM, TN, WTM, F>, dim3(kCus * P::kPerCu), dim3(P::kThreads), stream, l);
+  return {{kMatmulPipe, TM, TN}, pipe_kernel<TM, TN, WTM, F>, kCus * P::kPerCu, P::kThreads};
 }
 
 // Rows of operands that the busiest CU loads with tiles of TM tokens by TN
 // rows of b: what a call's time goes by.
 template <int TM, int TN, int F>
-uint32_t rows_a_cu(const MatmulLaunch& l) {
-  constexpr uint32_t out = F == kGated ? TN / 2 : TN;
-  const uint32_t tiles = ((l.m + TM - 1) / TM) * ((l.n + out - 1) / out);
-  return (tiles + kCus - 1) / kCus * (TM + TN);
+uint64_t rows_a_cu(const MatmulLaunch& l) {
+  return (tiles_of(l, TM, F == kGated ? TN / 2 : TN) + kCus - 1) / kCus * (TM + TN);
 }
 
 template <int F>
-hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
-  if (!l.vec) return launch_tiles<false, F>(l, stream);
+Choice choose(const MatmulLaunch& l) {
+  if (!l.vec) return general_tiles<false, F>(l);
   // All but the general kernel hold offsets within a tile in 30 bits.
   const bool near = (256 + (F == kGated ? static_cast<uint64_t>(l.n) : 0)) * l.b_stride + l.k < kFar &&
                     256 * l.a_stride + l.k < kFar;
-  if (!near) return launch_tiles<true, F>(l, stream);
-  if (l.m <= 16) return launch_few_sized<1, F>(l, stream);
-  if (l.m <= 32) return launch_few_sized<2, F>(l, stream);
+  if (!near) return general_tiles<true, F>(l);
+  if (l.m <= 32) {
+    const Choice c = l.m <= 16 ? few_sized<1, F>(l) : few_sized<2, F>(l);
+    return c.fits() ? c : general_tiles<true, F>(l);
+  }
   // The tile whose busiest CU loads least. The pipelined kernel's rows count
   // a quarter more: its CU takes 33 to 39 GB/s (the matrix units and the
   // power limit bound it), the others' 39 to 47 once most CUs have a tile.
@@ -1088,30 +1099,41 @@ hipError_t launch_as(const MatmulLaunch& l, hipStream_t stream) {
   // rows 74 us and 384 rows 48; 4096 by 9472, 1536 rows 204 us and 1920 rows
   // 221.
   const bool narrow = F != kCodes || l.scale_layout == kScaleE8M0Block32;  // less than 128 channels a tile
-  uint32_t best = ~0u;
-  hipError_t (*launch)(const MatmulLaunch&, hipStream_t) = nullptr;
-  auto offer = [&](uint32_t rows, hipError_t (*f)(const MatmulLaunch&, hipStream_t)) {
-    if (rows < best) {
-      best = rows;
-      launch = f;
+  uint64_t least = ~uint64_t{0};
+  Choice best = general_tiles<true, F>(l);
+  auto offer = [&](uint64_t rows, const Choice& c) {
+    if (rows < least && c.fits()) {
+      least = rows;
+      best = c;
     }
   };
-  if (l.k > kBlockK) offer(rows_a_cu<256, 256, F>(l) * 5 / 4, launch_pipe<256, 256, 128, F>);
-  offer(rows_a_cu<128, 256, F>(l), launch_mid<128, 256, 2, 3, F>);
-  offer(rows_a_cu<128, 128, F>(l), launch_mid<128, 128, 2, 4, F>);
-  offer(rows_a_cu<64, 128, F>(l), launch_mid<64, 128, 2, 6, F>);
+  if (l.k > kBlockK) offer(rows_a_cu<256, 256, F>(l) * 5 / 4, pipe<256, 256, 128, F>(l));
+  offer(rows_a_cu<128, 256, F>(l), mid<128, 256, 2, 3, F>(l));
+  offer(rows_a_cu<128, 128, F>(l), mid<128, 128, 2, 4, F>(l));
+  offer(rows_a_cu<64, 128, F>(l), mid<64, 128, 2, 6, F>(l));
   if (narrow) {
-    offer(rows_a_cu<64, 64, F>(l), launch_mid<64, 64, 4, 4, F>);
-    offer(rows_a_cu<64, 32, F>(l), launch_mid<64, 32, 8, 3, F>);
+    offer(rows_a_cu<64, 64, F>(l), mid<64, 64, 4, 4, F>(l));
+    offer(rows_a_cu<64, 32, F>(l), mid<64, 32, 8, 3, F>(l));
   }
-  return launch(l, stream);
+  return best;
+}
+
+Choice choose(const MatmulLaunch& l) {
+  if (l.quantize) return choose<kCodes>(l);
+  return l.gated ? choose<kGated>(l) : choose<kValues>(l);
 }
 
 }  // namespace
 
+MatmulShape matmul_shape(const MatmulLaunch& l) {
+  const Choice c = choose(l);
+  return {c.id, c.blocks, c.threads};
+}
+
 hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream) {
-  if (l.quantize) return launch_as<kCodes>(l, stream);
-  return l.gated ? launch_as<kGated>(l, stream) : launch_as<kValues>(l, stream);
+  const Choice c = choose(l);
+  if (!c.fits()) return hipErrorInvalidValue;
+  return launch_kernel(c.kernel, dim3(static_cast<uint32_t>(c.blocks)), dim3(c.threads), stream, l);
 }
 
 }  // namespace qrs
