@@ -41,10 +41,6 @@ struct RawPiece {
 #pragma unroll
     for (int j = 0; j < kPiece16<IO>; ++j) to[j] = v[j];
   }
-  __device__ __forceinline__ void put(const float* from) {
-#pragma unroll
-    for (int j = 0; j < kPiece16<IO>; ++j) v[j] = from[j];
-  }
   __device__ __forceinline__ void renew() {
 #pragma unroll
     for (int j = 0; j < kPiece16<IO>; ++j) asm volatile("" : "+v"(v[j]));
@@ -63,10 +59,6 @@ struct RawPiece16 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) unpack2<IO>(w[j], to + 2 * j);
   }
-  __device__ __forceinline__ void put(const float* from) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack2<IO>(from[2 * j], from[2 * j + 1]);
-  }
   __device__ __forceinline__ void renew() { asm volatile("" : "+v"(w)); }
 };
 template <>
@@ -82,7 +74,6 @@ struct RawPiece<kOutF32, true> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) to[j] = w[j];
   }
-  __device__ __forceinline__ void put(const float* from) { w = f32x4{from[0], from[1], from[2], from[3]}; }
   __device__ __forceinline__ void renew() { asm volatile("" : "+v"(w)); }
 };
 template <>
@@ -466,23 +457,16 @@ hipError_t launch_rows_io(const RowsLaunch& l, hipStream_t stream) {
 // in binary32, the pieces in binary64. |u| is at most sqrt(h) and |u * mean|
 // at most the largest |d * u|, so apart from these sums and d itself nothing
 // leaves binary32's range before the result does. Where a sum is not well
-// inside it, the row is taken again in binary64.
-//
-// d is held times 2^64 (kGradScale, in the weight; r takes it back), which is
-// exact: then the products of an ordinary row have room on both sides, and a
-// sum of d * s that is zero means that there are no gradients (as in rows of
-// padding), or none that the result could show. Binary16 products need no room.
-// A weight of 2^60 or more leaves none: its lane keeps its weights as they are
-// and makes the sum NaN, so that every row is taken in binary64.
+// inside it, the row is taken again in binary64. (A sum of d * s of less than
+// 2^-100 may have lost products. Of exactly zero, it is that of a row without
+// gradients, as in padding, or of products below 2^-150, which cannot show where
+// r is at most 2^20.)
 //
 // Work-group b takes rows b, b + gridDim, ...; the next row's operands are
 // under way while a row is reduced and written. It keeps its columns' share of
 // grad_weight in registers and leaves one row of partial sums in the workspace,
 // and grad_weight_kernel adds those rows in order: a fixed order without
 // atomics.
-template <int IO>
-constexpr float kGradScale = IO == kOutF16 ? 1.0f : 0x1p64f;
-
 template <int IO, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLaunch a) {
   constexpr int kWaves = NT / 64;
@@ -498,25 +482,6 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     w[p].template load<false>(a.weight, (p * NT + lane) * E, a.h);
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[p][j] = 0.0f;
-  }
-  float no_sum = 0.0f;  // NaN if the lane's weights are not scaled
-  if constexpr (kGradScale<IO> != 1.0f) {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float wv[E];
-      w[p].get(wv);
-#pragma unroll
-      for (int j = 0; j < E; ++j) no_sum = __builtin_fabsf(wv[j]) < 0x1p60f ? no_sum : __builtin_nanf("");
-    }
-    const float scale = no_sum == 0.0f ? kGradScale<IO> : 1.0f;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float wv[E];
-      w[p].get(wv);
-#pragma unroll
-      for (int j = 0; j < E; ++j) wv[j] *= scale;
-      w[p].put(wv);
-    }
   }
   struct Operands {
     Raw dy[P], s[P], g[P];
@@ -576,7 +541,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     // second pass overflow (4096 x 16384 bf16 161 us, renewed 101); with fewer
     // lanes unpacking twice costs more (16384 x 8192 bf16 176 us, renewed 186).
     constexpr bool kRenew = NT == 1024;
-    double ss = 0.0, ds = no_sum;
+    double ss = 0.0, ds = 0.0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       float wv[E], dy[E], s[E];
@@ -592,11 +557,12 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
     }
     row_sums(ss, ds);
     if (kRenew) renew();
-    double r = inverse_root(ss * a.inv_h + static_cast<double>(a.eps)), mean = r * (ds * a.inv_h);
-    // The same in every lane.
-    const bool wide = !(ss > 0x1p-70 && ss < 0x1p120 && __builtin_fabs(mean) < 0x1p110 &&
-                        (ds == 0.0 || __builtin_fabs(ds) > 0x1p-100));
-    const double unscale = no_sum == 0.0f ? 1.0 / kGradScale<IO> : 1.0;
+    const double m = ss * a.inv_h + static_cast<double>(a.eps);
+    double r = inverse_root(m), mean = r * (ds * a.inv_h);
+    // The same in every lane. Squares lost below 2^-150 do not show in an m of
+    // 2^-100, so rows of zeros are ordinary ones.
+    const bool wide = !(m > 0x1p-100 && ss < 0x1p120 && __builtin_fabs(mean) < 0x1p110 &&
+                        (__builtin_fabs(ds) > 0x1p-100 || (ds == 0.0 && m > 0x1p-40)));
     if (wide) {
       turn ^= 1;
       ss = ds = 0.0;
@@ -610,7 +576,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           ss = __builtin_fma(s[j], static_cast<double>(s[j]), ss);
-          ds = __builtin_fma(wv[j] * unscale * dy[j], static_cast<double>(s[j]), ds);
+          ds = __builtin_fma(static_cast<double>(wv[j]) * dy[j], static_cast<double>(s[j]), ds);
         }
       }
       row_sums(ss, ds);
@@ -618,16 +584,15 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
       r = inverse_root(ss * a.inv_h + static_cast<double>(a.eps));
       mean = r * (ds * a.inv_h);
     }
-    const float r32 = static_cast<float>(r), mean32 = static_cast<float>(mean), back = r32 * (1.0f / kGradScale<IO>);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
+    const float r32 = static_cast<float>(r), mean32 = static_cast<float>(mean);
+    auto finish = [&](int p, bool in64) {
       const uint32_t c = (p * NT + lane) * E;
       float wv[E], dy[E], s[E], g[E];
       operands(p, wv, dy, s);
       now.g[p].get(g);
 #pragma unroll
       for (int j = 0; j < E; ++j) g[j] = keep != 0.0f ? g[j] : 0.0f;
-      if (wide) {
+      if (in64) {
         as_new(wv);
         as_new(dy);
         as_new(s);
@@ -635,17 +600,30 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(const NormBackwardLau
         for (int j = 0; j < E; ++j) {
           const double u = s[j] * r;
           dw[p][j] += static_cast<float>(dy[j] * u);
-          g[j] = static_cast<float>(g[j] + r * (wv[j] * unscale * dy[j] - u * mean));
+          g[j] = static_cast<float>(g[j] + r * (static_cast<double>(wv[j]) * dy[j] - u * mean));
         }
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           const float u = s[j] * r32;
           dw[p][j] += dy[j] * u;
-          g[j] += back * (wv[j] * dy[j] - u * mean32);
+          g[j] += r32 * (wv[j] * dy[j] - u * mean32);
         }
       }
       store_piece<IO, VEC, E>(static_cast<char*>(a.grad_x) + row * a.grad_x_stride * kSize, c, a.h, g);
+    };
+    // One loop for each kind of row lets an ordinary row's pieces overlap
+    // (1021 x 7168 bf16 16.5 us with a branch in each piece, 15.8), but at
+    // 1024 lanes it overflows the registers (4096 x 16384 bf16 101 us, 258).
+    if (kRenew) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) finish(p, wide);
+    } else if (__builtin_expect(wide, false)) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) finish(p, true);
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p) finish(p, false);
     }
   }
   float* part_row = a.workspace + static_cast<uint64_t>(blockIdx.x) * a.h;
