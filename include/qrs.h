@@ -334,13 +334,15 @@ qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scal
  *
  * s is rounded once to the activations' type and stored in sum_out; y is
  * computed from the stored s in binary32 (the sum of squares mostly in
- * binary64) to within 5 * 2^-24 of itself, also where squares leave binary32's
+ * binary64) to within 7 * 2^-24 of itself, also where squares leave binary32's
  * range, and quantized by qrs_quantize's rules for QRS_SCALE_F32_GROUP128 and
  * QRS_SCALE_E8M0_BLOCK32. With the latter, a y too close to the border between
- * two codes to tell is taken again in binary64. QRS_SCALE_F32_ROW takes the
- * whole row as one group of the same rule. A group that holds a NaN or an infinity gets a NaN or
- * infinite scale (E8M0 code 255), so that it stays visible; its codes are
- * unspecified.
+ * two codes to tell is taken again in binary64, so that its code is that of the
+ * real number. (Both but where s / sqrt(..) or y itself is below 2^-126: there
+ * a rounding of up to 2^-150, in the first case times the weight, comes on top.)
+ * QRS_SCALE_F32_ROW takes the whole row as one group of the same rule. A group
+ * that holds a NaN or an infinity gets a NaN or infinite scale (E8M0 code 255),
+ * so that it stays visible; its codes are unspecified.
  *
  *   tokens, h     rows of x; h in [1, 65536], a multiple of the layout's
  *                 group (128 or 32; any for QRS_SCALE_F32_ROW).

@@ -139,11 +139,12 @@ __device__ __forceinline__ float round_to_odd(double y) {
 
 // One lane's pieces of a row and what makes values for codes of them.
 //
-// y = s * r * weight is taken in binary32, within 1.5 * 2^-24 of the product of
-// its operands, and in binary64 where that does not do: in rows whose squares leave binary32's
-// range, and, with E8M0 scales, where y is so close to a border between two
-// codes that the error could decide which one it gets. (In binary64 always, it
-// takes the registers of a second work-group: 8192 x 5120 fp32 117 us.)
+// y = s * r * weight is taken in binary32, with three roundings (r's and those of
+// the two products: 3 * 2^-24, where neither s * r nor y is subnormal), and in
+// binary64 where that does not do: in rows whose squares leave binary32's range,
+// and, with E8M0 scales, where y is so close to a border between two codes that
+// the error could decide which one it gets. (In binary64 always, it takes the
+// registers of a second work-group: 8192 x 5120 fp32 117 us.)
 template <int IO, bool VEC, bool NORM, int P>
 struct RowValues {
   static constexpr int E = kPiece16<IO>;
@@ -269,10 +270,10 @@ __device__ __forceinline__ void quantize_row(const Values& values, const RowsLau
 // operands are under way while a row is reduced and written.
 //
 // The squares are added in binary64 where codes go by more than binary32 (E8M0
-// scales); otherwise those of a piece in binary32 (at most 7 roundings, so r is
-// within 3.5 * 2^-24; their signs differ from piece to piece, which leaves far
-// less of a row) and the pieces in binary64. If the sum is not well inside
-// binary32's range, the row is taken in binary64.
+// scales); otherwise those of a piece in binary32 and the pieces in binary64. A
+// piece of eight 16-bit values has seven roundings (the squares are exact), one
+// of four binary32 values four, so r is within 3.5 * 2^-24, and y within 6.5. If
+// the sum is not well inside binary32's range, the row is taken in binary64.
 template <int IO, int SL, int NT, int P8, bool VEC, bool NORM, bool STREAM>
 __global__ __launch_bounds__(NT) void rows_kernel(const RowsLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
