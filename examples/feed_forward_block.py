@@ -13,7 +13,8 @@ and the same columns of the down projection. Per rank:
     matmul_int8_quantize    partial sums as E4M3 codes and E8M0 scales
 
 The ranks' codes are then reduced by run_all_shares, and the next block's norm
-starts from the shares. The result is compared with the same block in float32.
+starts from the shares. The result is compared with the same block in float32,
+and so are the gradients of the norm in front of it (rms_norm_backward).
 """
 
 import argparse
@@ -65,6 +66,23 @@ class Rank:
                                  "e4m3fn", "e8m0_block32")
 
 
+def norm_gradients(total, norm_weight, products, grad_out, grad_stream):
+    """Gradients of the residual stream and of the norm's weight by
+    rms_norm_backward, and the same by torch in float32.
+
+    ``total`` is the stream that the norm read, ``products`` what follows the
+    norm, in float32 (the products have no gradient here: what reaches the
+    norm's output is torch's, with the quantization passed through), ``grad_out``
+    the gradient of their result and ``grad_stream`` the stream's own."""
+    s, w = total.float().requires_grad_(), norm_weight.float().requires_grad_()
+    y = s * torch.rsqrt(s.square().mean(1, keepdim=True) + EPS) * w
+    y.retain_grad()
+    (products(y) * grad_out).sum().backward()
+    grad_s, grad_w = torch.empty_like(total), torch.empty(total.shape[1], device=total.device)
+    qrs.rms_norm_backward(y.grad.to(total.dtype), total, norm_weight, EPS, grad_stream, grad_s, grad_w)
+    return (grad_s, grad_w), (s.grad + grad_stream.float(), w.grad)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--ranks", type=int, default=4, choices=[2, 4, 8])
@@ -84,13 +102,16 @@ def main(argv=None):
     up = [normal(2 * inner, h, scale=h ** -0.5) for _ in range(w)]
     down = [normal(h, inner, scale=(w * inner) ** -0.5) for _ in range(w)]
 
+    def products(y):
+        out = torch.zeros(t, h, device="cuda")
+        for u, d in zip(up, down):
+            gate, lift = (y @ u.t()).chunk(2, dim=1)
+            out = out + (torch.nn.functional.silu(gate) * lift) @ d.t()
+        return out
+
     # The block in float32.
     s = (x.float() + residual.float()).bfloat16().float()
-    y = s * torch.rsqrt(s.square().mean(1, keepdim=True) + EPS) * norm_weight.float()
-    want = torch.zeros(t, h, device="cuda")
-    for u, d in zip(up, down):
-        gate, lift = (y @ u.t()).chunk(2, dim=1)
-        want += (torch.nn.functional.silu(gate) * lift) @ d.t()
+    want = products(s * torch.rsqrt(s.square().mean(1, keepdim=True) + EPS) * norm_weight.float())
 
     ranks = [Rank(t, h, u, d, norm_weight) for u, d in zip(up, down)]
     streams = [residual.clone() for _ in ranks]  # in a group, each rank's own copy of the residual stream
@@ -102,6 +123,10 @@ def main(argv=None):
     got = torch.cat(shares).float()
     error = float((got - want).norm() / want.norm())
     print(f"{w} ranks, {t} tokens, hidden {h}, inner {w * inner}: relative error {error:.4f} against float32")
+
+    grads, want = norm_gradients(streams[0], norm_weight, products, normal(t, h), normal(t, h).bfloat16())
+    errors = [float((g.float() - r).norm() / r.norm()) for g, r in zip(grads, want)]
+    print(f"gradients of the stream and of the norm's weight: relative errors {errors[0]:.5f}, {errors[1]:.5f}")
     return error
 
 
