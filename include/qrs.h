@@ -320,8 +320,9 @@ qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scal
  * default stream); kernels only, so they may be captured in a HIP graph;
  * nothing is allocated (a workspace, where one is needed, is the caller's);
  * rows are given by row strides in elements, elements within a row adjacent;
- * any alignment of the element type is accepted, and rows that start on
- * 16-byte boundaries are read and written 16 bytes at a time. Sizes must be
+ * any alignment of the element type is accepted (but for the codes of
+ * qrs_matmul_int_quantize, whose rows start on 16-byte boundaries), and rows that
+ * start on such boundaries are read and written 16 bytes at a time. Sizes must be
  * positive. An output's address span must not overlap an input's or another
  * output's, except where a call allows a buffer to be updated in place
  * (then pointer and row stride are the same). Results are deterministic:

@@ -322,7 +322,7 @@ Choice general_tiles(const MatmulLaunch& l) {
 constexpr int kStep = 64;
 constexpr int kBlockK = 2 * kStep;
 constexpr int kWaveN = 128;
-constexpr int kLoadQuarters = 4;  // quarters that a block's loads are spread over
+[[maybe_unused]] constexpr int kLoadQuarters = 4;  // quarters that a block's loads are spread over
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
@@ -333,17 +333,18 @@ __device__ __forceinline__ void wait_loads_and_sync() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// acc += b a^T of one 16x16x64 product, in place. Written out because the
+// acc += b a^T of one 16x16x64 product, in place. (Used in the device pass
+// alone, like the rest of the pipeline.) Written out because the
 // compiler takes a result for a value of its own and, over several stages,
 // moves accumulators between registers inside the pipeline. It sees no
 // matrix instruction here, so the waits that such results need before other
 // instructions touch them stand in settle().
-__device__ __forceinline__ void mfma(i32x4& acc, const i32x4& b, const i32x4& a) {
+[[maybe_unused]] __device__ __forceinline__ void mfma(i32x4& acc, const i32x4& b, const i32x4& a) {
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
 // acc = b a^T.
-__device__ __forceinline__ void mfma_first(i32x4& acc, const i32x4& b, const i32x4& a) {
+[[maybe_unused]] __device__ __forceinline__ void mfma_first(i32x4& acc, const i32x4& b, const i32x4& a) {
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(acc) : "v"(b), "v"(a));
 }
 
@@ -889,10 +890,14 @@ Choice few_sized(const MatmulLaunch& l) {
 // stage's KG steps and TN / (8 / KG) rows of b.
 //
 // A stage is KG / 2 blocks of rows of 128 bytes, loaded straight into LDS, 8
-// rows a load, S - 1 stages ahead: what bounds these tiles is the 64 bytes a
-// cycle that a CU takes from L2, so whole lines are asked for and most of
-// LDS holds operands in flight. Slots as in few_tokens_kernel. Two waves a
-// SIMD hide each other's reads; one barrier a stage.
+// rows a load, S - 1 stages ahead, so that most of LDS holds operands in
+// flight, in whole lines. What bounds these tiles is how fast operands come
+// into a CU: 333 tokens by 5120, k = 7168 (f16, 240 tiles of 64 x 128) ask L2
+// for 325 MB, 82 % of it found there, at 50 GB/s a CU with weights from HBM
+// (27 us) and 65 with weights in the Infinity Cache (20 us), about 30 bytes a
+// cycle at most; the matrix units are busy for a quarter of the time. Slots as
+// in few_tokens_kernel. Two waves a SIMD hide each other's reads; one barrier a
+// stage.
 template <int TM, int TN, int KG, int S>
 struct Mid {
   static constexpr int kThreads = 512, kWavesN = 8 / KG, WTN = TN / kWavesN;
