@@ -717,6 +717,8 @@ def _workspace(workspace, nbytes, like, stream):
     import torch
 
     if workspace is not None:
+        if isinstance(workspace, int):
+            raise ValueError("workspace: a tensor expected, whose size is known")
         return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
     if stream is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
@@ -746,6 +748,8 @@ def add_rms_norm_quantize(x, residual, weight, eps, sum_out, codes, scales, x_dt
     _vector(weight, "weight", h, x.dtype)
     ld_r = ld_s = 0
     if residual is not None:
+        if sum_out is None:
+            raise ValueError("sum_out: needed with a residual")
         ld_r = _matrix(residual, "residual", x.shape, x.dtype)
         ld_s = _matrix(sum_out, "sum_out", x.shape, x.dtype)
     mode = _mode(x_dtype, scale_layout)
