@@ -894,8 +894,9 @@ Choice few_sized(const MatmulLaunch& l) {
 // flight, in whole lines. What bounds these tiles is how fast operands come
 // into a CU: 333 tokens by 5120, k = 7168 (f16, 240 tiles of 64 x 128) ask L2
 // for 325 MB, 82 % of it found there, at 50 GB/s a CU with weights from HBM
-// (27 us) and 65 with weights in the Infinity Cache (20 us), about 30 bytes a
-// cycle at most; the matrix units are busy for a quarter of the time. Slots as
+// (27 us) and 68 with weights in the Infinity Cache (20 us): 25 and 34 bytes a
+// cycle of the 64 that a CU can take, the matrix units busy for a quarter of
+// the time. More in flight is what is missing, and LDS is full. Slots as
 // in few_tokens_kernel. Two waves a SIMD hide each other's reads; one barrier a
 // stage.
 template <int TM, int TN, int KG, int S>
