@@ -316,12 +316,24 @@ qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scal
  *   qrs_matmul_int_quantize    the same product, written as the codes and
  *                              scales that qrs_run reads
  *
+ * or, with 8-bit floating-point weights and a scale for each block of 128:
+ *
+ *   qrs_add_layer_norm_quantize  residual sum, layer norm, codes and scales
+ *   qrs_layer_norm_backward    its gradients
+ *   qrs_quantize_blocks        codes with one scale for each 128 x 128 block,
+ *                              also transposed
+ *   qrs_quantize_transposed    the transpose's codes, a scale for each 128 of
+ *                              its columns, and the rows' beside them
+ *   qrs_matmul_float             the product of such codes, also gated
+ *   qrs_matmul_float_quantize    the same, written as codes and scales
+ *
  * Common to all of them: asynchronous on `stream` (a hipStream_t, NULL = the
  * default stream); kernels only, so they may be captured in a HIP graph;
  * nothing is allocated (a workspace, where one is needed, is the caller's);
  * rows are given by row strides in elements, elements within a row adjacent;
  * any alignment of the element type is accepted (but for the codes of
- * qrs_matmul_int_quantize, whose rows start on 16-byte boundaries), and rows that
+ * qrs_matmul_int_quantize and qrs_matmul_float_quantize, whose rows start on 16-byte
+ * boundaries), and rows that
  * start on such boundaries are read and written 16 bytes at a time. Sizes must be
  * positive. An output's address span must not overlap an input's or another
  * output's, except where a call allows a buffer to be updated in place
@@ -452,6 +464,149 @@ typedef struct qrs_matmul_info {
 
 qrs_status qrs_matmul_launch_info(int64_t m, int64_t n, int64_t k, int gated, int quantize,
                                   qrs_scale_layout scale_layout, qrs_matmul_info* info_out);
+
+/*
+ * s = x + residual, y = (s - mean) / sqrt(var + eps) * weight + bias along each
+ * row, with mean and var (the mean of (s - mean)^2) of the row's s, and y as
+ * codes and scales.
+ *
+ * s is rounded once to the activations' type and stored in sum_out. Mean and
+ * variance are those of the stored s to within 2^-33 of themselves (of the
+ * largest |s - mean| for the mean), however large the mean is; y is computed in
+ * binary32 to within 2^-24 * (4.1 |y - bias| + |y|), and in binary64 for rows
+ * whose variance or mean is beyond 2^100 or var + eps below 2^-100; and it is
+ * quantized in binary32 by qrs_quantize's rules, or with the whole row as one
+ * group for QRS_SCALE_F32_ROW. A row that holds a NaN or an infinity, and one of
+ * equal values with eps = 0, has NaN in y: its scales are NaN (E8M0 code 255), and
+ * its codes are unspecified.
+ *
+ * Parameters as for qrs_add_rms_norm_quantize;
+ *
+ *   bias          [h], of io_dtype; may be NULL: zero.
+ */
+qrs_status qrs_add_layer_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype io_dtype, qrs_x_dtype x_dtype,
+                                       qrs_scale_layout scale_layout, float eps, const void* x, int64_t x_row_stride,
+                                       const void* residual, int64_t residual_row_stride, const void* weight,
+                                       const void* bias, void* sum_out, int64_t sum_row_stride, void* codes,
+                                       int64_t codes_row_stride, void* scales, void* stream);
+
+/*
+ * Gradients of y = u * weight + bias, u = (s - mean) * r, r = 1 / sqrt(var + eps),
+ * with the quantization passed through. With d = weight * grad_y:
+ *
+ *   grad_x      = grad_sum + r * (d - mean(d) - u * mean(d * u))
+ *   grad_weight = sum over tokens of grad_y * u
+ *   grad_bias   = sum over tokens of grad_y
+ *
+ * The sums along a row are binary64, of products d rounded to binary32; the rest
+ * is binary32, and binary64 for rows as above and those whose mean(d) or
+ * mean(d * u) is beyond 2^100; grad_x is rounded once to io_dtype. grad_weight
+ * and grad_bias are added in binary32.
+ *
+ *   grad_x      may be grad_y or grad_sum themselves (same pointer and
+ *               stride).
+ *   grad_bias   float32 [h]; may be NULL: not wanted.
+ *   workspace   DEVICE memory of at least qrs_layer_norm_backward_workspace
+ *               bytes, 16-byte aligned, for this call alone until it ends.
+ */
+qrs_status qrs_layer_norm_backward_workspace(int64_t tokens, int64_t h, size_t* bytes_out);
+qrs_status qrs_layer_norm_backward(int64_t tokens, int64_t h, qrs_out_dtype io_dtype, float eps, const void* grad_y,
+                                   int64_t grad_y_row_stride, const void* sum, int64_t sum_row_stride,
+                                   const void* weight, const void* grad_sum, int64_t grad_sum_row_stride, void* grad_x,
+                                   int64_t grad_x_row_stride, float* grad_weight, float* grad_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * A matrix as 8-bit floating-point codes with one binary32 scale for each block
+ * of 128 rows and 128 columns (the last ones of a row or column of blocks may be
+ * smaller), by qrs_quantize's per-group rule with the block as the group: the
+ * weights of qrs_matmul_float. The same codes transposed are the weights of the
+ * product that takes the gradient of its output back to its input.
+ *
+ *   rows, cols  x is [rows, cols]; both below 2^31, and ceil(rows / 128) *
+ *               ceil(cols / 128) below 2^24.
+ *   in_dtype    type of x. x_dtype: QRS_X_FP8_E4M3FN or QRS_X_FP8_E5M2.
+ *   codes, scales       [rows, cols], and contiguous [ceil(rows / 128),
+ *               ceil(cols / 128)]; codes may be NULL: neither is written.
+ *   codes_t, scales_t   [cols, rows_t], and contiguous [ceil(cols / 128),
+ *               ceil(rows / 128)]; codes_t may be NULL (not both): neither is
+ *               written. Columns from `rows` up to rows_t receive zeros: a
+ *               product reads rows of a multiple of 16 codes faster.
+ *   rows_t      in [rows, ceil(rows / 128) * 128].
+ *
+ * A block that holds a NaN or an infinity gets a NaN or infinite scale; its codes
+ * are unspecified.
+ */
+qrs_status qrs_quantize_blocks(int64_t rows, int64_t cols, qrs_out_dtype in_dtype, qrs_x_dtype x_dtype, const void* x,
+                               int64_t x_row_stride, void* codes, int64_t codes_row_stride, float* scales,
+                               void* codes_t, int64_t rows_t, int64_t codes_t_row_stride, float* scales_t,
+                               void* stream);
+
+/*
+ * The transpose of activations or of gradients as codes, with one scale for each
+ * 128 rows of a column of x (the last ones may be fewer): what a weight's
+ * gradient multiplies along the tokens. In the same pass, where codes is not NULL,
+ * the rows themselves, with one scale for each row and 128 columns.
+ *
+ *   codes_t, scales_t   [cols, rows_t], and contiguous [cols, ceil(rows / 128)].
+ *   codes, scales       [rows, cols], and contiguous [rows, ceil(cols / 128)];
+ *               codes may be NULL: neither is written.
+ *
+ * Otherwise as qrs_quantize_blocks.
+ */
+qrs_status qrs_quantize_transposed(int64_t rows, int64_t cols, qrs_out_dtype in_dtype, qrs_x_dtype x_dtype,
+                                   const void* x, int64_t x_row_stride, void* codes_t, int64_t rows_t,
+                                   int64_t codes_t_row_stride, float* scales_t, void* codes, int64_t codes_row_stride,
+                                   float* scales, void* stream);
+
+/*
+ * out[i][j] = sum over groups g of 128 of k of
+ *             P[i][j][g] * fp32(a_scales[i][g] * b_scales[j / R][g]),
+ * with P[i][j][g] the sum over k in g of a[i][k] * b[j][k]: a is [m, k] codes
+ * (tokens), b is [n, k] codes (output channels), each E4M3FN or E5M2. P is a matrix
+ * instruction's sum in binary32, its product with the scales is added by a fused
+ * operation, and groups are added in a fixed order for a given shape; the result is
+ * rounded once to out_dtype. NaN and infinite codes go through as in the formula.
+ *
+ * The gradients of the dequantized operands are such products themselves: of
+ * grad_out's rows with b transposed (qrs_quantize_blocks), and of the transposes of
+ * grad_out and a (qrs_quantize_transposed).
+ *
+ *   gated      1: b is [2n, k], n gate channels and then n up channels, and
+ *              out = silu(g) * u of the two binary32 products; silu as in
+ *              qrs_matmul_int.
+ *   k          in [1, 2^24]; the last group may be smaller than 128.
+ *   m, n       as for qrs_matmul_int.
+ *   a_dtype, b_dtype  QRS_X_FP8_E4M3FN or QRS_X_FP8_E5M2.
+ *   a_scales   float32, contiguous [m, ceil(k / 128)]: the scales of
+ *              QRS_SCALE_F32_GROUP128.
+ *   b_scale_rows      R, rows of b that share their scales: 128 or 1 (not
+ *              gated).
+ *   b_scales   float32, contiguous [ceil(n / R), ceil(k / 128)]; gated: the
+ *              ceil(n / 128) rows of the gates, then those of the ups.
+ */
+qrs_status qrs_matmul_float(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype, qrs_x_dtype a_dtype,
+                          const void* a, int64_t a_row_stride, const float* a_scales, qrs_x_dtype b_dtype,
+                          int b_scale_rows, const void* b, int64_t b_row_stride, const float* b_scales, void* out,
+                          int64_t out_row_stride, void* stream);
+
+/*
+ * The same product, gated or not, with scales of 128 rows of b, quantized in binary32 by
+ * qrs_quantize's rules: one rank's partial sums as qrs_run reads them, or (gated, with
+ * QRS_SCALE_F32_GROUP128) the next product's a. n is a multiple of 128 here;
+ * codes 16-byte aligned, its row stride a multiple of 16; scales contiguous
+ * [m, n / G]. A group that holds a NaN or an infinity gets a NaN or infinite
+ * scale (E8M0 code 255); its codes are unspecified.
+ */
+qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated, qrs_x_dtype x_dtype,
+                                   qrs_scale_layout scale_layout, qrs_x_dtype a_dtype, const void* a,
+                                   int64_t a_row_stride, const float* a_scales, qrs_x_dtype b_dtype, const void* b,
+                                   int64_t b_row_stride, const float* b_scales, void* codes, int64_t codes_row_stride,
+                                   void* scales, void* stream);
+
+/* qrs_matmul_launch_info of these two products. */
+qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gated, int b_scale_rows, int quantize,
+                                      qrs_scale_layout scale_layout, qrs_matmul_info* info_out);
 
 /* Free a plan. NULL is accepted. Plans in use by queued runs may be freed:
  * qrs_run copies what the kernel needs into its launch arguments. */

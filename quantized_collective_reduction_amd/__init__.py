@@ -19,6 +19,13 @@ What a layer computes between one share and the next, with 8-bit weights:
     matmul_int8(codes, scales, w, w_scales, out)               # gated=True: silu(gate) * up
     quantize_rows(out, codes2, scales2, "int8")
     matmul_int8_quantize(codes2, scales2, w2, w2_scales, x_codes, x_scales, "e4m3fn", "e8m0_block32")
+
+and with 8-bit floating-point weights, a scale for each 128 x 128 block of them:
+
+    quantize_blocks(w, w8, w8_scales, "e4m3fn")
+    add_layer_norm_quantize(x, residual, weight, bias, eps, total, codes, scales, "e4m3fn", "f32_group128")
+    matmul_fp8_quantize(codes, scales, w8, w8_scales, codes2, scales2, "e4m3fn", "f32_group128", gated=True)
+    matmul_fp8(codes2, scales2, v8, v8_scales, out)
 """
 
 import ctypes
@@ -52,10 +59,17 @@ __all__ = [
     "quantize_rows",
     "matmul_int8",
     "matmul_int8_quantize",
+    "add_layer_norm_quantize",
+    "layer_norm_backward",
+    "quantize_blocks",
+    "quantize_transposed",
+    "matmul_fp8",
+    "matmul_fp8_quantize",
     "stream_copy",
     "run_launch_info",
     "LaunchInfo",
     "matmul_launch_info",
+    "matmul_fp8_launch_info",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -78,7 +92,7 @@ class XDtype(IntEnum):
 class ScaleLayout(IntEnum):
     F32_GROUP128 = 0
     E8M0_BLOCK32 = 1
-    F32_ROW = 2  # add_rms_norm_quantize only
+    F32_ROW = 2  # add_rms_norm_quantize and add_layer_norm_quantize only
 
 
 class OutDtype(IntEnum):
@@ -116,6 +130,14 @@ EXPORTED_SYMBOLS = (
     "qrs_matmul_int",
     "qrs_matmul_int_quantize",
     "qrs_matmul_launch_info",
+    "qrs_add_layer_norm_quantize",
+    "qrs_layer_norm_backward",
+    "qrs_layer_norm_backward_workspace",
+    "qrs_quantize_blocks",
+    "qrs_quantize_transposed",
+    "qrs_matmul_float",
+    "qrs_matmul_float_quantize",
+    "qrs_matmul_float_launch_info",
 )
 
 
@@ -218,6 +240,28 @@ def load_library(path: str = LIB_PATH):
     lib.qrs_matmul_int_quantize.restype = c_int
     lib.qrs_matmul_launch_info.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, ctypes.POINTER(MatmulInfo)]
     lib.qrs_matmul_launch_info.restype = c_int
+    lib.qrs_add_layer_norm_quantize.argtypes = [c_i64, c_i64, c_int, c_int, c_int, c_f, vp, c_i64, vp, c_i64, vp, vp,
+                                                vp, c_i64, vp, c_i64, vp, vp]
+    lib.qrs_add_layer_norm_quantize.restype = c_int
+    lib.qrs_layer_norm_backward_workspace.argtypes = [c_i64, c_i64, ctypes.POINTER(c_sz)]
+    lib.qrs_layer_norm_backward_workspace.restype = c_int
+    lib.qrs_layer_norm_backward.argtypes = [c_i64, c_i64, c_int, c_f, vp, c_i64, vp, c_i64, vp, vp, c_i64, vp, c_i64,
+                                            vp, vp, vp, c_sz, vp]
+    lib.qrs_layer_norm_backward.restype = c_int
+    lib.qrs_quantize_blocks.argtypes = [c_i64, c_i64, c_int, c_int, vp, c_i64, vp, c_i64, vp, vp, c_i64, c_i64, vp, vp]
+    lib.qrs_quantize_blocks.restype = c_int
+    lib.qrs_quantize_transposed.argtypes = [c_i64, c_i64, c_int, c_int, vp, c_i64, vp, c_i64, c_i64, vp, vp, c_i64, vp,
+                                            vp]
+    lib.qrs_quantize_transposed.restype = c_int
+    lib.qrs_matmul_float.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, vp, c_i64, vp, c_int, c_int, vp, c_i64,
+                                   vp, vp, c_i64, vp]
+    lib.qrs_matmul_float.restype = c_int
+    lib.qrs_matmul_float_quantize.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int, vp, c_i64, vp, c_int, vp,
+                                            c_i64, vp, vp, c_i64, vp, vp]
+    lib.qrs_matmul_float_quantize.restype = c_int
+    lib.qrs_matmul_float_launch_info.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
+                                               ctypes.POINTER(MatmulInfo)]
+    lib.qrs_matmul_float_launch_info.restype = c_int
     _lib = lib
     return lib
 
@@ -850,6 +894,226 @@ def matmul_int8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale
                                        scales.data_ptr(), _stream_handle(stream)))
 
 
+def add_layer_norm_quantize(x, residual, weight, bias, eps, sum_out, codes, scales, x_dtype, scale_layout,
+                            stream=None):
+    """s = x + residual, y = (s - mean) / sqrt(var + eps) * weight + bias along
+    each row, and y as codes and scales (qrs_add_layer_norm_quantize). ``bias``:
+    ``[h]`` of the activations' type, or None = zero; otherwise as
+    ``add_rms_norm_quantize``."""
+    lib = load_library()
+    io = _act_dtype(x, "x")
+    ld_x = _matrix(x, "x")
+    tokens, h = x.shape
+    _vector(weight, "weight", h, x.dtype)
+    if bias is not None:
+        _vector(bias, "bias", h, x.dtype)
+    ld_r = ld_s = 0
+    if residual is not None:
+        if sum_out is None:
+            raise ValueError("sum_out: needed with a residual")
+        ld_r = _matrix(residual, "residual", x.shape, x.dtype)
+        ld_s = _matrix(sum_out, "sum_out", x.shape, x.dtype)
+    mode = _mode(x_dtype, scale_layout)
+    ld_c = _codes_and_scales(codes, scales, x.shape, mode)
+    _check(lib.qrs_add_layer_norm_quantize(
+        tokens, h, io, mode[0], mode[1], eps, x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(),
+        ld_r, weight.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else sum_out.data_ptr(), ld_s, codes.data_ptr(), ld_c, scales.data_ptr(),
+        _stream_handle(stream)))
+
+
+def layer_norm_backward(grad_y, sum, weight, eps, grad_sum, grad_x, grad_weight, grad_bias=None, workspace=None,
+                        stream=None):
+    """Gradients of ``add_layer_norm_quantize``'s y, with the quantization
+    passed through (qrs_layer_norm_backward): ``grad_x`` of s (so of x and of
+    residual alike), ``grad_weight`` and ``grad_bias`` (float32 ``[h]``; None =
+    not wanted).
+
+    ``sum`` is s; ``grad_sum`` the gradient that reaches s by the residual
+    stream (None = zero). ``grad_x`` may be ``grad_y`` or ``grad_sum`` itself.
+    ``workspace``: device memory of qrs_layer_norm_backward_workspace's bytes, by
+    default taken from torch's allocator."""
+    import torch
+
+    lib = load_library()
+    io = _act_dtype(sum, "sum")
+    ld_s = _matrix(sum, "sum")
+    tokens, h = sum.shape
+    ld_y = _matrix(grad_y, "grad_y", sum.shape, sum.dtype)
+    ld_g = 0 if grad_sum is None else _matrix(grad_sum, "grad_sum", sum.shape, sum.dtype)
+    ld_x = _matrix(grad_x, "grad_x", sum.shape, sum.dtype)
+    _vector(weight, "weight", h, sum.dtype)
+    _vector(grad_weight, "grad_weight", h, torch.float32)
+    if grad_bias is not None:
+        _vector(grad_bias, "grad_bias", h, torch.float32)
+    need = ctypes.c_size_t()
+    _check(lib.qrs_layer_norm_backward_workspace(tokens, h, ctypes.byref(need)))
+    ws, nbytes, _keep = _workspace(workspace, need.value, sum, stream)  # _keep: until it is enqueued
+    _check(lib.qrs_layer_norm_backward(
+        tokens, h, io, eps, grad_y.data_ptr(), ld_y, sum.data_ptr(), ld_s, weight.data_ptr(),
+        None if grad_sum is None else grad_sum.data_ptr(), ld_g, grad_x.data_ptr(), ld_x, grad_weight.data_ptr(),
+        None if grad_bias is None else grad_bias.data_ptr(), ws, nbytes, _stream_handle(stream)))
+
+
+_BLOCK = 128  # rows and columns that share a scale
+
+
+def _blocks(n):
+    return -(-n // _BLOCK)
+
+
+@functools.lru_cache(maxsize=None)
+def _fp8_types():
+    import torch
+
+    return ({torch.float8_e4m3fn: int(XDtype.FP8_E4M3FN), torch.float8_e5m2: int(XDtype.FP8_E5M2)}, torch.uint8,
+            torch.float32)
+
+
+def _fp8_kind(t, what, given=None):
+    """The format of 8-bit floating-point codes: the tensor's, or of uint8 the
+    one that is given."""
+    types, raw, _ = _fp8_types()
+    kind = types.get(t.dtype)
+    if given is not None:
+        want = int(_enum(given, _X_NAMES, XDtype))
+        if t.dtype == raw:
+            return want
+        if kind != want:
+            raise ValueError(f"{what}: {t.dtype} codes, {given} given")
+    if kind is None:
+        raise ValueError(f"{what}: float8_e4m3fn, float8_e5m2, or uint8 with its format named, expected, got {t.dtype}")
+    return kind
+
+
+def _scale_matrix(t, what, shape):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: device tensors only (there is no CPU path)")
+    if t.shape != shape or t.dtype != _fp8_types()[2] or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous float32 {list(shape)} expected, got {list(t.shape)} {t.dtype}")
+
+
+def _fp8_codes(t, scales, what, shape, scale_shape, kind):
+    """Checks written codes and their scales; the codes' row stride."""
+    ld = _matrix(t, what, shape)
+    if _fp8_kind(t, what, kind) != kind:
+        raise ValueError(f"{what}: codes of {kind.name} expected, got {t.dtype}")
+    if scales is None:
+        raise ValueError(f"{what}: needs its scales")
+    _scale_matrix(scales, f"scales of {what}", scale_shape)
+    return ld
+
+
+def _quantize_blocks(by_block, x, codes, scales, codes_t, scales_t, x_dtype, stream):
+    lib = load_library()
+    kind = _act_dtype(x, "x")
+    ld_x = _matrix(x, "x")
+    rows, cols = x.shape
+    xd = _enum(x_dtype, _X_NAMES, XDtype)
+    if xd not in (XDtype.FP8_E4M3FN, XDtype.FP8_E5M2):
+        raise ValueError(f"x_dtype: e4m3fn or e5m2 expected, got {x_dtype}")
+    br, bc = (_blocks(rows), _blocks(cols)) if by_block else (rows, cols)
+    ld_c = ld_t = rows_t = 0
+    if codes is not None:
+        ld_c = _fp8_codes(codes, scales, "codes", (rows, cols), (br, _blocks(cols)), xd)
+    if codes_t is not None:
+        if codes_t.dim() != 2 or not rows <= codes_t.shape[1] <= _blocks(rows) * _BLOCK:
+            raise ValueError(f"codes_t: [{cols}, {rows} to {_blocks(rows) * _BLOCK}] expected, got {list(codes_t.shape)}")
+        rows_t = codes_t.shape[1]
+        ld_t = _fp8_codes(codes_t, scales_t, "codes_t", (cols, rows_t), (bc, _blocks(rows)), xd)
+    ptr = [None if t is None else t.data_ptr() for t in (codes, scales, codes_t, scales_t)]
+    if by_block:
+        _check(lib.qrs_quantize_blocks(rows, cols, kind, xd, x.data_ptr(), ld_x, ptr[0], ld_c, ptr[1], ptr[2], rows_t,
+                                       ld_t, ptr[3], _stream_handle(stream)))
+    else:
+        _check(lib.qrs_quantize_transposed(rows, cols, kind, xd, x.data_ptr(), ld_x, ptr[2], rows_t, ld_t, ptr[3],
+                                           ptr[0], ld_c, ptr[1], _stream_handle(stream)))
+
+
+def quantize_blocks(x, codes, scales, x_dtype, codes_t=None, scales_t=None, stream=None):
+    """``x [rows, cols]`` (float32, bfloat16 or float16) as 8-bit floating-point
+    ``codes`` with a float32 scale for each 128 x 128 block, ``scales
+    [ceil(rows / 128), ceil(cols / 128)]``: the weights of ``matmul_fp8``
+    (qrs_quantize_blocks).
+
+    ``codes_t [cols, rows_t]``, ``scales_t``: the transpose of both, in the same
+    pass; rows_t is rows, or more up to the next multiple of 128, with zeros in
+    the columns that come on top. ``codes`` and ``scales`` may be None then."""
+    _quantize_blocks(True, x, codes, scales, codes_t, scales_t, x_dtype, stream)
+
+
+def quantize_transposed(x, codes_t, scales_t, x_dtype, codes=None, scales=None, stream=None):
+    """The transpose of ``x [rows, cols]`` as 8-bit floating-point ``codes_t
+    [cols, rows_t]`` with a float32 scale for each 128 rows of a column of x,
+    ``scales_t [cols, ceil(rows / 128)]``: what a weight's gradient multiplies
+    along the tokens (qrs_quantize_transposed). rows_t as for
+    ``quantize_blocks``.
+
+    ``codes [rows, cols]``, ``scales [rows, ceil(cols / 128)]``: the rows
+    themselves, a scale for each 128 columns, in the same pass."""
+    if codes_t is None:
+        raise ValueError("codes_t: a tensor expected")
+    _quantize_blocks(False, x, codes, scales, codes_t, scales_t, x_dtype, stream)
+
+
+def _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype):
+    """The arguments of both products up to the output."""
+    ld_a = _matrix(a, "a")
+    ld_b = _matrix(b, "b")
+    ka, kb = _fp8_kind(a, "a", a_dtype), _fp8_kind(b, "b", b_dtype)
+    m, k = a.shape
+    wide, k_b = b.shape
+    if k_b != k or (gated and wide % 2):
+        raise ValueError(f"b: expected [{'2 n' if gated else 'n'}, {k}], got {list(b.shape)}")
+    n, groups = wide // 2 if gated else wide, _blocks(k)
+    _scale_matrix(a_scales, "a_scales", (m, groups))
+    blocks = _blocks(n)
+    grouped = not gated and n != blocks and b_scales.dim() == 2 and b_scales.shape[0] == n
+    _scale_matrix(b_scales, "b_scales", (n if grouped else 2 * blocks if gated else blocks, groups))
+    return m, n, k, ka, ld_a, kb, 1 if grouped else _BLOCK, ld_b
+
+
+def matmul_fp8(a, a_scales, b, b_scales, out, gated=False, a_dtype=None, b_dtype=None, stream=None):
+    """The product ``a @ b.T`` of 8-bit floating-point codes ``a [m, k]``
+    (tokens) and ``b [n, k]`` (channels) with float32 scales for each 128 of k
+    (qrs_matmul_float): ``a_scales [m, ceil(k / 128)]``, as "f32_group128" codes
+    have them, and ``b_scales [ceil(n / 128), ceil(k / 128)]``, as
+    ``quantize_blocks`` gives them, or ``[n, ceil(k / 128)]``, a row of scales for
+    each row of b. ``out [m, n]``: float32, bfloat16 or float16.
+
+    ``a_dtype``, ``b_dtype``: "e4m3fn" or "e5m2", for codes that are held as
+    uint8.
+
+    ``gated``: ``b`` is ``[2 n, k]``, n gate and then n up channels, ``b_scales``
+    the gates' ceil(n / 128) rows and then the ups', and
+    ``out = silu(gate product) * up product``."""
+    lib = load_library()
+    m, n, k, ka, ld_a, kb, scale_rows, ld_b = _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype)
+    kind = _act_dtype(out, "out")
+    ld_o = _matrix(out, "out", (m, n))
+    _check(lib.qrs_matmul_float(m, n, k, 1 if gated else 0, kind, ka, a.data_ptr(), ld_a, a_scales.data_ptr(), kb,
+                              scale_rows, b.data_ptr(), ld_b, b_scales.data_ptr(), out.data_ptr(), ld_o,
+                              _stream_handle(stream)))
+
+
+def matmul_fp8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_layout, gated=False, a_dtype=None,
+                        b_dtype=None, stream=None):
+    """``matmul_fp8``'s product (b's scales those of 128 x 128 blocks),
+    quantized in float32 into ``codes [m, n]`` and scales
+    (qrs_matmul_float_quantize): one rank's partial sums, as ``run`` and
+    ``run_all_shares`` read them, or with "f32_group128" the next product's a.
+    n is a multiple of 128."""
+    lib = load_library()
+    m, n, k, ka, ld_a, kb, scale_rows, ld_b = _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype)
+    if scale_rows != _BLOCK:
+        raise ValueError(f"b_scales: [{_blocks(n)}, {_blocks(k)}] expected, got {list(b_scales.shape)}")
+    mode = _mode(x_dtype, scale_layout)
+    ld_c = _codes_and_scales(codes, scales, (m, n), mode)
+    _check(lib.qrs_matmul_float_quantize(m, n, k, 1 if gated else 0, mode[0], mode[1], ka, a.data_ptr(), ld_a,
+                                       a_scales.data_ptr(), kb, b.data_ptr(), ld_b, b_scales.data_ptr(),
+                                       codes.data_ptr(), ld_c, scales.data_ptr(), _stream_handle(stream)))
+
+
 def run_launch_info(p: Plan, stream=None) -> dict:
     """The grid, residency cap and device sizes of the launch ``run`` makes
     for ``p`` on ``stream``'s device (qrs_run_launch_info); launches nothing."""
@@ -869,6 +1133,19 @@ def matmul_launch_info(m, n, k, gated=False, scale_layout=None) -> dict:
     layout = ScaleLayout.F32_GROUP128 if scale_layout is None else _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
     _check(lib.qrs_matmul_launch_info(m, n, k, 1 if gated else 0, 0 if scale_layout is None else 1, layout,
                                       ctypes.byref(info)))
+    return {"kernel": ("tiles", "few_tokens", "mid", "pipe")[info.kernel], "tile": (info.tile_m, info.tile_n),
+            "blocks": info.blocks, "threads_per_block": info.threads_per_block}
+
+
+def matmul_fp8_launch_info(m, n, k, gated=False, scale_layout=None, b_scale_rows=128) -> dict:
+    """``matmul_launch_info`` of ``matmul_fp8`` and, with a ``scale_layout``,
+    ``matmul_fp8_quantize``; ``b_scale_rows``: 128, or 1 for a row of scales for
+    each row of b (qrs_matmul_float_launch_info)."""
+    lib = load_library()
+    info = MatmulInfo()
+    layout = ScaleLayout.F32_GROUP128 if scale_layout is None else _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
+    _check(lib.qrs_matmul_float_launch_info(m, n, k, 1 if gated else 0, b_scale_rows, 0 if scale_layout is None else 1,
+                                          layout, ctypes.byref(info)))
     return {"kernel": ("tiles", "few_tokens", "mid", "pipe")[info.kernel], "tile": (info.tile_m, info.tile_n),
             "blocks": info.blocks, "threads_per_block": info.threads_per_block}
 

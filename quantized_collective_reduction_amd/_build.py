@@ -27,6 +27,12 @@ SOURCES = [
     os.path.join(CSRC, "qrs_layer.cpp"),
     os.path.join(CSRC, "qrs_rows.hip"),
     os.path.join(CSRC, "qrs_matmul.hip"),
+    os.path.join(CSRC, "qrs_layer_norm.hip"),
+    os.path.join(CSRC, "qrs_blocks.hip"),
+    os.path.join(CSRC, "qrs_matmul_fp8_e4m3_e4m3.hip"),
+    os.path.join(CSRC, "qrs_matmul_fp8_e4m3_e5m2.hip"),
+    os.path.join(CSRC, "qrs_matmul_fp8_e5m2_e4m3.hip"),
+    os.path.join(CSRC, "qrs_matmul_fp8_e5m2_e5m2.hip"),
 ]
 
 BASE_FLAGS = [
@@ -44,6 +50,14 @@ BASE_FLAGS = [
     "-Xarch_device", "-mllvm=-amdgpu-kernarg-preload-count=14",
     "-Wall",
 ]
+
+# Sums of a matrix instruction in the registers that vector instructions read:
+# every one of them is multiplied by its scales at once.
+FP8_FLAGS = ["-Xarch_device", "-mllvm=-amdgpu-mfma-vgpr-form=1"]
+
+
+def source_flags(src: str) -> list:
+    return FP8_FLAGS if os.path.basename(src).startswith("qrs_matmul_fp8") else []
 
 
 def hipcc() -> str:
@@ -71,7 +85,7 @@ def build(out_path: str = LIB_PATH, defines=(), verbose: bool = False) -> str:
             jobs = []
             for src in SOURCES:
                 obj = os.path.join(objs, os.path.basename(src) + ".o")
-                jobs.append((obj, pool.submit(run, [hipcc(), *flags, "-I", INCLUDE, "-I", CSRC,
+                jobs.append((obj, pool.submit(run, [hipcc(), *flags, *source_flags(src), "-I", INCLUDE, "-I", CSRC,
                                                     *[f"-D{d}" for d in defines], "-c", src, "-o", obj])))
             for _, job in jobs:
                 job.result()

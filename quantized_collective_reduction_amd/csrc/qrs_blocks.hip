@@ -1,0 +1,179 @@
+// gfx950 kernel that quantizes 128 x 128 blocks of a matrix to 8-bit
+// floating-point codes, and writes them as they lie, transposed, or both: the
+// operands of the product in qrs_matmul_fp8.h and of its gradients.
+//
+//   scale = amax / qmax, codes = RNE(clamp(v * (qmax / amax), +-qmax))
+//
+// with amax over the block (weights), or over 128 columns of a row for the
+// codes and 128 rows of a column for the transposed ones (activations and
+// gradients, whose transposes are multiplied along the tokens).
+//
+// A work-group of 256 lanes holds a block in registers, 8 x 8 values a lane, so
+// one read of the matrix serves both outputs. A lane's eight rows of a column are
+// the eight bytes of a piece of the transpose, which goes through LDS and leaves in whole
+// lines. The kernel is a stream, bound by HBM.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qrs_device.h"
+#include "qrs_layer.h"
+
+// One rounding per operation: never fuse.
+#pragma clang fp contract(off)
+
+namespace qrs {
+namespace {
+
+using namespace dev;
+
+constexpr int kSide = 128;
+
+// v: a piece's values -> their largest magnitude as bits (NaN above infinity).
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[kPiece]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) m = max(m, abs_bits(v[j]));
+  return m;
+}
+
+template <int IO, int XF, bool BY_BLOCK, bool VEC>
+__global__ __launch_bounds__(256) void blocks_kernel(const BlocksLaunch a) {
+  // The transposed codes: piece b (8 rows) of column c in slot b ^ (c / 8) of the
+  // column's 128 bytes, which spreads the columns of a write over the banks.
+  __shared__ __attribute__((aligned(16))) uint8_t turned[kSide * kSide];
+  __shared__ uint32_t maxima[4][kSide];
+  const uint32_t tiles_c = static_cast<uint32_t>((a.cols + kSide - 1) / kSide);
+  const uint32_t tr = blockIdx.x / tiles_c, tc = blockIdx.x % tiles_c;
+  const uint64_t r0 = static_cast<uint64_t>(tr) * kSide, c0 = static_cast<uint64_t>(tc) * kSide;
+  const uint32_t rows = static_cast<uint32_t>(min<uint64_t>(kSide, a.rows - r0));
+  const uint32_t cols = static_cast<uint32_t>(min<uint64_t>(kSide, a.cols - c0));
+  const uint32_t wave = threadIdx.x / 64, pc = threadIdx.x % 16, pr = threadIdx.x / 16;
+
+  // Rows 8 pr .. + 7, columns 8 pc .. + 7; zeros outside.
+  float v[kPiece][kPiece];
+  const char* x = static_cast<const char*>(a.x) + (r0 * a.x_stride + c0) * kOutSize<IO>;
+#pragma unroll
+  for (int i = 0; i < kPiece; ++i) {
+    const uint32_t r = pr * kPiece + i;
+    load_piece<IO, VEC, kPiece>(x + static_cast<uint64_t>(min(r, rows - 1)) * a.x_stride * kOutSize<IO>, pc * kPiece,
+                                r < rows ? cols : 0, v[i]);
+  }
+
+  constexpr float kMax = CodeFormat<XF>::kMax;
+  float block_mul = 0.0f, block_scale = 0.0f;
+  if constexpr (BY_BLOCK) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) amax = max(amax, max_bits(v[i]));
+    amax = wave_max(amax);
+    if (threadIdx.x % 64 == 0) maxima[wave][0] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = max(amax, maxima[i][0]);
+    block_mul = f32_multiplier(amax, kMax, &block_scale);
+    if (threadIdx.x == 0) {
+      const uint32_t tiles_r = static_cast<uint32_t>((a.rows + kSide - 1) / kSide);
+      if (a.codes) a.scales[static_cast<uint64_t>(tr) * tiles_c + tc] = block_scale;
+      if (a.codes_t) a.scales_t[static_cast<uint64_t>(tc) * tiles_r + tr] = block_scale;
+    }
+  }
+  if (a.codes) {
+    uint8_t* out = static_cast<uint8_t*>(a.codes) + r0 * a.codes_stride + c0;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const uint32_t r = pr * kPiece + i;
+      float mul = block_mul, scale;
+      if constexpr (!BY_BLOCK) mul = f32_multiplier(group_max<16>(max_bits(v[i])), kMax, &scale);
+      if (r < rows) {
+        store_codes<VEC, kPiece>(out + r * a.codes_stride, pc * kPiece, cols, encode_piece<XF>(v[i], mul));
+        if (!BY_BLOCK && pc == 0) a.scales[(r0 + r) * tiles_c + tc] = scale;
+      }
+    }
+  }
+  if (!a.codes_t) return;
+
+  float mul[kPiece];
+  if constexpr (BY_BLOCK) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) mul[j] = block_mul;
+  } else {
+    // Lanes 16 apart hold the same columns.
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kPiece; ++i) m = max(m, abs_bits(v[i][j]));
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+      if (threadIdx.x % 64 < 16) maxima[wave][pc * kPiece + j] = m;
+    }
+    __syncthreads();
+    const uint32_t tiles_r = static_cast<uint32_t>((a.rows + kSide - 1) / kSide);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const uint32_t c = pc * kPiece + j;
+      float scale;
+      mul[j] = f32_multiplier(max(max(maxima[0][c], maxima[1][c]), max(maxima[2][c], maxima[3][c])), kMax, &scale);
+      if (pr == 0 && c < cols) a.scales_t[(c0 + c) * tiles_r + tr] = scale;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) {
+    float column[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) column[i] = v[i][j];
+    const Codes<kPiece> codes = encode_piece<XF>(column, mul[j]);
+    *reinterpret_cast<u32x2*>(turned + (pc * kPiece + j) * kSide + (pr ^ pc) * kPiece) = u32x2{codes.w[0], codes.w[1]};
+  }
+  __syncthreads();
+  // 16 rows of a column a lane.
+  const uint32_t rows_t = static_cast<uint32_t>(min<uint64_t>(kSide, a.rows_t - r0));
+  uint8_t* out = static_cast<uint8_t*>(a.codes_t) + c0 * a.codes_t_stride + r0;
+  const uint32_t r = threadIdx.x % 8 * 16;
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) {
+    const uint32_t c = i * 32 + threadIdx.x / 8, key = c / kPiece;
+    u32x4 w = *reinterpret_cast<const u32x4*>(turned + c * kSide + ((r / kPiece) ^ (key & ~1u)) * kPiece);
+    if (key % 2) w = u32x4{w[2], w[3], w[0], w[1]};
+    if (c >= cols) continue;
+    uint8_t* to = out + c * a.codes_t_stride + r;
+    if (a.vec_t) {
+      if (r < rows_t) *reinterpret_cast<u32x4*>(to) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (r + j < rows_t) to[j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
+    }
+  }
+}
+
+template <int IO, int XF, bool BY_BLOCK>
+hipError_t launch_typed(const BlocksLaunch& l, hipStream_t stream) {
+  const uint64_t tiles = (l.rows + kSide - 1) / kSide * ((l.cols + kSide - 1) / kSide);
+  if (tiles == 0 || tiles >= uint64_t{1} << 24) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 work-items
+  return launch_kernel(l.vec ? blocks_kernel<IO, XF, BY_BLOCK, true> : blocks_kernel<IO, XF, BY_BLOCK, false>,
+                       dim3(static_cast<uint32_t>(tiles)), dim3(256), stream, l);
+}
+
+template <int IO>
+hipError_t launch_io(const BlocksLaunch& l, hipStream_t stream) {
+  if (l.x_format == kXE4M3FN)
+    return l.by_block ? launch_typed<IO, kXE4M3FN, true>(l, stream) : launch_typed<IO, kXE4M3FN, false>(l, stream);
+  if (l.x_format == kXE5M2)
+    return l.by_block ? launch_typed<IO, kXE5M2, true>(l, stream) : launch_typed<IO, kXE5M2, false>(l, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_blocks(const BlocksLaunch& l, hipStream_t stream) {
+  switch (l.io_format) {
+    case kOutF32: return launch_io<kOutF32>(l, stream);
+    case kOutBF16: return launch_io<kOutBF16>(l, stream);
+    case kOutF16: return launch_io<kOutF16>(l, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace qrs

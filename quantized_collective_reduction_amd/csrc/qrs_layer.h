@@ -67,6 +67,65 @@ uint32_t norm_backward_parts(uint64_t rows, uint32_t h);
 
 hipError_t launch_norm_backward(const NormBackwardLaunch& l, hipStream_t stream);
 
+// Rows to codes through the layer norm: RowsLaunch's fields.
+struct LayerNormLaunch {
+  OutFormat io_format;
+  XFormat x_format;
+  int scale_layout;  // ScaleLayout or kScaleF32Row
+  bool vec;  // h % 8 == 0, and every row starts on a 16-byte boundary (codes: 8)
+  uint32_t h;
+  float eps;
+  double inv_h;  // 1 / h
+  uint64_t rows;
+  const void* x;
+  uint64_t x_stride;
+  const void* residual;  // nullptr: none
+  uint64_t residual_stride;
+  const void* weight;
+  const void* bias;  // nullptr: zero
+  void* sum;  // written where there is a residual
+  uint64_t sum_stride;
+  void* codes;
+  uint64_t codes_stride;
+  void* scales;
+};
+
+// h in [1, kMaxRowElems], a multiple of the layout's group.
+hipError_t launch_layer_norm(const LayerNormLaunch& l, hipStream_t stream);
+
+struct LayerNormBackwardLaunch : NormBackwardLaunch {
+  float* grad_bias;  // nullptr: not wanted. workspace: layer_norm_backward_parts(rows, h) rows of 2 h floats
+};
+
+// Work-groups of the backward pass, and rows of its workspace.
+uint32_t layer_norm_backward_parts(uint64_t rows, uint32_t h);
+
+hipError_t launch_layer_norm_backward(const LayerNormBackwardLaunch& l, hipStream_t stream);
+
+// 128 x 128 blocks of x [rows, cols] to codes and, transposed, to codes_t
+// [cols, rows_t], whose columns from `rows` on are zeros (rows_t: less than the
+// next multiple of 128 away). by_block: one scale for each block; else codes have a scale
+// for each row and 128 columns, codes_t for each column and 128 rows. Strides
+// in elements.
+struct BlocksLaunch {
+  OutFormat io_format;
+  XFormat x_format;  // kXE4M3FN or kXE5M2
+  bool by_block;
+  bool vec;    // cols % 8 == 0, and every row of x starts on a 16-byte boundary, of codes on 8
+  bool vec_t;  // rows_t % 16 == 0, and every row of codes_t starts on a 16-byte boundary
+  uint64_t rows, cols, rows_t;
+  const void* x;
+  uint64_t x_stride;
+  void* codes;  // nullptr: none, like its scales
+  uint64_t codes_stride;
+  float* scales;
+  void* codes_t;  // nullptr: none, like its scales
+  uint64_t codes_t_stride;
+  float* scales_t;
+};
+
+hipError_t launch_blocks(const BlocksLaunch& l, hipStream_t stream);
+
 // P = a b^T of int8 a [m, k] and b [n, k] (gated: [2n, k]), strides in
 // bytes, scaled and written as values (quantize = false) or as codes and
 // scales (quantize = true).
@@ -99,6 +158,22 @@ constexpr int64_t kMaxMatmulK = 131071;
 // launching nothing, beyond that.
 hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream);
 
+// P = a b^T of 8-bit floating-point codes, whose scales are those of groups of
+// 128 of k: a's of each row, b's of each row (grouped) or of each 128 rows
+// (gated: of the gates, then of the ups). a and b hold the codes; a_scales and
+// b_scales are [.., groups].
+struct MatmulFp8Launch : MatmulLaunch {
+  XFormat a_format, b_format;  // kXE4M3FN or kXE5M2
+  bool grouped;                // not gated, quantize = false
+  uint32_t groups;             // ceil(k / 128)
+  uint32_t up_block;           // gated: the first of the ups' rows of b_scales
+};
+
+constexpr int64_t kMaxFp8K = int64_t{1} << 24;
+
+// As launch_matmul.
+hipError_t launch_matmul_fp8(const MatmulFp8Launch& l, hipStream_t stream);
+
 // The kernel that launch_matmul takes: its family, and its tile in tokens and
 // rows of b.
 enum MatmulFamily : uint32_t { kMatmulTiles = 0, kMatmulFewTokens = 1, kMatmulMid = 2, kMatmulPipe = 3 };
@@ -112,5 +187,6 @@ struct MatmulShape {
   uint32_t threads;
 };
 MatmulShape matmul_shape(const MatmulLaunch& l);
+MatmulShape matmul_fp8_shape(const MatmulFp8Launch& l);
 
 }  // namespace qrs

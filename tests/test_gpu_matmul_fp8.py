@@ -1,0 +1,318 @@
+"""GPU parity of matmul_fp8 and matmul_fp8_quantize against oracle/blocks.py in
+64 bits. Operands of small whole numbers, whose sums binary32 holds in any order,
+pin every index: results equal the oracle's bit for bit."""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_collective_reduction_amd as qrs
+from fp8_util import FP8, G, Operands, assert_codes_within, float_bits, fp8, up
+from gpu_util import out_bits
+from layer_util import TORCH, device, empty_codes, host, padded
+from oracle.blocks import quantize_groups
+from oracle.layer import HALF_STEP
+from oracle.quantize import quantize_values
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [("e4m3fn", "e4m3fn"), ("e4m3fn", "e5m2"), ("e5m2", "e4m3fn"), ("e5m2", "e5m2")]
+KINDS = ["bf16", "f16", "f32"]
+
+
+def _run(o, kind, a=None, b=None):
+    out = torch.full((o.m, o.n), float("nan"), dtype=TORCH[kind], device="cuda")
+    da, sa, db, sb = o.device()
+    qrs.matmul_fp8(da if a is None else a, sa, db if b is None else b, sb, out, gated=o.gated)
+    return out
+
+
+def _check_whole(o, kind, a=None, b=None):
+    got, want = out_bits(_run(o, kind, a, b)), float_bits(o.want()[0], kind)
+    bad = np.argwhere((got != want) & (((got | want) << 1) != 0))  # zeros of either sign
+    assert bad.size == 0, (len(bad), bad[:4])
+
+
+def _check(o, kind):
+    want, tol = o.want()
+    tol = tol + np.abs(want) * HALF_STEP[kind] * 1.01 + (2.0 ** -25 if kind == "f16" else 0)
+    off = np.abs(host(_run(o, kind)) - want)
+    assert np.all(off <= tol), np.max(off / tol)
+
+
+SIZES = [
+    # one token to a few, every row of a fragment
+    (1, 8192, 512), (1, 1, 16), (1, 33, 48), (2, 100, 4096), (3, 640, 1040), (7, 64, 8192), (8, 2048, 2064),
+    (15, 200, 272), (16, 1000, 1024), (17, 512, 640), (24, 96, 7168), (31, 77, 96), (32, 4096, 256), (33, 130, 1600),
+    (48, 256, 4112), (63, 63, 64), (64, 640, 512),
+    # tiles and their edges
+    (65, 129, 128), (100, 1000, 1008), (127, 255, 144), (128, 128, 128), (129, 257, 272), (200, 520, 2048),
+    (255, 511, 528), (256, 256, 256), (257, 640, 384), (333, 1280, 1792), (400, 2000, 80), (512, 512, 4096),
+    (513, 769, 1152), (777, 1111, 336), (1024, 1024, 1024), (1100, 2304, 512), (2048, 1000, 208),
+]
+
+
+def _kind(m, n, k):
+    return KINDS[(m + n + k // 16) % 3]
+
+
+@pytest.mark.parametrize("grouped", [False, True], ids=["block", "group"])
+@pytest.mark.parametrize("m,n,k", SIZES, ids=lambda v: str(v))
+def test_product(gpu, m, n, k, grouped):
+    rng = np.random.default_rng([m, n, k])
+    for i, (ta, tb) in enumerate(TYPES):
+        if i and (m + n) % 4 != i:
+            continue  # E4M3 by E4M3 at each size, another pair at most
+        _check_whole(Operands(rng, m, n, k, ta, tb, grouped=grouped, whole=True), _kind(m, n, k))
+
+
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(t))
+@pytest.mark.parametrize("grouped", [False, True], ids=["block", "group"])
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 2048), (20, 384, 1168), (90, 1000, 784), (333, 640, 1024), (1030, 2304, 512),
+                                   (5, 130, 333)])
+def test_product_of_any_values(gpu, m, n, k, grouped, types):
+    rng = np.random.default_rng([m, n, k, 7])
+    _check(Operands(rng, m, n, k, *types, grouped=grouped), "f32")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_product_is_rounded_once(gpu, kind):
+    rng = np.random.default_rng(5)
+    _check(Operands(rng, 70, 640, 1024), kind)
+
+
+@pytest.mark.parametrize("grouped", [False, True], ids=["block", "group"])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 5, 3), (3, 7, 15), (2, 130, 17), (66, 65, 100), (130, 131, 1001),
+                                   (5, 1000, 4095), (200, 300, 129)])
+def test_product_at_any_k(gpu, m, n, k, grouped):
+    rng = np.random.default_rng([m, n, k])
+    for kind in KINDS:
+        _check_whole(Operands(rng, m, n, k, grouped=grouped, whole=True), kind)
+
+
+@pytest.mark.parametrize("m,n", [(1, 300), (40, 70), (300, 300)])
+@pytest.mark.parametrize("shift", [1, 2, 4, 8])
+def test_product_of_rows_off_their_lines(gpu, m, n, shift):
+    """Operands that start off 16-byte boundaries, or whose row stride is no
+    multiple of 16; what lies beside them is 448 and must not be added."""
+    rng = np.random.default_rng([m, n, shift])
+    o = Operands(rng, m, n, 256, whole=True)
+    _check_whole(o, "f32", a=padded(device(o.a), shift, 16 - shift, 0x7E)[1].view(FP8["e4m3fn"]))
+    _check_whole(o, "f32", b=padded(device(o.b), 0, shift, 0x7E)[1].view(FP8["e4m3fn"]))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 200, 528), (16, 128, 1040), (40, 300, 272), (300, 520, 176), (600, 900, 400)])
+def test_product_of_column_ranges(gpu, m, n, k):
+    """Column ranges of wider matrices, NaN beside them."""
+    rng = np.random.default_rng([m, n, k, 1])
+    o = Operands(rng, m, n, k, whole=True)
+    da = padded(device(o.a), 16, 32, 0x7F)[1].view(FP8["e4m3fn"])
+    db = padded(device(o.b), 32, 16, 0xFF)[1].view(FP8["e4m3fn"])
+    for left, right in [(8, 8), (1, 2)]:
+        buf, out = padded(torch.zeros(m, n, dtype=torch.bfloat16, device="cuda"), left, right, 5.0)
+        qrs.matmul_fp8(da, device(o.sa), db, device(o.sb), out)
+        assert np.array_equal(host(out.contiguous()), host(torch.from_numpy(o.want()[0]).bfloat16()))
+        assert torch.all(buf[:, :left] == 5) and torch.all(buf[:, left + n:] == 5)
+
+
+@pytest.mark.parametrize("far", ["a", "b", "out"])
+@pytest.mark.parametrize("m,n,k", [(12, 300, 80), (140, 200, 144)])
+def test_product_of_far_rows(gpu, m, n, k, far):
+    """Rows 4 MiB and more apart: a tile's rows span more than 2^30 bytes."""
+    rng = np.random.default_rng([m, n, k, 5])
+    o = Operands(rng, m, n, k, whole=True)
+    spread = lambda t, stride: torch.empty_strided(t.shape, (stride, 1), dtype=t.dtype, device="cuda").copy_(t)
+    da, sa, db, sb = o.device()
+    if far == "a":
+        da = spread(da.view(torch.uint8), (1 << 22) + 16).view(FP8["e4m3fn"])
+    if far == "b":
+        db = spread(db.view(torch.uint8), (1 << 22) + 32).view(FP8["e4m3fn"])
+    out = spread(torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda"), (1 << 22) + 8 if far == "out" else n)
+    qrs.matmul_fp8(da, sa, db, sb, out)
+    assert np.array_equal(host(out.contiguous()), host(torch.from_numpy(o.want()[0]).bfloat16()))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 640), (20, 300, 640), (90, 300, 640), (600, 900, 640)])
+def test_codes_and_scales_that_are_not_finite(gpu, m, n, k):
+    """NaN and infinite codes and scales go where the formula takes them, and
+    nowhere else."""
+    rng = np.random.default_rng([m, n])
+    o = Operands(rng, m, n, k, "e5m2", "e4m3fn", whole=True)
+    o.b[7, 130], o.b[n - 1, 5] = 0x7F, 0xFF  # NaN
+    o.a[0, 300] = 0x7C  # infinity
+    o.b[9, 300] = 0  # infinity times zero
+    if m > 3:
+        o.sa[3, 1] = np.nan
+        o.a[2, 0] = 0x7E  # NaN
+    da, sa, db, sb = o.device()
+    out = torch.empty(m, n, device="cuda")
+    qrs.matmul_fp8(da, sa, db, sb, out)
+    with np.errstate(invalid="ignore"):
+        a, b = o.values()
+        want = np.zeros((m, n))
+        for g in range(up(k)):
+            part = slice(g * G, min((g + 1) * G, k))
+            want += a[:, part] @ b[:, part].T
+    got = host(out)
+    finite = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[finite], want[finite].astype(np.float32))
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf])
+
+
+GATED = [(1, 1, 16), (1, 2048, 1024), (4, 100, 272), (16, 1792, 512), (17, 33, 64), (64, 256, 2048), (100, 130, 96),
+         (128, 128, 256), (130, 1000, 528), (333, 640, 1024), (600, 700, 304), (1030, 1280, 512), (3, 9, 35)]
+
+
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "-".join(t))
+@pytest.mark.parametrize("m,n,k", GATED)
+def test_gated(gpu, m, n, k, types):
+    rng = np.random.default_rng([m, n, k, 2])
+    kind = KINDS[(m + n) % 3]
+    o = Operands(rng, m, n, k, *types, gated=True, whole=True)
+    # Gates of a few units, both signs.
+    o.sa *= np.float32(2.0 ** -np.round(np.log2(k) / 2))
+    _check(o, kind)
+
+
+@pytest.mark.parametrize("m", [1, 20, 40, 300])
+def test_gated_at_gates_of_any_size(gpu, m):
+    g = np.array([-3e38, -1e30, -1e4, -104, -89, -88, -87, 0, 1e30, 3e38, np.inf, -np.inf, np.nan], np.float32)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = g.astype(np.float64) / (1.0 + np.exp(-g.astype(np.float64)))
+    bound = np.where(np.isfinite(want), np.abs(want) * 16 * 2.0 ** -24 + 2.0 ** -100, 0.0)
+    one = 0x38  # 1.0
+    a, b = np.zeros((m, 16), np.uint8), np.zeros((2, 16), np.uint8)
+    a[:, 0] = b[:, 0] = one
+    for i, v in enumerate(g):
+        out = torch.empty(m, 1, device="cuda")
+        sb = np.array([[v], [1.0]], np.float32)
+        qrs.matmul_fp8(fp8(a, "e4m3fn"), torch.ones(m, 1, device="cuda"), fp8(b, "e4m3fn"), device(sb), out, gated=True)
+        got = host(out)
+        with np.errstate(invalid="ignore"):
+            assert np.all((np.abs(got - want[i]) <= bound[i]) | (got == want[i]) | (np.isnan(got) & np.isnan(want[i]))), v
+
+
+MODES = [("int8", "f32_group128"), ("e4m3fn", "f32_group128"), ("e5m2", "f32_group128"), ("e4m3fn", "e8m0_block32"),
+         ("e5m2", "e8m0_block32")]
+CODE_SIZES = [(1, 128, 16), (1, 4096, 1024), (5, 256, 3584), (16, 1024, 272), (33, 384, 64), (64, 2048, 512),
+              (130, 640, 1040), (300, 1280, 256), (1030, 2048, 512), (7, 128, 37)]
+
+
+@pytest.mark.parametrize("x_format,layout", MODES)
+@pytest.mark.parametrize("m,n,k", CODE_SIZES)
+def test_quantized_product(gpu, m, n, k, x_format, layout):
+    rng = np.random.default_rng([m, n, k, 3])
+    o = Operands(rng, m, n, k, *TYPES[(m + n + k) % 4], whole=True)
+    if m > 2:
+        o.sa[1] = 0  # a row of zeros
+    codes, scales = empty_codes(m, n, layout)
+    qrs.matmul_fp8_quantize(*o.device(), codes, scales, x_format, layout)
+    c, s = quantize_values(o.want()[0].astype(np.float32), x_format, layout)
+    assert np.array_equal(scales.cpu().numpy().reshape(s.shape), s)
+    got = codes.cpu().numpy()
+    # Zeros may keep their sign in floating codes.
+    bad = (got != c) & (((got | c) & 0x7F) != 0) if x_format != "int8" else got != c
+    assert not bad.any(), np.argwhere(bad)[:4]
+
+
+@pytest.mark.parametrize("x_format,layout", MODES)
+@pytest.mark.parametrize("m,n,k", CODE_SIZES)
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+def test_quantized_product_of_any_values(gpu, m, n, k, x_format, layout, gated):
+    rng = np.random.default_rng([m, n, k, 4])
+    o = Operands(rng, m, n, k, gated=gated)
+    codes, scales = empty_codes(m, n, layout)
+    qrs.matmul_fp8_quantize(*o.device(), codes, scales, x_format, layout, gated=gated)
+    want, tol = o.want()
+    assert_codes_within(codes.cpu().numpy(), scales.cpu().numpy(), want, tol, x_format, layout)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 256, 64), (30, 256, 64), (200, 512, 128), (1030, 2048, 256), (3, 256, 17)])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("x_format,layout", [("int8", "f32_group128"), ("e4m3fn", "e8m0_block32")])
+def test_quantized_product_that_is_not_finite(gpu, m, n, k, x_format, layout, gated):
+    """NaN and sums that overflow show in the scales of their groups alone."""
+    rng = np.random.default_rng([m, n, k, 5])
+    o = Operands(rng, m, n, k, gated=gated, whole=True)
+    clean_codes, clean_scales = empty_codes(m, n, layout)
+    qrs.matmul_fp8_quantize(*o.device(), clean_codes, clean_scales, x_format, layout, gated=gated)
+    o.b[40, 3] = 0x7F  # NaN in channel 40
+    codes, scales = empty_codes(m, n, layout)
+    qrs.matmul_fp8_quantize(*o.device(), codes, scales, x_format, layout, gated=gated)
+    g = 32 if layout == "e8m0_block32" else 128
+    got = scales.reshape(m, n // g)
+    bad = got == 255 if g == 32 else ~torch.isfinite(got)
+    assert torch.all(bad[:, 40 // g])
+    bad[:, 40 // g] = False
+    assert not bad.any()
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[40 // g * g:40 // g * g + g] = False
+    assert torch.equal(codes[:, keep], clean_codes[:, keep])
+    o.b[40, 3] = 0x38
+    o.sa[m - 1] = np.float32(3e38)  # a row whose products overflow
+    qrs.matmul_fp8_quantize(*o.device(), codes, scales, x_format, layout, gated=gated)
+    got = scales.reshape(m, n // g)
+    bad = got == 255 if g == 32 else ~torch.isfinite(got)
+    assert bad[m - 1].any() and not bad[:m - 1].any()
+
+
+def test_codes_held_as_bytes(gpu):
+    rng = np.random.default_rng(1)
+    o = Operands(rng, 9, 200, 256, "e5m2", "e4m3fn", whole=True)
+    da, sa, db, sb = o.device()
+    out = torch.empty(9, 200, device="cuda")
+    qrs.matmul_fp8(da.view(torch.uint8), sa, db.view(torch.uint8), sb, out, a_dtype="e5m2", b_dtype="e4m3fn")
+    assert np.array_equal(host(out), o.want()[0])
+    for bad in [lambda: qrs.matmul_fp8(da.view(torch.uint8), sa, db, sb, out),
+                lambda: qrs.matmul_fp8(da, sa, db, sb, out, a_dtype="e4m3fn"),
+                lambda: qrs.matmul_fp8(da, sa, db[:, :128], sb, out), lambda: qrs.matmul_fp8(da, sa[:, :1], db, sb, out),
+                lambda: qrs.matmul_fp8(da, sa, db, sb[:1], out), lambda: qrs.matmul_fp8(da, sa, db, sb.t(), out),
+                lambda: qrs.matmul_fp8(da, sa, db, sb, out.double()), lambda: qrs.matmul_fp8(da, sa.half(), db, sb, out),
+                lambda: qrs.matmul_fp8(da, sa, db, sb, out[:, :100]),
+                lambda: qrs.matmul_fp8(da, sa, db[:199], sb, out, gated=True)]:
+        with pytest.raises(ValueError):
+            bad()
+    codes, scales = empty_codes(9, 256, "f32_group128")
+    o = Operands(rng, 9, 256, 256, grouped=True)
+    with pytest.raises(ValueError, match="b_scales"):
+        qrs.matmul_fp8_quantize(*o.device(), codes, scales, "e4m3fn", "f32_group128")
+
+
+def test_blocks_feed_the_product(gpu):
+    """quantize_blocks' codes and scales are the product's b as they are, and
+    its transpose the b of the product that goes back."""
+    rng = np.random.default_rng(4)
+    n, k, m = 200, 300, 17
+    w = rng.standard_normal((n, k)).astype(np.float32)
+    codes, scales = torch.empty(n, k, dtype=FP8["e4m3fn"], device="cuda"), torch.empty(up(n), up(k), device="cuda")
+    codes_t = torch.empty(k, 208, dtype=FP8["e4m3fn"], device="cuda")
+    scales_t = torch.empty(up(k), up(n), device="cuda")
+    qrs.quantize_blocks(device(w), codes, scales, "e4m3fn", codes_t, scales_t)
+    held = quantize_groups(w, "e4m3fn", G, G)
+    o = Operands(rng, m, n, k, whole=True)
+    o.b, o.sb = held
+    out = torch.empty(m, n, device="cuda")
+    da, sa, _, _ = o.device()
+    qrs.matmul_fp8(da, sa, codes, scales, out)
+    want, tol = o.want()
+    assert np.all(np.abs(host(out) - want) <= tol)
+    back = Operands(rng, m, k, 208, whole=True)
+    back.a[:, n:] = 0
+    back.b = np.zeros((k, 208), np.uint8)
+    back.b[:, :n], back.sb = held[0].T, np.ascontiguousarray(held[1].T)
+    out = torch.empty(m, k, device="cuda")
+    da, sa, _, _ = back.device()
+    qrs.matmul_fp8(da, sa, codes_t, scales_t, out)
+    want, tol = back.want()
+    assert np.all(np.abs(host(out) - want) <= tol)
+
+
+def test_random_sizes(gpu):
+    rng = np.random.default_rng(77)
+    for case in range(60):
+        m, n = (int(np.exp(rng.uniform(0, np.log(1200)))) for _ in range(2))
+        k = int(np.exp(rng.uniform(0, np.log(4000))))
+        k = k if case % 4 == 0 else -(-k // 16) * 16
+        print(f"case {case}: m={m} n={n} k={k}", flush=True)
+        _check_whole(Operands(rng, m, n, k, *TYPES[case % 4], grouped=case % 3 == 0, whole=True), KINDS[case % 3])
