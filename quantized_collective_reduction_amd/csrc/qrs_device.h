@@ -211,6 +211,14 @@ __device__ __forceinline__ float wave_sum(float v) {
          (__builtin_bit_cast(float, lane_value(b, 32)) + __builtin_bit_cast(float, lane_value(b, 48)));
 }
 
+// A work-group barrier that orders LDS accesses alone: __syncthreads would also
+// wait for the loads of the next row.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Between writes to LDS and reads of them by other lanes of the same wave, and
 // between such reads and the next writes. LDS serves a wave's accesses in
 // order, so this costs no instruction; it keeps the compiler from moving one

@@ -74,14 +74,6 @@ struct RawPiece<kOutF16, true> : RawPiece16<kOutF16> {};
 // pass, 1074 MB: 195 us, as a stream 174; 59 MB, found there: 20.2 and 21.6).
 constexpr uint64_t kStreamBytes = uint64_t{256} << 20;
 
-// A work-group barrier that orders LDS accesses alone: __syncthreads would also
-// wait for the loads of the next row.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 __device__ __forceinline__ double wave_sum(double v) {
   auto from = [](double x, auto f) {
     const uint64_t b = __builtin_bit_cast(uint64_t, x);
