@@ -597,12 +597,18 @@ qrs_status qrs_matmul_float(int64_t m, int64_t n, int64_t k, int gated, qrs_out_
  * codes 16-byte aligned, its row stride a multiple of 16; scales contiguous
  * [m, n / G]. A group that holds a NaN or an infinity gets a NaN or infinite
  * scale (E8M0 code 255); its codes are unspecified.
+ *
+ *   workspace  DEVICE memory of at least qrs_matmul_float_quantize_workspace
+ *              bytes, 16-byte aligned, for this call alone until it ends; NULL
+ *              where that is 0 (more than 32 tokens; E8M0 scales, not gated).
  */
+qrs_status qrs_matmul_float_quantize_workspace(int64_t m, int64_t n, int gated, qrs_scale_layout scale_layout,
+                                               size_t* bytes_out);
 qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated, qrs_x_dtype x_dtype,
                                    qrs_scale_layout scale_layout, qrs_x_dtype a_dtype, const void* a,
                                    int64_t a_row_stride, const float* a_scales, qrs_x_dtype b_dtype, const void* b,
                                    int64_t b_row_stride, const float* b_scales, void* codes, int64_t codes_row_stride,
-                                   void* scales, void* stream);
+                                   void* scales, void* workspace, size_t workspace_bytes, void* stream);
 
 /* qrs_matmul_launch_info of these two products. */
 qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gated, int b_scale_rows, int quantize,

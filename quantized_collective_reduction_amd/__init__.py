@@ -137,6 +137,7 @@ EXPORTED_SYMBOLS = (
     "qrs_quantize_transposed",
     "qrs_matmul_float",
     "qrs_matmul_float_quantize",
+    "qrs_matmul_float_quantize_workspace",
     "qrs_matmul_float_launch_info",
 )
 
@@ -257,7 +258,9 @@ def load_library(path: str = LIB_PATH):
                                    vp, vp, c_i64, vp]
     lib.qrs_matmul_float.restype = c_int
     lib.qrs_matmul_float_quantize.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int, vp, c_i64, vp, c_int, vp,
-                                            c_i64, vp, vp, c_i64, vp, vp]
+                                              c_i64, vp, vp, c_i64, vp, vp, c_sz, vp]
+    lib.qrs_matmul_float_quantize_workspace.argtypes = [c_i64, c_i64, c_int, c_int, ctypes.POINTER(c_sz)]
+    lib.qrs_matmul_float_quantize_workspace.restype = c_int
     lib.qrs_matmul_float_quantize.restype = c_int
     lib.qrs_matmul_float_launch_info.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
                                                ctypes.POINTER(MatmulInfo)]
@@ -1097,21 +1100,27 @@ def matmul_fp8(a, a_scales, b, b_scales, out, gated=False, a_dtype=None, b_dtype
 
 
 def matmul_fp8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_layout, gated=False, a_dtype=None,
-                        b_dtype=None, stream=None):
+                        b_dtype=None, workspace=None, stream=None):
     """``matmul_fp8``'s product (b's scales those of 128 x 128 blocks),
     quantized in float32 into ``codes [m, n]`` and scales
     (qrs_matmul_float_quantize): one rank's partial sums, as ``run`` and
     ``run_all_shares`` read them, or with "f32_group128" the next product's a.
-    n is a multiple of 128."""
+    n is a multiple of 128. ``workspace``: device memory of
+    qrs_matmul_float_quantize_workspace's bytes, by default taken from torch's
+    allocator where any is needed."""
     lib = load_library()
     m, n, k, ka, ld_a, kb, scale_rows, ld_b = _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype)
     if scale_rows != _BLOCK:
         raise ValueError(f"b_scales: [{_blocks(n)}, {_blocks(k)}] expected, got {list(b_scales.shape)}")
     mode = _mode(x_dtype, scale_layout)
     ld_c = _codes_and_scales(codes, scales, (m, n), mode)
+    need = ctypes.c_size_t()
+    _check(lib.qrs_matmul_float_quantize_workspace(m, n, 1 if gated else 0, mode[1], ctypes.byref(need)))
+    ws, nbytes, _keep = _workspace(workspace, need.value, a, stream) if need.value else (None, 0, None)
     _check(lib.qrs_matmul_float_quantize(m, n, k, 1 if gated else 0, mode[0], mode[1], ka, a.data_ptr(), ld_a,
-                                       a_scales.data_ptr(), kb, b.data_ptr(), ld_b, b_scales.data_ptr(),
-                                       codes.data_ptr(), ld_c, scales.data_ptr(), _stream_handle(stream)))
+                                         a_scales.data_ptr(), kb, b.data_ptr(), ld_b, b_scales.data_ptr(),
+                                         codes.data_ptr(), ld_c, scales.data_ptr(), ws, nbytes,
+                                         _stream_handle(stream)))
 
 
 def run_launch_info(p: Plan, stream=None) -> dict:

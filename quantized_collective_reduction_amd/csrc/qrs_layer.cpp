@@ -642,6 +642,13 @@ qrs_status matmul_fp8(qrs::MatmulFp8Launch* l, int64_t m, int64_t n, int64_t k, 
     QRS_TRY(check_rows(scales));
     QRS_TRY(check_apart(scales, in, 4, false));
     QRS_TRY(check_apart(scales, &out, 1, false));
+    const Rows ws = {"workspace", l->workspace, m, n, n, 4};
+    if (ws.p) {
+      QRS_TRY(check_rows(ws));
+      QRS_TRY(check_apart(ws, in, 4, false));
+      QRS_TRY(check_apart(ws, &out, 1, false));
+      QRS_TRY(check_apart(ws, &scales, 1, false));
+    }
   }
   fp8_shape(l, m, n, k, gated, b_scale_rows);
   l->a_format = to_format(a_dtype);
@@ -708,7 +715,7 @@ qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated,
                                    qrs_scale_layout scale_layout, qrs_x_dtype a_dtype, const void* a,
                                    int64_t a_row_stride, const float* a_scales, qrs_x_dtype b_dtype, const void* b,
                                    int64_t b_row_stride, const float* b_scales, void* codes, int64_t codes_row_stride,
-                                   void* scales, void* stream) {
+                                   void* scales, void* workspace, size_t workspace_bytes, void* stream) {
   QRS_TRY(check_fp8_shape(m, n, k, gated));
   QRS_TRY(check_codes(x_dtype, scale_layout, false));
   QRS_TRY(check_multiple(n));
@@ -722,8 +729,28 @@ qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated,
   const Rows o = {"codes", codes, m, n, codes_row_stride, 1};
   if (codes && !o.rows_on(16)) return fail(QRS_ERR_INVALID_ARG, "rows of codes are not on 16-byte boundaries");
   const Rows s = {"scales", scales, m, n / g, n / g, e8m0 ? 1 : 4};
+  const uint64_t need = qrs::fp8_workspace(static_cast<uint64_t>(m), static_cast<uint64_t>(n), gated != 0, l.scale_layout);
+  if (need) {
+    if (!workspace || workspace_bytes < need)
+      return fail(QRS_ERR_INVALID_ARG, "the workspace must hold %llu bytes", static_cast<unsigned long long>(need));
+    if (!aligned(workspace, 16)) return fail(QRS_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    l.workspace = static_cast<float*>(workspace);
+  }
   return matmul_fp8(&l, m, n, k, gated, a_dtype, a, a_row_stride, a_scales, b_dtype, static_cast<int>(kSide), b,
                     b_row_stride, b_scales, o, s, stream);
+}
+
+qrs_status qrs_matmul_float_quantize_workspace(int64_t m, int64_t n, int gated, qrs_scale_layout scale_layout,
+                                               size_t* bytes_out) {
+  if (!bytes_out) return fail(QRS_ERR_INVALID_ARG, "null bytes_out");
+  *bytes_out = 0;
+  QRS_TRY(check_matmul_shape(m, n, 1, gated));
+  QRS_TRY(check_codes(QRS_X_FP8_E4M3FN, scale_layout, false));
+  QRS_TRY(check_multiple(n));
+  *bytes_out = qrs::fp8_workspace(static_cast<uint64_t>(m), static_cast<uint64_t>(n), gated != 0,
+                                  scale_layout == QRS_SCALE_E8M0_BLOCK32 ? qrs::kScaleE8M0Block32
+                                                                         : qrs::kScaleF32Group128);
+  return ok();
 }
 
 qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gated, int b_scale_rows, int quantize,

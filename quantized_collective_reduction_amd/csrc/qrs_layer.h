@@ -167,7 +167,16 @@ struct MatmulFp8Launch : MatmulLaunch {
   bool grouped;                // not gated, quantize = false
   uint32_t groups;             // ceil(k / 128)
   uint32_t up_block;           // gated: the first of the ups' rows of b_scales
+  float* workspace;            // fp8_workspace(..) bytes, 16-byte aligned
 };
+
+constexpr uint32_t kMaxFewTokens = 32;
+
+// What a product written as codes needs: binary32 values of few tokens, where
+// the outputs that share a scale are of more rows of b than a work-group should read.
+inline uint64_t fp8_workspace(uint64_t m, uint64_t n, bool gated, ScaleLayout layout) {
+  return m <= kMaxFewTokens && (gated || layout == kScaleF32Group128) ? m * n * 4 : 0;
+}
 
 constexpr int64_t kMaxFp8K = int64_t{1} << 24;
 

@@ -46,7 +46,31 @@ enum Form : int { kPlain = 0, kGatedForm = 1, kGrouped = 2 };
 
 constexpr uint32_t kGroup = 128;  // of k: a scale of a, and of b
 
+typedef const __attribute__((address_space(1))) void* global_ptr;
+
+// A wave's own loads to LDS but the last N have landed; its reads of LDS have.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_reads() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+template <XFormat AF, XFormat BF>
+__device__ __forceinline__ f32x4 sums8(const i32x8& b, const i32x8& a) {
+  // Operand formats: 0 E4M3, 1 E5M2. Both scale codes zero: the plain instruction.
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, BF == kXE5M2 ? 1 : 0,
+                                                          AF == kXE5M2 ? 1 : 0, 0, 0, 0, 0);
+}
 
 // Eight codes as bfloat16.
 template <XFormat F>
@@ -80,13 +104,11 @@ struct Wide {
   }
 };
 
-// The sums of a 16 x 16 fragment over its 64 N codes of each row.
+// The products of a 16 x 16 fragment over its 64 N codes of each row.
 template <int N>
-__device__ __forceinline__ f32x4 group_sums(const Wide<N>& b, const Wide<N>& a) {
-  f32x4 sums = {0.0f, 0.0f, 0.0f, 0.0f};
+__device__ __forceinline__ void add_products(f32x4& sums, const Wide<N>& b, const Wide<N>& a) {
 #pragma unroll
   for (int t = 0; t < 2 * N; ++t) sums = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.part[t], a.part[t], sums, 0, 0, 0);
-  return sums;
 }
 
 __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& sums, float scale) {
@@ -194,7 +216,8 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulFp8Launch a) {
       const float token = sa[i][g];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const f32x4 sums = group_sums(fb[j], fa);
+        f32x4 sums = {0.0f, 0.0f, 0.0f, 0.0f};
+        add_products(sums, fb[j], fa);
         if constexpr (FORM == kGrouped) {
           f32x4 s;
 #pragma unroll
@@ -295,7 +318,7 @@ __device__ __forceinline__ uint32_t max_bits(const float* v) {
   return m;
 }
 
-template <XFormat AF, XFormat BF, int FORM>
+template <XFormat AF, XFormat BF, int FORM, bool WIDE>
 __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8Launch a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the buffer builtins' types exist in the device pass alone
   using P = Pipe;
@@ -384,6 +407,46 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
   const uint32_t lane_off[2] = {lane % 16 * kGroup + ((lane / 16) ^ (lane % 16 / 2)) * 16u,
                                 lane % 16 * kGroup + ((4 + lane / 16) ^ (lane % 16 / 2)) * 16u};
   f32x4 acc[FM][FN];
+  auto compute8 = [&](uint32_t slot) {
+    const char* base = lds + slot * P::kBlock;
+    const char* la = base + wm * P::kWaveM * kGroup;
+    const char* lb = base + P::kSide * kGroup + wn * P::kWaveN * kGroup;
+    const float* sa = reinterpret_cast<const float*>(base + P::kOperands) + wm * P::kWaveM + lane % 16;
+    const float* sb = reinterpret_cast<const float*>(base + P::kOperands) + P::kSide + wn * P::kWaveN;
+    float token[FM], scale[FORM == kGatedForm ? 2 : 1][FM];
+    auto fragment = [&](const char* p) {
+      return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(p + lane_off[0]),
+                                     *reinterpret_cast<const i32x4*>(p + lane_off[1]), 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    i32x8 fa[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      token[i] = sa[16 * i];
+      fa[i] = fragment(la + i * 16 * kGroup);
+    }
+    if constexpr (FORM != kGrouped) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        scale[0][i] = token[i] * sb[0];
+        if constexpr (FORM == kGatedForm) scale[1][i] = token[i] * sb[32];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const i32x8 fb = fragment(lb + j * 16 * kGroup);
+      f32x4 sums[FM];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) sums[i] = sums8<AF, BF>(fb, fa[i]);
+      if constexpr (FORM == kGrouped) {
+        const f32x4 channels = *reinterpret_cast<const f32x4*>(sb + 16 * j + lane / 16 * 4);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) add_scaled(acc[i][j], sums[i], token[i], channels);
+      } else {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) add_scaled(acc[i][j], sums[i], scale[FORM == kGatedForm ? j / 2 % 2 : 0][i]);
+      }
+    }
+  };
   auto compute = [&](uint32_t slot) {
     const char* base = lds + slot * P::kBlock;
     const char* la = base + wm * P::kWaveM * kGroup;
@@ -450,7 +513,10 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
       else
         wait_loads_and_sync<0>();
       if (advance()) load();
-      compute(slot);
+      if constexpr (WIDE)
+        compute(slot);
+      else
+        compute8(slot);
       slot ^= 1;
     }
 
@@ -552,6 +618,386 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
 #endif
 }
 
+// ---- few tokens --------------------------------------------------------
+
+// Up to 8 * M8 tokens: the weights are read once and bound the time. A
+// work-group takes 32 or 16 (RB) rows of b times GW (gated: in runs of RB / 2 gates
+// and their ups); its GW parts of KW waves take RB rows each and share k: wave w
+// of a part takes every KW'th group of k, a line of 128 bytes of each row.
+//
+// Lines go from memory straight into a ring of the wave's own in LDS, S - 1 of them
+// ahead, so no wave waits for another before its last line, and no register for
+// a line under way. (With lines in registers, 16 waves of them, those that the
+// widened codes leave too few: 8192 x 8192 19.1 us.) A load covers 8 rows; chunk c
+// of row r lies in slot c ^ (r / 2 % 8), as in the pipelined tiles. One more load
+// brings the scales of the rows of b and of the tokens, one a lane.
+//
+// The waves' sums meet in LDS and are added in the order of the waves.
+template <int M8, int GW, int KW, int RB, int FORM>
+struct Few {
+  static constexpr int kWaves = GW * KW, MT = (M8 + 1) / 2, FB = RB / 16;
+  static constexpr int kLoadsB = RB / 8, kLoads = kLoadsB + M8 + 1;  // of a line
+  static constexpr int kScales = (RB + 8 * M8) * 128, kLine = kScales + 64 * 4;
+  // Two work-groups a CU where that leaves each a line ahead.
+  static constexpr int kPair = 81920 / (kWaves * kLine), kAlone = 163840 / (kWaves * kLine);
+  static constexpr int kFit = kPair >= 2 ? kPair : kAlone;
+  static constexpr int S = kFit < 3 ? kFit : 3;
+  static constexpr int kRing = kWaves * S * kLine + (M8 == 1 ? 1024 : 0);  // a fragment of 8 tokens is read as 16 rows
+  static constexpr int kPitch = RB + 4;                    // words of a token's sums
+  static constexpr int kSums = kWaves * 16 * MT * kPitch * 4;
+  static constexpr int kLds = kRing > kSums ? kRing : kSums;
+  static constexpr uint32_t kRows = RB * GW, kOut = FORM == kGatedForm ? kRows / 2 : kRows;
+  static_assert(S >= 2 && RB + 8 * M8 <= 64 && kLoads * (S - 1) < 64, "a line under way, a scale a lane, the counter");
+};
+
+template <XFormat AF, XFormat BF, int M8, int GW, int KW, int RB, int FORM>
+__global__ __launch_bounds__(64 * GW * KW) void few_tokens_kernel(const MatmulFp8Launch a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using P = Few<M8, GW, KW, RB, FORM>;
+  constexpr int MT = P::MT, FB = P::FB, S = P::S;
+  constexpr bool kGated = FORM == kGatedForm;
+  __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t part = wave / KW, kw = wave % KW;
+  const uint32_t j0 = blockIdx.x * P::kOut;
+
+  // Row r of the work-group's part of b.
+  auto channel = [&](uint32_t r) { return min(j0 + (kGated ? r / RB * (RB / 2) + r % (RB / 2) : r), a.n - 1); };
+  auto up = [](uint32_t r) { return kGated && r % RB >= RB / 2; };
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.a), 0, kFar, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar, 0x00020000);
+  // Load t of a line covers rows 8 t .. 8 t + 7, of b and then tokens.
+  const uint32_t chunk[2] = {(lane % 8 ^ lane / 16) * 16u, (lane % 8 ^ (4 + lane / 16)) * 16u};
+  uint32_t off_b[P::kLoadsB], off_a[M8];
+#pragma unroll
+  for (int t = 0; t < P::kLoadsB; ++t) {
+    const uint32_t r = part * RB + 8 * t + lane / 8;
+    off_b[t] = (channel(r) - j0 + (up(r) ? a.n : 0)) * static_cast<uint32_t>(a.b_stride) + chunk[t % 2];
+  }
+#pragma unroll
+  for (int t = 0; t < M8; ++t)  // tokens past the last: the last one, not stored
+    off_a[t] = min(8u * t + lane / 8, a.m - 1) * static_cast<uint32_t>(a.a_stride) + chunk[t % 2];
+  const float* scale;
+  if (lane < RB) {
+    const uint32_t r = part * RB + lane;
+    const uint32_t row = FORM == kGrouped ? channel(r) : channel(r) / kGroup + (up(r) ? a.up_block : 0);
+    scale = a.b_scales + static_cast<uint64_t>(row) * a.groups;
+  } else {
+    scale = a.a_scales + static_cast<uint64_t>(min(static_cast<uint32_t>(lane - RB), a.m - 1)) * a.groups;
+  }
+  char* mine = lds + wave * S * P::kLine;
+  auto load = [&](uint32_t g, uint32_t slot) {
+    const uint32_t at = min(g, a.groups - 1), k = g * kGroup;  // past the last group: zeros
+    char* to = mine + slot * P::kLine;
+#pragma unroll
+    for (int t = 0; t < P::kLoadsB; ++t) {
+      const uint32_t far = k + chunk[t % 2] < a.k ? 0 : kFar;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(to + t * 1024), 16, off_b[t] + far, k, 0, 2);  // streamed
+    }
+#pragma unroll
+    for (int t = 0; t < M8; ++t) {
+      const uint32_t far = k + chunk[t % 2] < a.k ? 0 : kFar;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(to + RB * 128 + t * 1024), 16, off_a[t] + far, k, 0, 0);
+    }
+    __builtin_amdgcn_global_load_lds((global_ptr)(scale + at), (lds_ptr)(to + P::kScales), 4, 0, 0);
+  };
+
+  f32x4 acc[MT][FB];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int h = 0; h < FB; ++h) acc[i][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (uint32_t s = 0; s < S; ++s) load(kw + s * KW, s);
+  const uint32_t lane_off[2] = {lane % 16 * 128 + ((lane / 16) ^ (lane % 16 / 2)) * 16u,
+                                lane % 16 * 128 + ((4 + lane / 16) ^ (lane % 16 / 2)) * 16u};
+  uint32_t slot = 0;
+  for (uint32_t g = kw; g < a.groups; g += KW) {
+    wait_loads<P::kLoads*(S - 1)>();
+    const char* line = mine + slot * P::kLine;
+    const float* scales = reinterpret_cast<const float*>(line + P::kScales);
+    i32x4 fb[FB][2], fa[MT][2];
+    float token[MT];
+    f32x4 channels[FB];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int h = 0; h < FB; ++h) fb[h][n] = *reinterpret_cast<const i32x4*>(line + h * 2048 + lane_off[n]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i][n] = *reinterpret_cast<const i32x4*>(line + (FB + i) * 2048 + lane_off[n]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) token[i] = scales[RB + 16 * i + lane % 16];
+#pragma unroll
+    for (int h = 0; h < FB; ++h) channels[h] = *reinterpret_cast<const f32x4*>(scales + 16 * h + lane / 16 * 4);
+    wait_reads();
+    load(g + S * KW, slot);
+    slot = slot + 1 == S ? 0 : slot + 1;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      Wide<2> wa;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) wa.template set<AF>(n, fa[i][n]);
+#pragma unroll
+      for (int h = 0; h < FB; ++h) {
+        Wide<2> wb;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) wb.template set<BF>(n, fb[h][n]);
+        f32x4 sums = {0.0f, 0.0f, 0.0f, 0.0f};
+        add_products(sums, wb, wa);
+        if constexpr (FORM == kGrouped)
+          add_scaled(acc[i][h], sums, token[i], channels[h]);
+        else
+          add_scaled(acc[i][h], sums, token[i] * channels[h][0]);
+      }
+    }
+  }
+
+  wait_loads_and_sync<0>();
+  // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16.
+  float* sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int h = 0; h < FB; ++h)
+      *reinterpret_cast<f32x4*>(sums + ((wave * MT + i) * 16 + lane % 16) * P::kPitch + h * 16 + lane / 16 * 4) =
+          acc[i][h];
+  __syncthreads();
+  constexpr uint32_t pieces = P::kOut / kPiece, part_pieces = pieces / GW;
+  // Of M8 = 1 a fragment's first 8 tokens.
+  for (uint32_t t = threadIdx.x; t < 8 * M8 * pieces; t += 64 * P::kWaves) {
+    const uint32_t i = t / pieces, piece = t % pieces;
+    const float* row = sums + (piece / part_pieces * KW * 16 * MT + i) * P::kPitch + piece % part_pieces * kPiece;
+    float v[kPiece], ups[kPiece];
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) v[e] = ups[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const float* p = row + w * 16 * MT * P::kPitch;
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) {
+        v[e] += p[e];
+        if constexpr (kGated) ups[e] += p[RB / 2 + e];
+      }
+    }
+    const uint32_t j = j0 + piece * kPiece;
+    finish_outputs<FORM>(a, i, j, i < a.m && j < a.n, v, ups);
+  }
+#endif
+}
+
+// ---- tens to hundreds of tokens ----------------------------------------
+
+// Too few tiles of the pipelined kernel for 256 CUs: TM tokens by TN rows of
+// b a work-group. Its eight waves are KG ways of sharing k, WM of the tokens and
+// the rest of the rows of b; wave (g, w) takes group g of each stage's KG groups.
+//
+// A stage is KG groups of k of all rows, loaded straight into LDS, 8 rows a
+// load, S - 1 stages ahead, with their scales, so that most of LDS holds operands in
+// flight, in whole lines. What bounds these tiles is how fast operands come
+// into a CU, and next the widening of their codes. Slots as in the pipelined tiles.
+// Two waves a SIMD hide each other's reads; one barrier a stage.
+template <int TM, int TN, int KG, int WM, int S>
+struct Mid {
+  static constexpr int kThreads = 512, kWavesN = 8 / KG / WM, WTM = TM / WM, WTN = TN / kWavesN;
+  static constexpr int FM = WTM / 16, FN = WTN / 16;
+  static constexpr int kRows = TM + TN;
+  static constexpr int kOperands = kRows * KG * 128, kStage = kOperands + 8 * 64 * 4;
+  static constexpr int kLoads = kOperands / 1024 / 8 + 1;  // of a wave
+  static constexpr int kPitch = TN + 4;                    // words of a token's sums
+  static constexpr int kSums = KG * TM * kPitch * 4;
+  static constexpr int kLds = S * kStage > kSums ? S * kStage : kSums;
+  static_assert(kOperands % 8192 == 0 && WTN % 16 == 0 && WTM % 16 == 0, "whole loads and fragments");
+  static_assert(kRows * KG <= 512 && kLds <= 163840, "one scale a lane");
+};
+
+template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM>
+__global__ __launch_bounds__(512, 2) void mid_kernel(const MatmulFp8Launch a) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using P = Mid<TM, TN, KG, WM, S>;
+  constexpr int FM = P::FM, FN = P::FN;
+  constexpr bool kGated = FORM == kGatedForm;
+  // One array: with several, the compiler tells their accesses apart and
+  // waits for every load to LDS before it reads any.
+  __shared__ __attribute__((aligned(1024))) char lds[P::kLds];
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int kg = wave % KG, wm = wave / KG % WM, wn = wave / KG / WM;
+
+  constexpr uint32_t kOut = kGated ? TN / 2 : TN;
+  const TileOrder order = {(a.m + TM - 1) / TM, (a.n + kOut - 1) / kOut};
+  const uint32_t tiles = order.tiles_m * order.tiles_n, xcd = blockIdx.x % 8;
+  uint32_t tm, tn;
+  order.at((tiles / 8) * xcd + min(xcd, tiles % 8) + blockIdx.x / 8, &tm, &tn);
+  const uint32_t i0 = tm * TM, j0 = tn * kOut;
+  // Row r of the tile's part of b: in the gated form every fragment of 16
+  // gates is followed by their ups.
+  auto channel = [&](uint32_t r) { return min(j0 + (kGated ? r / 32 * 16 + r % 16 : r), a.n - 1); };
+  auto up = [](uint32_t r) { return kGated && r % 32 >= 16; };
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(a.a + static_cast<uint64_t>(i0) * a.a_stride), 0, kFar, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int8_t*>(a.b + static_cast<uint64_t>(j0) * a.b_stride), 0, kFar, 0x00020000);
+
+  // Load t covers rows 8 (t % (kRows / 8)) .. + 7 of group t / (kRows / 8);
+  // lane l the chunk of row l / 8 whose slot is l % 8.
+  constexpr int kCodeLoads = P::kLoads - 1;
+  uint32_t offset[kCodeLoads], in_k[kCodeLoads];
+#pragma unroll
+  for (int t = 0; t < kCodeLoads; ++t) {
+    const uint32_t at = wave * kCodeLoads + t, r = at % (P::kRows / 8) * 8 + lane / 8;
+    in_k[t] = at / (P::kRows / 8) * 128 + (lane % 8 ^ (r / 2 % 8)) * 16;
+    const uint32_t q = r - TM;
+    offset[t] = (r < TM ? (min(i0 + r, a.m - 1) - i0) * static_cast<uint32_t>(a.a_stride)
+                        : (channel(q) - j0 + (up(q) ? a.n : 0)) * static_cast<uint32_t>(a.b_stride)) + in_k[t];
+  }
+  // Lane l of wave w loads the scale of row (64 w + l) % kRows in group (64 w + l) / kRows.
+  const uint32_t scale_at = threadIdx.x, scale_row = scale_at % P::kRows;
+  const uint32_t scale_group = min(scale_at / P::kRows, KG - 1u);
+  const float* scale;
+  if (scale_row < TM) {
+    scale = a.a_scales + static_cast<uint64_t>(min(i0 + scale_row, a.m - 1)) * a.groups;
+  } else {
+    const uint32_t q = scale_row - TM;
+    const uint32_t row = FORM == kGrouped ? channel(q) : channel(q) / kGroup + (up(q) ? a.up_block : 0);
+    scale = a.b_scales + static_cast<uint64_t>(row) * a.groups;
+  }
+  // Load t of stage st, to `slot`; `full`: the stage ends inside k.
+  auto load = [&](uint32_t st, uint32_t slot, int t, bool full) {
+    char* to = lds + slot * P::kStage;
+    if (t == kCodeLoads) {  // past the last group: its scales, which nothing is multiplied by
+      __builtin_amdgcn_global_load_lds((global_ptr)(scale + min(st * KG + scale_group, a.groups - 1)),
+                                       (lds_ptr)(to + P::kOperands + wave * 256), 4, 0, 0);
+      return;
+    }
+    const uint32_t k = __builtin_amdgcn_readfirstlane(st * KG * 128);
+    const uint32_t at = wave * kCodeLoads + t;
+    const uint32_t far = full || k + in_k[t] < a.k ? 0 : kFar;  // past the end of k: zeros
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(at % (P::kRows / 8) * 8 < TM ? ra : rb, (lds_ptr)(to + at * 1024), 16,
+                                             offset[t] + far, k, 0, 0);
+  };
+
+  const uint32_t stages = (a.groups + KG - 1) / KG, full_stages = a.k / (KG * 128);
+#pragma unroll
+  for (uint32_t st = 0; st < S; ++st)  // past the last stage: zeros
+#pragma unroll
+    for (int t = 0; t < P::kLoads; ++t) load(st, st, t, false);
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // Lane l reads row l % 16 of a fragment, chunks l / 16 and 4 + l / 16.
+  const uint32_t lane_off[2] = {lane % 16 * 128 + ((lane / 16) ^ (lane % 16 / 2)) * 16u,
+                                lane % 16 * 128 + ((4 + lane / 16) ^ (lane % 16 / 2)) * 16u};
+  const char* frag_a = lds + (kg * P::kRows + wm * P::WTM) * 128;
+  const char* frag_b = lds + (kg * P::kRows + TM + wn * P::WTN) * 128;
+  const char* scales_a = lds + P::kOperands + (kg * P::kRows + wm * P::WTM + lane % 16) * 4;
+  const char* scales_b = lds + P::kOperands + (kg * P::kRows + TM + wn * P::WTN + lane / 16 * 4) * 4;
+  constexpr int kScalesB = FORM == kGrouped ? 4 : 1;  // of a lane, in each fragment
+  struct Fragments {  // of a stage
+    i32x4 a[FM][2], b[FN][2];
+    float token[FM], channel[FN][kScalesB];
+  } now, next;
+  auto read_a = [&](Fragments& f, uint32_t slot, int i) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      f.a[i][n] = *reinterpret_cast<const i32x4*>(frag_a + slot * P::kStage + i * 2048 + lane_off[n]);
+    f.token[i] = *reinterpret_cast<const float*>(scales_a + slot * P::kStage + 64 * i);
+  };
+  auto read_b = [&](Fragments& f, uint32_t slot, int j) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      f.b[j][n] = *reinterpret_cast<const i32x4*>(frag_b + slot * P::kStage + j * 2048 + lane_off[n]);
+#pragma unroll
+    for (int e = 0; e < kScalesB; ++e)
+      f.channel[j][e] = *reinterpret_cast<const float*>(scales_b + slot * P::kStage + 64 * j + 4 * e);
+  };
+  // Multiplies stage st (in registers, its LDS `slot`) while stage st + 1 is
+  // read and stage st + S loaded into st's place in LDS.
+  auto stage = [&](uint32_t st, uint32_t slot, bool full) {
+    wait_loads_and_sync<P::kLoads*(S - 2)>();
+    const uint32_t after = slot + 1 == S ? 0 : slot + 1;
+    Wide<2> wb[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) wb[j].template set<BF>(n, now.b[j][n]);
+      read_b(next, after, j);
+    }
+    const bool live = full || st * KG + kg < a.groups;  // scales past the last group may be anything
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      Wide<2> wa;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) wa.template set<AF>(n, now.a[i][n]);
+      read_a(next, after, i);
+#pragma unroll
+      for (int t = i * P::kLoads / FM; t < (i + 1) * P::kLoads / FM; ++t) load(st + S, slot, t, full);
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          f32x4 sums = {0.0f, 0.0f, 0.0f, 0.0f};
+          add_products(sums, wb[j], wa);
+          if constexpr (FORM == kGrouped)
+            add_scaled(acc[i][j], sums, now.token[i],
+                       f32x4{now.channel[j][0], now.channel[j][1], now.channel[j][2], now.channel[j][3]});
+          else
+            add_scaled(acc[i][j], sums, now.token[i] * now.channel[j][0]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    now = next;
+  };
+  wait_loads_and_sync<P::kLoads*(S - 1)>();
+#pragma unroll
+  for (int j = 0; j < FN; ++j) read_b(now, 0, j);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) read_a(now, 0, i);
+  uint32_t st = 0;
+  // Rounds with fixed slots and nothing to check, while all that they load is
+  // inside k; then a stage at a time.
+  for (; st + 2 * S <= full_stages; st += S) {
+#pragma unroll
+    for (uint32_t r = 0; r < S; ++r) stage(st + r, r, true);
+  }
+  for (; st < stages; ++st) stage(st, st % S, false);
+
+  // The KG partial sums meet in LDS, and are added in order.
+  float* sums = reinterpret_cast<float*>(lds);
+  wait_loads_and_sync<0>();
+  // Lane l holds channels 4 (l / 16) .. + 3 of token l % 16 of a fragment.
+  float* at = sums + (kg * TM + wm * P::WTM + lane % 16) * P::kPitch + wn * P::WTN + lane / 16 * 4;
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) *reinterpret_cast<f32x4*>(at + i * 16 * P::kPitch + j * 16) = acc[i][j];
+  __syncthreads();
+  constexpr uint32_t pieces = kOut / kPiece;
+  static_assert(TM * pieces % 64 == 0, "whole waves");
+  for (uint32_t t = threadIdx.x; t < TM * pieces; t += P::kThreads) {
+    const uint32_t i = t / pieces, jj = t % pieces * kPiece;
+    const float* row = sums + i * P::kPitch + (kGated ? jj / 16 * 32 + jj % 16 : jj);
+    float v[kPiece], ups[kPiece];
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      v[e] = row[e];
+      if constexpr (kGated) ups[e] = row[16 + e];
+#pragma unroll
+      for (int g = 1; g < KG; ++g) {
+        v[e] += row[g * TM * P::kPitch + e];
+        if constexpr (kGated) ups[e] += row[g * TM * P::kPitch + 16 + e];
+      }
+    }
+    finish_outputs<FORM>(a, i0 + i, j0 + jj, i0 + i < a.m && j0 + jj < a.n, v, ups);
+  }
+#endif
+}
+
 // A kernel and its grid for a call.
 struct Choice {
   MatmulKernel id;
@@ -573,9 +1019,51 @@ Choice general_tiles(const MatmulFp8Launch& l) {
           tiles_of(l, kTileM, kTileN), 256};
 }
 
+template <XFormat AF, XFormat BF, int M8, int GW, int KW, int RB, int FORM>
+Choice few(const MatmulFp8Launch& l) {
+  using P = Few<M8, GW, KW, RB, FORM>;
+  return {{kMatmulFewTokens, 8 * M8, P::kRows}, few_tokens_kernel<AF, BF, M8, GW, KW, RB, FORM>,
+          tiles_of(l, 8 * M8, P::kOut), 64 * P::kWaves};
+}
+
+// Groups of 128 outputs (256 rows of b, gated; 64 rows for E8M0 scales) are more than
+// a work-group should read for few tokens: a CU takes 40 GB/s. Their values go
+// through the workspace, and a second kernel makes the codes (16 tokens, gated,
+// 2 x 3584 x 8192: 44 us in one kernel, 15 in two; with E8M0 scales 23).
+bool by_workspace(const MatmulFp8Launch& l) {
+  return l.quantize && fp8_workspace(l.m, l.n, l.gated, l.scale_layout) != 0;
+}
+
+// Sixteen rows of b a wave: more work-groups, two of them a CU, keep more lines under
+// way than 32 rows do (one token, us with 16 and 32: 8192 x 8192 14.2 and 17.9,
+// 28672 x 8192 38.1 and 52.6; 16 tokens, 8192 x 8192 16.1 and 18.4), but for more
+// than 16 tokens, whose own lines would be two of three (21.0 and 20.0).
+template <XFormat AF, XFormat BF, int M8, int FORM>
+Choice few_sized(const MatmulFp8Launch& l) {
+  constexpr int RB = M8 == 4 ? 32 : 16;
+  if constexpr (FORM == kPlain) {
+    // E8M0 scales need 32 outputs in a work-group.
+    if (l.quantize && !by_workspace(l)) return few<AF, BF, M8, 32 / RB, RB / 4, RB, FORM>(l);
+  }
+  return few<AF, BF, M8, 1, M8 == 2 ? 4 : 8, RB, FORM>(l);
+}
+
+template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM>
+Choice mid(const MatmulFp8Launch& l) {
+  return {{kMatmulMid, TM, TN}, mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM>,
+          tiles_of(l, TM, FORM == kGatedForm ? TN / 2 : TN), 512};
+}
+
+// Rows of operands that the busiest CU loads with tiles of TM tokens by TN
+// rows of b: what a call's time goes by.
+template <int TM, int TN, int FORM>
+uint64_t rows_a_cu(const MatmulFp8Launch& l) {
+  return (tiles_of(l, TM, FORM == kGatedForm ? TN / 2 : TN) + kCus - 1) / kCus * (TM + TN);
+}
+
 template <XFormat AF, XFormat BF, int FORM>
-Choice pipe(const MatmulFp8Launch&) {
-  return {{kMatmulPipe, Pipe::kSide, Pipe::kSide}, pipe_kernel<AF, BF, FORM>, kCus, Pipe::kThreads};
+Choice pipe(const MatmulFp8Launch& l) {
+  return {{kMatmulPipe, Pipe::kSide, Pipe::kSide}, l.quantize || l.out_format == kOutF32 ? pipe_kernel<AF, BF, FORM, true> : pipe_kernel<AF, BF, FORM, false>, kCus, Pipe::kThreads};
 }
 
 template <XFormat AF, XFormat BF, int FORM>
@@ -586,8 +1074,31 @@ Choice choose_form(const MatmulFp8Launch& l) {
   const bool near = (256 + up_rows) * l.b_stride + l.k < kFar && 256 * l.a_stride + l.k < kFar &&
                     (257 + up_blocks) * l.groups * 4 < kFar;
   if (!near) return general_tiles<AF, BF, true, FORM>(l);
-  if (l.m > 256) return pipe<AF, BF, FORM>(l);
-  return general_tiles<AF, BF, true, FORM>(l);
+  if (l.m <= kMaxFewTokens) {
+    const Choice c = l.m <= 8    ? few_sized<AF, BF, 1, FORM>(l)
+                     : l.m <= 16 ? few_sized<AF, BF, 2, FORM>(l)
+                                 : few_sized<AF, BF, 4, FORM>(l);
+    return c.fits() ? c : general_tiles<AF, BF, true, FORM>(l);
+  }
+  // The tile whose busiest CU loads least.
+  uint64_t least = ~uint64_t{0};
+  Choice best = general_tiles<AF, BF, true, FORM>(l);
+  auto offer = [&](uint64_t rows, const Choice& c) {
+    if (rows < least && c.fits()) {
+      least = rows;
+      best = c;
+    }
+  };
+  offer(rows_a_cu<256, 256, FORM>(l) * 5 / 4, pipe<AF, BF, FORM>(l));
+  const bool group = l.quantize && l.scale_layout == kScaleF32Group128;  // 128 channels a tile
+  if (FORM != kGatedForm || !group) {
+    offer(rows_a_cu<128, 128, FORM>(l), mid<AF, BF, 128, 128, 1, 2, 4, FORM>(l));
+    offer(rows_a_cu<64, 128, FORM>(l), mid<AF, BF, 64, 128, 2, 1, 3, FORM>(l));
+    if (!group) offer(rows_a_cu<64, 64, FORM>(l), mid<AF, BF, 64, 64, 2, 2, 4, FORM>(l));
+  } else {
+    offer(rows_a_cu<64, 256, FORM>(l), mid<AF, BF, 64, 256, 1, 2, 3, FORM>(l));
+  }
+  return best;
 }
 
 template <XFormat AF, XFormat BF>
@@ -596,11 +1107,30 @@ Choice choose(const MatmulFp8Launch& l) {
   return l.gated ? choose_form<AF, BF, kGatedForm>(l) : choose_form<AF, BF, kPlain>(l);
 }
 
+// Codes of values in binary32 [m, n].
+__global__ __launch_bounds__(256) void codes_kernel(const MatmulFp8Launch a) {
+  const uint32_t pieces = a.n / kPiece;  // a multiple of a group's 16
+  const uint32_t t = blockIdx.x * 256 + threadIdx.x, i = t / pieces, j = t % pieces * kPiece;
+  float v[kPiece];
+  load_piece<kOutF32, true, kPiece>(a.workspace + static_cast<uint64_t>(min(i, a.m - 1)) * a.n, j, a.n, v);
+  finish_codes(a, i, j, i < a.m, false, v);
+}
+
 template <XFormat AF, XFormat BF>
 hipError_t launch_formats(const MatmulFp8Launch& l, hipStream_t stream) {
   const Choice c = choose<AF, BF>(l);
   if (!c.fits()) return hipErrorInvalidValue;
-  return launch_kernel(c.kernel, dim3(static_cast<uint32_t>(c.blocks)), dim3(c.threads), stream, l);
+  const dim3 grid(static_cast<uint32_t>(c.blocks)), block(c.threads);
+  if (!(c.id.family == kMatmulFewTokens && by_workspace(l))) return launch_kernel(c.kernel, grid, block, stream, l);
+  MatmulFp8Launch values = l;
+  values.quantize = false;
+  values.out_format = kOutF32;
+  values.out_vec = true;
+  values.out = l.workspace;
+  values.out_stride = l.n;
+  const hipError_t e = launch_kernel(c.kernel, grid, block, stream, values);
+  if (e != hipSuccess) return e;
+  return launch_kernel(codes_kernel, dim3((l.m * (l.n / kPiece) + 255) / 256), dim3(256), stream, l);
 }
 
 }  // namespace

@@ -37,7 +37,7 @@ BLOCKS = dict(rows=300, cols=200, kind=BF16, xd=E4M3, x=_at(0), ldx=200, c=_at(1
 MM = dict(m=4, n=256, k=512, gated=0, kind=BF16, ad=E4M3, a=_at(0), lda=512, sa=_at(1), bd=E4M3, bs=128, b=_at(2),
           ldb=512, sb=_at(3), o=_at(4), ldo=256)
 MMQ = dict(m=4, n=256, k=512, gated=0, xd=E4M3, sl=MX, ad=E4M3, a=_at(0), lda=512, sa=_at(1), bd=E5M2, b=_at(2),
-           ldb=512, sb=_at(3), c=_at(4), ldc=256, sc=_at(6))
+           ldb=512, sb=_at(3), c=_at(4), ldc=256, sc=_at(6), ws=_at(7), wsb=1 << 20)
 
 
 def _norm(lib, **kw):
@@ -76,7 +76,7 @@ def _mmq(lib, **kw):
     d = {**MMQ, **kw}
     return lib.qrs_matmul_float_quantize(d["m"], d["n"], d["k"], d["gated"], d["xd"], d["sl"], d["ad"], d["a"],
                                          d["lda"], d["sa"], d["bd"], d["b"], d["ldb"], d["sb"], d["c"], d["ldc"],
-                                         d["sc"], None)
+                                         d["sc"], d["ws"], d["wsb"], None)
 
 
 NORM_BAD = [
@@ -124,6 +124,9 @@ MMQ_BAD = [
     (dict(c=_at(4) + 8), "16-byte"), (dict(ldc=264), "16-byte"), (dict(sc=None), "scales"), (dict(c=None), "codes"),
     (dict(sc=_at(4) + 1), "overlaps"), (dict(sc=_at(2)), "overlaps"), (dict(sl=GROUP, sc=_at(6) + 1), "aligned"),
     (dict(m=0), "must be positive"), (dict(k=-3), "k -3"), (dict(ad=INT8), "a_dtype"), (dict(bd=INT8), "b_dtype"),
+    (dict(sl=GROUP, ws=None), "workspace"), (dict(sl=GROUP, wsb=4 * 256 * 4 - 1), "workspace"),
+    (dict(sl=GROUP, ws=_at(7) + 4), "16-byte"), (dict(sl=GROUP, ws=_at(4)), "overlaps"),
+    (dict(sl=GROUP, ws=_at(2)), "overlaps b"), (dict(sl=GROUP, ws=_at(6)), "overlaps scales"),
 ]
 
 
@@ -155,6 +158,17 @@ def test_workspace_query(lib):
     assert 0 < n.value <= 1 << 24  # bounded whatever the number of tokens
     assert lib.qrs_layer_norm_backward_workspace(0, 1024, ctypes.byref(n)) == INVALID and n.value == 0
     assert lib.qrs_layer_norm_backward_workspace(4, 1024, None) == INVALID
+
+
+def test_product_workspace_query(lib):
+    n = ctypes.c_size_t(7)
+    ask = lib.qrs_matmul_float_quantize_workspace
+    for gated in (0, 1):
+        assert ask(32, 256, gated, GROUP, ctypes.byref(n)) == 0 and n.value == 32 * 256 * 4
+        assert ask(33, 256, gated, GROUP, ctypes.byref(n)) == 0 and n.value == 0
+        assert ask(32, 256, gated, MX, ctypes.byref(n)) == 0 and n.value == 32 * 256 * 4 * gated
+    assert ask(32, 200, 0, GROUP, ctypes.byref(n)) == INVALID and ask(32, 256, 2, GROUP, ctypes.byref(n)) == INVALID
+    assert ask(32, 256, 0, ROW, ctypes.byref(n)) == INVALID and ask(32, 256, 0, GROUP, None) == INVALID
 
 
 def test_launch_info_refusals(lib):
