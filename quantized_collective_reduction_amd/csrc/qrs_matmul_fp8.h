@@ -72,23 +72,18 @@ __device__ __forceinline__ f32x4 sums8(const i32x8& b, const i32x8& a) {
                                                           AF == kXE5M2 ? 1 : 0, 0, 0, 0, 0);
 }
 
+// Two of four codes, the high or the low ones, as bfloat16.
+template <XFormat F, bool HIGH>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  if constexpr (F == kXE4M3FN)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HIGH));
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, HIGH));
+}
+
 // Eight codes as bfloat16.
 template <XFormat F>
 __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
-  bf16x2 p[4];
-  if constexpr (F == kXE4M3FN) {
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  } else {
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
-  }
-  const u32x4 w = {__builtin_bit_cast(uint32_t, p[0]), __builtin_bit_cast(uint32_t, p[1]),
-                   __builtin_bit_cast(uint32_t, p[2]), __builtin_bit_cast(uint32_t, p[3])};
+  const u32x4 w = {widen2<F, false>(lo), widen2<F, true>(lo), widen2<F, false>(hi), widen2<F, true>(hi)};
   return __builtin_bit_cast(bf16x8, w);
 }
 
@@ -407,89 +402,92 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
   const uint32_t lane_off[2] = {lane % 16 * kGroup + ((lane / 16) ^ (lane % 16 / 2)) * 16u,
                                 lane % 16 * kGroup + ((4 + lane / 16) ^ (lane % 16 / 2)) * 16u};
   f32x4 acc[FM][FN];
-  auto compute8 = [&](uint32_t slot) {
-    const char* base = lds + slot * P::kBlock;
-    const char* la = base + wm * P::kWaveM * kGroup;
-    const char* lb = base + P::kSide * kGroup + wn * P::kWaveN * kGroup;
+  // A block's scales: of this lane's tokens times those of b's rows (grouped: kept apart).
+  struct Scales {
+    float token[FM], product[FORM == kGatedForm ? 2 : 1][FM];
+  };
+  auto read_scales = [&](const char* base, Scales& s) {
     const float* sa = reinterpret_cast<const float*>(base + P::kOperands) + wm * P::kWaveM + lane % 16;
     const float* sb = reinterpret_cast<const float*>(base + P::kOperands) + P::kSide + wn * P::kWaveN;
-    float token[FM], scale[FORM == kGatedForm ? 2 : 1][FM];
-    auto fragment = [&](const char* p) {
-      return __builtin_shufflevector(*reinterpret_cast<const i32x4*>(p + lane_off[0]),
-                                     *reinterpret_cast<const i32x4*>(p + lane_off[1]), 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-    i32x8 fa[FM];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      token[i] = sa[16 * i];
-      fa[i] = fragment(la + i * 16 * kGroup);
-    }
+    for (int i = 0; i < FM; ++i) s.token[i] = sa[16 * i];
     if constexpr (FORM != kGrouped) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        scale[0][i] = token[i] * sb[0];
-        if constexpr (FORM == kGatedForm) scale[1][i] = token[i] * sb[32];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const i32x8 fb = fragment(lb + j * 16 * kGroup);
-      f32x4 sums[FM];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sums[i] = sums8<AF, BF>(fb, fa[i]);
-      if constexpr (FORM == kGrouped) {
-        const f32x4 channels = *reinterpret_cast<const f32x4*>(sb + 16 * j + lane / 16 * 4);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) add_scaled(acc[i][j], sums[i], token[i], channels);
-      } else {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) add_scaled(acc[i][j], sums[i], scale[FORM == kGatedForm ? j / 2 % 2 : 0][i]);
+        s.product[0][i] = s.token[i] * sb[0];
+        if constexpr (FORM == kGatedForm) s.product[1][i] = s.token[i] * sb[32];
       }
     }
   };
+  // Adds a fragment's sums; x = FM j + i.
+  auto add = [&](const Scales& s, const f32x4& channels, const f32x4& sums, int x) {
+    const int i = x % FM, j = x / FM;
+    if constexpr (FORM == kGrouped)
+      add_scaled(acc[i][j], sums, s.token[i], channels);
+    else
+      add_scaled(acc[i][j], sums, s.product[FORM == kGatedForm ? j / 2 % 2 : 0][i]);
+  };
+  auto read_channels = [&](const char* base, int j) {
+    if constexpr (FORM != kGrouped) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const float* sb = reinterpret_cast<const float*>(base + P::kOperands) + P::kSide + wn * P::kWaveN;
+    return *reinterpret_cast<const f32x4*>(sb + 16 * j + lane / 16 * 4);
+  };
+
   auto compute = [&](uint32_t slot) {
     const char* base = lds + slot * P::kBlock;
     const char* la = base + wm * P::kWaveM * kGroup;
     const char* lb = base + P::kSide * kGroup + wn * P::kWaveN * kGroup;
-    const float* sa = reinterpret_cast<const float*>(base + P::kOperands) + wm * P::kWaveM + lane % 16;
-    const float* sb = reinterpret_cast<const float*>(base + P::kOperands) + P::kSide + wn * P::kWaveN;
-    float token[FM], scale[FORM == kGatedForm ? 2 : 1][FM];
-    Wide<2> fa[FM];
+    Scales scales;
+    read_scales(base, scales);
+    auto read = [&](const char* rows, int f, int n) {
+      return *reinterpret_cast<const i32x4*>(rows + lane_off[n] + f * 16 * kGroup);
+    };
+    if constexpr (WIDE) {
+      Wide<2> fa[FM];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      token[i] = sa[16 * i];
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-        fa[i].template set<AF>(n, *reinterpret_cast<const i32x4*>(la + lane_off[n] + i * 16 * kGroup));
-    }
-    if constexpr (FORM != kGrouped) {
+        for (int n = 0; n < 2; ++n) fa[i].template set<AF>(n, read(la, i, n));
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        scale[0][i] = token[i] * sb[0];
-        if constexpr (FORM == kGatedForm) scale[1][i] = token[i] * sb[32];
+      for (int j = 0; j < FN; ++j) {
+        Wide<2> fb;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) fb.template set<BF>(n, read(lb, j, n));
+        f32x4 sums[FM];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sums[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+            sums[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb.part[t], fa[i].part[t], sums[i], 0, 0, 0);
+        const f32x4 channels = read_channels(base, j);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) add(scales, channels, sums[i], FM * j + i);
       }
-    }
+    } else {
+      constexpr int kBehind = 4, kRing = kBehind + 1;
+      f32x4 sums[kRing], channels[2];
+      auto fragment = [&](const char* rows, int f) {
+        return __builtin_shufflevector(read(rows, f, 0), read(rows, f, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+      };
+      i32x8 fa[FM], fb[2];
+      fb[0] = fragment(lb, 0);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      Wide<2> fb;
+      for (int i = 0; i < FM; ++i) fa[i] = fragment(la, i);
+      channels[0] = read_channels(base, 0);
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-        fb.template set<BF>(n, *reinterpret_cast<const i32x4*>(lb + lane_off[n] + j * 16 * kGroup));
-      f32x4 sums[FM];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) sums[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-          sums[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb.part[t], fa[i].part[t], sums[i], 0, 0, 0);
-      if constexpr (FORM == kGrouped) {
-        const f32x4 channels = *reinterpret_cast<const f32x4*>(sb + 16 * j + lane / 16 * 4);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) add_scaled(acc[i][j], sums[i], token[i], channels);
-      } else {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) add_scaled(acc[i][j], sums[i], scale[FORM == kGatedForm ? j / 2 % 2 : 0][i]);
+      for (int x = 0; x < FM * FN + kBehind; ++x) {
+        const int i = x % FM, j = x / FM;
+        if (x < FM * FN) {
+          sums[x % kRing] = sums8<AF, BF>(fb[j % 2], fa[i]);
+          if (i == 0 && j + 1 < FN) {
+            fb[(j + 1) % 2] = fragment(lb, j + 1);
+            channels[(j + 1) % 2] = read_channels(base, j + 1);
+          }
+        }
+        if (x >= kBehind) add(scales, channels[(x - kBehind) / FM % 2], sums[(x - kBehind) % kRing], x - kBehind);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -513,10 +511,7 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
       else
         wait_loads_and_sync<0>();
       if (advance()) load();
-      if constexpr (WIDE)
-        compute(slot);
-      else
-        compute8(slot);
+      compute(slot);
       slot ^= 1;
     }
 
@@ -813,7 +808,7 @@ struct Mid {
   static_assert(kRows * KG <= 512 && kLds <= 163840, "one scale a lane");
 };
 
-template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM>
+template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM, bool WIDE>
 __global__ __launch_bounds__(512, 2) void mid_kernel(const MatmulFp8Launch a) {
 #ifdef __HIP_DEVICE_COMPILE__
   using P = Mid<TM, TN, KG, WM, S>;
@@ -916,48 +911,105 @@ __global__ __launch_bounds__(512, 2) void mid_kernel(const MatmulFp8Launch a) {
     for (int e = 0; e < kScalesB; ++e)
       f.channel[j][e] = *reinterpret_cast<const float*>(scales_b + slot * P::kStage + 64 * j + 4 * e);
   };
+  // Fragment x = KF u + q joins the q-th kept and the u-th streamed fragment: of
+  // the operand with fewer of them all are kept widened, of the other one at a time.
+  constexpr bool kKeepA = FM < FN;
+  constexpr int KF = kKeepA ? FM : FN, SF = kKeepA ? FN : FM;
+  auto add = [&](const Fragments& f, const f32x4& sums, int x) {
+    const int i = kKeepA ? x % KF : x / KF, j = kKeepA ? x / KF : x % KF;
+    if constexpr (FORM == kGrouped)
+      add_scaled(acc[i][j], sums, f.token[i], f32x4{f.channel[j][0], f.channel[j][1], f.channel[j][2], f.channel[j][3]});
+    else
+      add_scaled(acc[i][j], sums, f.token[i] * f.channel[j][0]);
+  };
+  // Two codes' widening of a streamed or kept fragment: `word` of its 16.
+  auto widen_word = [&](Wide<2>& to, const Fragments& f, bool kept, int index, int word) {
+    const bool of_a = kept == kKeepA;
+    const uint32_t codes = static_cast<uint32_t>(of_a ? f.a[index][word / 8][word / 2 % 4] : f.b[index][word / 8][word / 2 % 4]);
+    u32x4 w = __builtin_bit_cast(u32x4, to.part[word / 4]);
+    if (of_a)
+      w[word % 4] = word % 2 ? widen2<AF, true>(codes) : widen2<AF, false>(codes);
+    else
+      w[word % 4] = word % 2 ? widen2<BF, true>(codes) : widen2<BF, false>(codes);
+    to.part[word / 4] = __builtin_bit_cast(bf16x8, w);
+  };
+  Wide<2> kept[KF], streamed[2];
+  auto widen_kept = [&](const Fragments& f, int q) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) widen_word(kept[q], f, true, q, w);
+  };
+  auto widen_first = [&](const Fragments& f) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) widen_word(streamed[0], f, false, 0, w);
+  };
   // Multiplies stage st (in registers, its LDS `slot`) while stage st + 1 is
-  // read and stage st + S loaded into st's place in LDS.
+  // read and stage st + S loaded into st's place in LDS. Every matrix
+  // instruction has others behind it: the widening of the next streamed fragment,
+  // the scaled addition of the sums before, reads and loads.
   auto stage = [&](uint32_t st, uint32_t slot, bool full) {
     wait_loads_and_sync<P::kLoads*(S - 2)>();
     const uint32_t after = slot + 1 == S ? 0 : slot + 1;
-    Wide<2> wb[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) wb[j].template set<BF>(n, now.b[j][n]);
-      read_b(next, after, j);
-    }
     const bool live = full || st * KG + kg < a.groups;  // scales past the last group may be anything
+    constexpr int kSteps = WIDE ? 4 * FM * FN : FM * FN, kReads = FM + FN;
+    constexpr int kBehind = WIDE ? 1 : 2, kRing = kBehind + 1;
+    f32x4 sums[kRing];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      Wide<2> wa;
+    for (int y = 0; y < kSteps; ++y) {
+      if constexpr (WIDE) {
+        const int x = y / 4, t = y % 4, q = x % KF, u = x / KF;
+        f32x4& to = sums[x % kRing];
+        if (t == 0) to = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const bf16x8 k = kept[q].part[t], v = streamed[u % 2].part[t];
+        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kKeepA ? v : k, kKeepA ? k : v, to, 0, 0, 0);
+        constexpr int kWords = 4 / KF;  // for each step
+        if (u + 1 < SF) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n) wa.template set<AF>(n, now.a[i][n]);
-      read_a(next, after, i);
-#pragma unroll
-      for (int t = i * P::kLoads / FM; t < (i + 1) * P::kLoads / FM; ++t) load(st + S, slot, t, full);
-      if (live) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          f32x4 sums = {0.0f, 0.0f, 0.0f, 0.0f};
-          add_products(sums, wb[j], wa);
-          if constexpr (FORM == kGrouped)
-            add_scaled(acc[i][j], sums, now.token[i],
-                       f32x4{now.channel[j][0], now.channel[j][1], now.channel[j][2], now.channel[j][3]});
-          else
-            add_scaled(acc[i][j], sums, now.token[i] * now.channel[j][0]);
+          for (int w = 0; w < kWords; ++w)
+            widen_word(streamed[(u + 1) % 2], now, false, u + 1, (y % (4 * KF)) * kWords + w);
         }
+        if (x > 0 && live) {  // a quarter of the fragment before
+          const f32x4& from = sums[(x - 1) % kRing];
+          const int i = kKeepA ? (x - 1) % KF : (x - 1) / KF, j = kKeepA ? (x - 1) / KF : (x - 1) % KF;
+          const float scale = FORM == kGrouped ? now.token[i] * now.channel[j][t % kScalesB] : now.token[i] * now.channel[j][0];
+          acc[i][j][t] = __builtin_fmaf(from[t], scale, acc[i][j][t]);
+        }
+      } else {
+        auto whole = [](const i32x4 (&f)[2]) { return __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7); };
+        const int i = kKeepA ? y % KF : y / KF, j = kKeepA ? y / KF : y % KF;
+        sums[y % kRing] = sums8<AF, BF>(whole(now.b[j]), whole(now.a[i]));
+        if (y >= kBehind && live) add(now, sums[(y - kBehind) % kRing], y - kBehind);
       }
+#pragma unroll
+      for (int r = y * kReads / kSteps; r < (y + 1) * kReads / kSteps; ++r) {
+        if (r < FN)
+          read_b(next, after, r);
+        else
+          read_a(next, after, r - FN);
+      }
+#pragma unroll
+      for (int t = y * P::kLoads / kSteps; t < (y + 1) * P::kLoads / kSteps; ++t) load(st + S, slot, t, full);
       __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int x = FM * FN - kBehind; x < FM * FN; ++x)
+      if (live) add(now, sums[x % kRing], x);
     now = next;
+    if constexpr (WIDE) {
+      widen_first(now);
+#pragma unroll
+      for (int q = 0; q < KF; ++q) widen_kept(now, q);
+    }
   };
   wait_loads_and_sync<P::kLoads*(S - 1)>();
 #pragma unroll
   for (int j = 0; j < FN; ++j) read_b(now, 0, j);
 #pragma unroll
   for (int i = 0; i < FM; ++i) read_a(now, 0, i);
+  if constexpr (WIDE) {
+    widen_first(now);
+#pragma unroll
+    for (int q = 0; q < KF; ++q) widen_kept(now, q);
+  }
   uint32_t st = 0;
   // Rounds with fixed slots and nothing to check, while all that they load is
   // inside k; then a stage at a time.
@@ -1048,9 +1100,13 @@ Choice few_sized(const MatmulFp8Launch& l) {
   return few<AF, BF, M8, 1, M8 == 2 ? 4 : 8, RB, FORM>(l);
 }
 
+// Whether codes are widened: for outputs of binary32, and codes, whose scales are.
+bool wide(const MatmulFp8Launch& l) { return l.quantize || l.out_format == kOutF32; }
+
 template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM>
 Choice mid(const MatmulFp8Launch& l) {
-  return {{kMatmulMid, TM, TN}, mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM>,
+  return {{kMatmulMid, TM, TN},
+          wide(l) ? mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, true> : mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, false>,
           tiles_of(l, TM, FORM == kGatedForm ? TN / 2 : TN), 512};
 }
 
@@ -1063,7 +1119,8 @@ uint64_t rows_a_cu(const MatmulFp8Launch& l) {
 
 template <XFormat AF, XFormat BF, int FORM>
 Choice pipe(const MatmulFp8Launch& l) {
-  return {{kMatmulPipe, Pipe::kSide, Pipe::kSide}, l.quantize || l.out_format == kOutF32 ? pipe_kernel<AF, BF, FORM, true> : pipe_kernel<AF, BF, FORM, false>, kCus, Pipe::kThreads};
+  return {{kMatmulPipe, Pipe::kSide, Pipe::kSide},
+          wide(l) ? pipe_kernel<AF, BF, FORM, true> : pipe_kernel<AF, BF, FORM, false>, kCus, Pipe::kThreads};
 }
 
 template <XFormat AF, XFormat BF, int FORM>
