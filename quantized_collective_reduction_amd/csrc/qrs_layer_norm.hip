@@ -60,6 +60,14 @@ __device__ __forceinline__ WaveMoments wave_moments(float s0, double d1, double 
   return {s0 + dm, d2 - d1 * dm};
 }
 
+// Sum over each row of 16 lanes, in a fixed order, in every lane of it.
+__device__ __forceinline__ double sum16(double v) {
+  v += lanes(v, [](uint32_t x) { return dpp<kDppSwap1>(x); });
+  v += lanes(v, [](uint32_t x) { return dpp<kDppSwap2>(x); });
+  v += lanes(v, [](uint32_t x) { return dpp<kDppHalfMirror>(x); });
+  return v + lanes(v, [](uint32_t x) { return dpp<kDppMirror>(x); });
+}
+
 // A row's mean, as a float and what that leaves, and 1 / sqrt(var + eps).
 struct Moments {
   double mean, r, m;  // m = var + eps
@@ -89,8 +97,8 @@ struct Format {
   static constexpr int value = XF;
 };
 
-// Codes of a piece of y, whose group of G elements lies in the G / E lanes
-// around it (or in the row, with the multiplier given).
+// Codes of a piece of y, whose group of elements lies in the lanes around it (or
+// in the row, with the multiplier given).
 template <int SL, int XF, int E>
 __device__ __forceinline__ Codes<E> encode_y(const float* y, float mul, uint32_t* scale_bits) {
   if constexpr (SL == kScaleE8M0Block32) {
@@ -106,9 +114,9 @@ __device__ __forceinline__ Codes<E> encode_y(const float* y, float mul, uint32_t
 // Work-group b takes rows b, b + gridDim, ...; the next row's operands are
 // under way while a row is reduced and written.
 //
-// y takes four roundings of its product (s - mean: two, r, (s - mean) * r) and
-// one of the sum with the bias: |error| <= 2^-24 (4.1 |y - bias| + |y|). Rows
-// whose variance or mean leaves the range above are taken in binary64.
+// y is computed in binary64 and rounded once to binary32, so that its codes are
+// those of the formula but where binary64 itself could not tell: the operations
+// fit beside the stream.
 template <int IO, int SL, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
@@ -172,8 +180,8 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a)
       const uint32_t c = (p * NT + lane) * E;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const bool in = VEC ? c < a.h : c + j < a.h;
-        const double d = in ? static_cast<double>(s[p][j]) - s0 : 0.0;
+        if (!(VEC ? c < a.h : c + j < a.h)) continue;
+        const double d = static_cast<double>(s[p][j]) - s0;
         d1 += d;
         d2 = __builtin_fma(d, d, d2);
       }
@@ -184,37 +192,35 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a)
       part[turn][lane / 64][1] = wm.squares;
     }
     lds_barrier();
-    double mean = 0.0, squares = 0.0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) mean += count[i] * part[turn][i][0];
-    mean *= a.inv_h;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      const double d = part[turn][i][0] - mean;
-      squares += __builtin_fma(count[i] * d, d, part[turn][i][1]);
-    }
-    Moments mo;
-    mo.finish(mean, squares, a.inv_h, a.eps);
-    const bool wide = mo.wide();  // the same in every lane
+    // Lane l joins wave l % 16's part.
+    const int i = lane % 16;
+    const double n = i < kWaves ? count[i] : 0.0, wave_mean = i < kWaves ? part[turn][i][0] : 0.0;
+    const double mean = sum16(n * wave_mean) * a.inv_h;
+    const double off = wave_mean - mean;
+    const double squares = sum16(__builtin_fma(n * off, off, i < kWaves ? part[turn][i][1] : 0.0));
+    const double r = inverse_root(squares * a.inv_h + static_cast<double>(a.eps));
 
     // y over s.
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t c = (p * NT + lane) * E;
       float wv[E], bv[E];
+      if (VEC && c >= a.h) continue;  // zeros, like the weight and the bias
+      if (IO != kOutF32) {
+        // Unpacked and converted again: kept, they would cost the registers of more
+        // waves (bf16 16384 x 8192 179 us, renewed 170; fp32 8192 x 5120 92 and 106).
+        as_new(s[p]);
+        w[p].renew();
+        b[p].renew();
+      }
       w[p].get(wv);
       b[p].get(bv);
-      if (__builtin_expect(wide, false)) {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-          s[p][j] = static_cast<float>((static_cast<double>(s[p][j]) - mo.mean) * mo.r * wv[j] + bv[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j) s[p][j] = __builtin_fmaf(mo.centred(s[p][j]) * mo.r32, wv[j], bv[j]);
+      for (int j = 0; j < E; ++j) {
+        const double u = (static_cast<double>(s[p][j]) - mean) * r;
+        const float y = static_cast<float>(__builtin_fma(u, static_cast<double>(wv[j]), static_cast<double>(bv[j])));
+        s[p][j] = VEC || c + j < a.h ? y : 0.0f;
       }
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (!(VEC ? c < a.h : c + j < a.h)) s[p][j] = 0.0f;
     }
     uint32_t amax = 0;
     if constexpr (SL == kScaleF32Row) {
@@ -238,7 +244,7 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a)
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const uint32_t c = (p * NT + lane) * E;
-        uint32_t scale;
+        uint32_t scale = 0;
         store_codes<VEC, E>(codes_row, c, a.h, encode_y<SL, XF, E>(s[p], mul, &scale));
         if (SL == kScaleE8M0Block32 && c < a.h && c % 32 == 0)
           static_cast<uint8_t*>(a.scales)[row * (a.h / 32) + c / 32] = static_cast<uint8_t>(scale);
@@ -257,23 +263,32 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a)
 }
 
 template <int IO, int SL, int NT, int P, bool VEC, bool STREAM>
-hipError_t launch_norm_as(const LayerNormLaunch& l, hipStream_t stream) {
-  const uint32_t blocks = NT * P <= 512 ? 4096 : NT < 1024 ? 512 : 256;
+hipError_t launch_norm_as(const LayerNormLaunch& l, uint32_t blocks, hipStream_t stream) {
   return launch_kernel(layer_norm_kernel<IO, SL, NT, P, VEC, STREAM>,
                        dim3(static_cast<uint32_t>(l.rows < blocks ? l.rows : blocks)), dim3(NT), stream, l);
 }
 
-// The smallest shape that holds a row; rows off 16-byte boundaries have two.
+// The smallest shape that holds a row, 16 elements a lane where registers allow:
+// few waves a row, which each pay for the reductions. Work-groups that even out by
+// themselves, but for binary32 in 768 lanes as many as run at once. us: bf16
+// 16384 x 1024 128 x 1 28, 256 x 2 58; 8192 x 4096 256 x 2 45, 512 x 1 50; 16384 x 8192
+// 512 x 2 in 256, 512 and 2048 work-groups 202, 178 and 170, 256 x 4 213; 4096 x 7168
+// 52, 45 and 44; fp32 8192 x 5120 768 x 1 in 256 and 4096 92 and 110, 512 x 2 96 and 128.
+// Rows off 16-byte boundaries have two shapes. (Scratch memory takes part of rows
+// past 8192 elements.)
 template <int IO, int SL, bool VEC, bool STREAM>
 hipError_t launch_norm_sized(const LayerNormLaunch& l, hipStream_t stream) {
   if constexpr (VEC) {
-    if (l.h <= 256 * 1 * kPiece) return launch_norm_as<IO, SL, 256, 1, VEC, STREAM>(l, stream);
-    if (l.h <= 512 * 1 * kPiece) return launch_norm_as<IO, SL, 512, 1, VEC, STREAM>(l, stream);
+    if (l.h <= 128 * 1 * kPiece) return launch_norm_as<IO, SL, 128, 1, VEC, STREAM>(l, 2048, stream);
+    if (l.h <= 128 * 2 * kPiece) return launch_norm_as<IO, SL, 128, 2, VEC, STREAM>(l, 2048, stream);
+    if (l.h <= 256 * 2 * kPiece) return launch_norm_as<IO, SL, 256, 2, VEC, STREAM>(l, 2048, stream);
+    if (IO == kOutF32 && l.h <= 768 * 1 * kPiece) return launch_norm_as<IO, SL, 768, 1, VEC, STREAM>(l, 256, stream);
   }
-  if (l.h <= 512 * 2 * kPiece) return launch_norm_as<IO, SL, 512, 2, VEC, STREAM>(l, stream);
+  if (l.h <= 512 * 2 * kPiece)
+    return launch_norm_as<IO, SL, 512, 2, VEC, STREAM>(l, IO == kOutF32 ? 256 : 2048, stream);
   if constexpr (VEC)
-    if (l.h <= 1024 * 2 * kPiece) return launch_norm_as<IO, SL, 1024, 2, VEC, STREAM>(l, stream);
-  if (l.h <= 1024 * 8 * kPiece) return launch_norm_as<IO, SL, 1024, 8, VEC, STREAM>(l, stream);
+    if (l.h <= 1024 * 2 * kPiece) return launch_norm_as<IO, SL, 1024, 2, VEC, STREAM>(l, 256, stream);
+  if (l.h <= 1024 * 8 * kPiece) return launch_norm_as<IO, SL, 1024, 8, VEC, STREAM>(l, 256, stream);
   return hipErrorInvalidValue;
 }
 
@@ -352,7 +367,7 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
   int turn = 0;  // halves of `part`, as in the forward pass
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     if (!kAhead) load_row(row);
-    const Operands now = next;
+    Operands now = next;
     if (kAhead && row + gridDim.x < a.rows) load_row(row + gridDim.x);
     float first[E];
     now.s[0].get(first);
@@ -367,9 +382,9 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
       now.s[p].get(s);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const bool in = VEC ? c < a.h : c + j < a.h;
-        const double d = in ? static_cast<double>(s[j]) - s0 : 0.0;
-        const double g = wv[j] * dy[j];  // zero past the row's end
+        if (!(VEC ? c < a.h : c + j < a.h)) continue;
+        const double d = static_cast<double>(s[j]) - s0;
+        const double g = wv[j] * dy[j];
         d1 += d;
         d2 = __builtin_fma(d, d, d2);
         g1 += g;
@@ -388,20 +403,29 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
       to[3] = gd - g1 * (d1 * inv_mine);
     }
     lds_barrier();
-    double mean = 0.0, squares = 0.0, sum_d = 0.0, sum_du = 0.0;
+    const int i = lane % 16;
+    double n = 0.0, all[4] = {0.0, 0.0, 0.0, 0.0};  // of wave i
+    if (i < kWaves) {
+      n = count[i];
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) mean += count[i] * part[turn][i][0];
-    mean *= a.inv_h;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      const double d = part[turn][i][0] - mean;
-      squares += __builtin_fma(count[i] * d, d, part[turn][i][1]);
-      sum_d += part[turn][i][2];
-      sum_du += __builtin_fma(part[turn][i][2], d, part[turn][i][3]);
+      for (int e = 0; e < 4; ++e) all[e] = part[turn][i][e];
     }
+    const double mean = sum16(n * all[0]) * a.inv_h, off = all[0] - mean;
+    const double squares = sum16(__builtin_fma(n * off, off, all[1])), sum_d = sum16(all[2]);
+    const double sum_du = sum16(__builtin_fma(all[2], off, all[3]));
     Moments mo;
     mo.finish(mean, squares, a.inv_h, a.eps);
     const double mean_d = sum_d * a.inv_h, mean_du = sum_du * a.inv_h * mo.r;
+    if (IO != kOutF32) {
+      // Unpacked again: kept, they would cost the registers of a second work-group
+      // (bf16 16384 x 8192 208 us, renewed 190).
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        w[p].renew();
+        now.dy[p].renew();
+        now.s[p].renew();
+      }
+    }
     const bool wide = mo.wide() || !(__builtin_fabs(mean_d) < 0x1p100 && __builtin_fabs(mean_du) < 0x1p100);
     const float mean_d32 = static_cast<float>(mean_d), mean_du32 = static_cast<float>(mean_du);
 #pragma unroll
@@ -490,12 +514,16 @@ hipError_t launch_backward_as(const LayerNormBackwardLaunch& l, hipStream_t stre
                        static_cast<const float*>(l.workspace), l.grad_weight, l.grad_bias, parts, l.h);
 }
 
-// The smallest shape that holds a row, as above.
+// The smallest shape that holds a row, as above. us: bf16 16384 x 1024 128 x 1 46,
+// 256 x 1 74; 8192 x 2048 128 x 2 37, 256 x 1 42; 8192 x 4096 256 x 2 58, 512 x 1 67;
+// 16384 x 8192 256 x 4 190, 512 x 2 216; fp32 8192 x 5120 112 with 512 x 2, 134 with 256 x 4.
 template <int IO, bool VEC, bool STREAM>
 hipError_t launch_backward_sized(const LayerNormBackwardLaunch& l, hipStream_t stream) {
   if constexpr (VEC) {
-    if (l.h <= 256 * 1 * kPiece) return launch_backward_as<IO, 256, 1, VEC, STREAM>(l, stream);
+    if (l.h <= 128 * 1 * kPiece) return launch_backward_as<IO, 128, 1, VEC, STREAM>(l, stream);
+    if (l.h <= 128 * 2 * kPiece) return launch_backward_as<IO, 128, 2, VEC, STREAM>(l, stream);
     if (l.h <= 256 * 2 * kPiece) return launch_backward_as<IO, 256, 2, VEC, STREAM>(l, stream);
+    if (IO == kOutF32 && l.h <= 512 * 2 * kPiece) return launch_backward_as<IO, 512, 2, VEC, STREAM>(l, stream);
   }
   if (l.h <= 256 * 4 * kPiece) return launch_backward_as<IO, 256, 4, VEC, STREAM>(l, stream);
   if constexpr (VEC)
@@ -523,7 +551,15 @@ hipError_t launch_layer_norm(const LayerNormLaunch& l, hipStream_t stream) {
 }
 
 uint32_t layer_norm_backward_parts(uint64_t rows, uint32_t h) {
-  const uint32_t parts = h <= 256 * kPiece && rows >= 4 * 512 ? 512 : 256;
+  // One a CU, as each leaves two rows of partial sums; more where rows are narrow, if
+  // they have rows to load ahead. us with 256, 512 and 1024: bf16 16384 x 1024 92, 73 and
+  // 46; 8192 x 2048 66, 52 and 37; 8192 x 4096 71, 58 and 67; 16384 x 8192 226, 190 and 200;
+  // 1021 x 7168 24, 27 and 37; 500 x 2048 12, 13 and 13.
+  uint32_t parts = 256;
+  if (h <= 256 * kPiece && rows >= 4 * 1024)
+    parts = 1024;
+  else if (rows >= (h <= 512 * kPiece ? 4 * 512 : 16 * 512 + 1))
+    parts = 512;
   return static_cast<uint32_t>(rows < parts ? rows : parts);
 }
 

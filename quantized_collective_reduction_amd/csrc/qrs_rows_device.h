@@ -74,19 +74,22 @@ struct RawPiece<kOutF16, true> : RawPiece16<kOutF16> {};
 // pass, 1074 MB: 195 us, as a stream 174; 59 MB, found there: 20.2 and 21.6).
 constexpr uint64_t kStreamBytes = uint64_t{256} << 20;
 
+// v from the lanes that f takes its 32-bit halves from.
+template <typename F>
+__device__ __forceinline__ double lanes(double v, F f) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = f(static_cast<uint32_t>(b)), hi = f(static_cast<uint32_t>(b >> 32));
+  return __builtin_bit_cast(double, lo | hi << 32);
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
-  auto from = [](double x, auto f) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, x);
-    const uint64_t lo = f(static_cast<uint32_t>(b)), hi = f(static_cast<uint32_t>(b >> 32));
-    return __builtin_bit_cast(double, lo | hi << 32);
-  };
-  v += from(v, [](uint32_t x) { return dpp<kDppSwap1>(x); });
-  v += from(v, [](uint32_t x) { return dpp<kDppSwap2>(x); });
-  v += from(v, [](uint32_t x) { return dpp<kDppHalfMirror>(x); });
-  v += from(v, [](uint32_t x) { return dpp<kDppMirror>(x); });
+  v += lanes(v, [](uint32_t x) { return dpp<kDppSwap1>(x); });
+  v += lanes(v, [](uint32_t x) { return dpp<kDppSwap2>(x); });
+  v += lanes(v, [](uint32_t x) { return dpp<kDppHalfMirror>(x); });
+  v += lanes(v, [](uint32_t x) { return dpp<kDppMirror>(x); });
   double row[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) row[i] = from(v, [i](uint32_t x) { return lane_value(x, 16 * i); });
+  for (int i = 0; i < 4; ++i) row[i] = lanes(v, [i](uint32_t x) { return lane_value(x, 16 * i); });
   return (row[0] + row[1]) + (row[2] + row[3]);
 }
 
