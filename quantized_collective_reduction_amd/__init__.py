@@ -949,13 +949,27 @@ def layer_norm_backward(grad_y, sum, weight, eps, grad_sum, grad_x, grad_weight,
     _vector(grad_weight, "grad_weight", h, torch.float32)
     if grad_bias is not None:
         _vector(grad_bias, "grad_bias", h, torch.float32)
-    need = ctypes.c_size_t()
-    _check(lib.qrs_layer_norm_backward_workspace(tokens, h, ctypes.byref(need)))
-    ws, nbytes, _keep = _workspace(workspace, need.value, sum, stream)  # _keep: until it is enqueued
+    need = _layer_norm_backward_workspace(tokens, h)
+    ws, nbytes, _keep = _workspace(workspace, need, sum, stream)  # _keep: until it is enqueued
     _check(lib.qrs_layer_norm_backward(
         tokens, h, io, eps, grad_y.data_ptr(), ld_y, sum.data_ptr(), ld_s, weight.data_ptr(),
         None if grad_sum is None else grad_sum.data_ptr(), ld_g, grad_x.data_ptr(), ld_x, grad_weight.data_ptr(),
         None if grad_bias is None else grad_bias.data_ptr(), ws, nbytes, _stream_handle(stream)))
+
+
+# A call's workspace goes by its shape alone, and a program has few shapes.
+@functools.lru_cache(maxsize=4096)
+def _layer_norm_backward_workspace(tokens, h):
+    need = ctypes.c_size_t()
+    _check(load_library().qrs_layer_norm_backward_workspace(tokens, h, ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _product_workspace(m, n, gated, layout):
+    need = ctypes.c_size_t()
+    _check(load_library().qrs_matmul_float_quantize_workspace(m, n, int(gated), layout, ctypes.byref(need)))
+    return need.value
 
 
 _BLOCK = 128  # rows and columns that share a scale
@@ -984,6 +998,8 @@ def _fp8_kind(t, what, given=None):
             return want
         if kind != want:
             raise ValueError(f"{what}: {t.dtype} codes, {given} given")
+    elif kind is not None:
+        return kind
     if kind is None:
         raise ValueError(f"{what}: float8_e4m3fn, float8_e5m2, or uint8 with its format named, expected, got {t.dtype}")
     return kind
@@ -1114,9 +1130,8 @@ def matmul_fp8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_
         raise ValueError(f"b_scales: [{_blocks(n)}, {_blocks(k)}] expected, got {list(b_scales.shape)}")
     mode = _mode(x_dtype, scale_layout)
     ld_c = _codes_and_scales(codes, scales, (m, n), mode)
-    need = ctypes.c_size_t()
-    _check(lib.qrs_matmul_float_quantize_workspace(m, n, 1 if gated else 0, mode[1], ctypes.byref(need)))
-    ws, nbytes, _keep = _workspace(workspace, need.value, a, stream) if need.value else (None, 0, None)
+    need = _product_workspace(m, n, bool(gated), mode[1])
+    ws, nbytes, _keep = _workspace(workspace, need, a, stream) if need else (None, 0, None)
     _check(lib.qrs_matmul_float_quantize(m, n, k, 1 if gated else 0, mode[0], mode[1], ka, a.data_ptr(), ld_a,
                                          a_scales.data_ptr(), kb, b.data_ptr(), ld_b, b_scales.data_ptr(),
                                          codes.data_ptr(), ld_c, scales.data_ptr(), ws, nbytes,
