@@ -467,7 +467,7 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
       }
     } else {
       constexpr int kBehind = 4, kRing = kBehind + 1;
-      f32x4 sums[kRing], channels[2];
+      f32x4 sums[kRing], channels[3];  // of the next, this and the last fragment of b
       auto fragment = [&](const char* rows, int f) {
         return __builtin_shufflevector(read(rows, f, 0), read(rows, f, 1), 0, 1, 2, 3, 4, 5, 6, 7);
       };
@@ -483,10 +483,11 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
           sums[x % kRing] = sums8<AF, BF>(fb[j % 2], fa[i]);
           if (i == 0 && j + 1 < FN) {
             fb[(j + 1) % 2] = fragment(lb, j + 1);
-            channels[(j + 1) % 2] = read_channels(base, j + 1);
+            channels[(j + 1) % 3] = read_channels(base, j + 1);
           }
         }
-        if (x >= kBehind) add(scales, channels[(x - kBehind) / FM % 2], sums[(x - kBehind) % kRing], x - kBehind);
+        static_assert(kBehind <= FM, "the last fragment's scales are kept");
+        if (x >= kBehind) add(scales, channels[(x - kBehind) / FM % 3], sums[(x - kBehind) % kRing], x - kBehind);
         __builtin_amdgcn_sched_barrier(0);
       }
     }

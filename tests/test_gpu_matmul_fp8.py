@@ -196,7 +196,7 @@ def test_gated_at_gates_of_any_size(gpu, m):
 MODES = [("int8", "f32_group128"), ("e4m3fn", "f32_group128"), ("e5m2", "f32_group128"), ("e4m3fn", "e8m0_block32"),
          ("e5m2", "e8m0_block32")]
 CODE_SIZES = [(1, 128, 16), (1, 4096, 1024), (5, 256, 3584), (16, 1024, 272), (33, 384, 64), (64, 2048, 512),
-              (130, 640, 1040), (300, 1280, 256), (1030, 2048, 512), (7, 128, 37)]
+              (130, 640, 1040), (300, 1280, 256), (1030, 2048, 512), (7, 128, 37), (29, 256, 640)]
 
 
 @pytest.mark.parametrize("x_format,layout", MODES)
