@@ -610,9 +610,11 @@ qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated,
                                    int64_t b_row_stride, const float* b_scales, void* codes, int64_t codes_row_stride,
                                    void* scales, void* workspace, size_t workspace_bytes, void* stream);
 
-/* qrs_matmul_launch_info of these two products. */
+/* qrs_matmul_launch_info of these two products; out_dtype is unused where
+ * quantize = 1. */
 qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gated, int b_scale_rows, int quantize,
-                                      qrs_scale_layout scale_layout, qrs_matmul_info* info_out);
+                                        qrs_out_dtype out_dtype, qrs_scale_layout scale_layout,
+                                        qrs_matmul_info* info_out);
 
 /* Free a plan. NULL is accepted. Plans in use by queued runs may be freed:
  * qrs_run copies what the kernel needs into its launch arguments. */

@@ -262,8 +262,8 @@ def load_library(path: str = LIB_PATH):
     lib.qrs_matmul_float_quantize_workspace.argtypes = [c_i64, c_i64, c_int, c_int, ctypes.POINTER(c_sz)]
     lib.qrs_matmul_float_quantize_workspace.restype = c_int
     lib.qrs_matmul_float_quantize.restype = c_int
-    lib.qrs_matmul_float_launch_info.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
-                                               ctypes.POINTER(MatmulInfo)]
+    lib.qrs_matmul_float_launch_info.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int, c_int,
+                                                 ctypes.POINTER(MatmulInfo)]
     lib.qrs_matmul_float_launch_info.restype = c_int
     _lib = lib
     return lib
@@ -1161,15 +1161,15 @@ def matmul_launch_info(m, n, k, gated=False, scale_layout=None) -> dict:
             "blocks": info.blocks, "threads_per_block": info.threads_per_block}
 
 
-def matmul_fp8_launch_info(m, n, k, gated=False, scale_layout=None, b_scale_rows=128) -> dict:
-    """``matmul_launch_info`` of ``matmul_fp8`` and, with a ``scale_layout``,
-    ``matmul_fp8_quantize``; ``b_scale_rows``: 128, or 1 for a row of scales for
+def matmul_fp8_launch_info(m, n, k, gated=False, scale_layout=None, b_scale_rows=128, out_dtype="f32") -> dict:
+    """``matmul_launch_info`` of ``matmul_fp8`` with outputs of ``out_dtype`` and,
+    with a ``scale_layout``, of ``matmul_fp8_quantize``; ``b_scale_rows``: 128, or 1 for a row of scales for
     each row of b (qrs_matmul_float_launch_info)."""
     lib = load_library()
     info = MatmulInfo()
     layout = ScaleLayout.F32_GROUP128 if scale_layout is None else _enum(scale_layout, _SCALE_NAMES, ScaleLayout)
     _check(lib.qrs_matmul_float_launch_info(m, n, k, 1 if gated else 0, b_scale_rows, 0 if scale_layout is None else 1,
-                                          layout, ctypes.byref(info)))
+                                            _enum(out_dtype, _OUT_NAMES, OutDtype), layout, ctypes.byref(info)))
     return {"kernel": ("tiles", "few_tokens", "mid", "pipe")[info.kernel], "tile": (info.tile_m, info.tile_n),
             "blocks": info.blocks, "threads_per_block": info.threads_per_block}
 

@@ -754,7 +754,8 @@ qrs_status qrs_matmul_float_quantize_workspace(int64_t m, int64_t n, int gated, 
 }
 
 qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gated, int b_scale_rows, int quantize,
-                                      qrs_scale_layout scale_layout, qrs_matmul_info* info_out) {
+                                        qrs_out_dtype out_dtype, qrs_scale_layout scale_layout,
+                                        qrs_matmul_info* info_out) {
   if (!info_out) return fail(QRS_ERR_INVALID_ARG, "null info pointer");
   QRS_TRY(check_fp8_shape(m, n, k, gated));
   QRS_TRY(check_scale_rows(b_scale_rows, gated));
@@ -763,11 +764,14 @@ qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gat
     QRS_TRY(check_codes(QRS_X_FP8_E4M3FN, scale_layout, false));
     QRS_TRY(check_multiple(n));
     if (b_scale_rows == 1) return fail(QRS_ERR_INVALID_ARG, "b_scale_rows 1: codes take scales of 128 rows of b");
+  } else {
+    QRS_TRY(check_float_type(out_dtype, "out_dtype"));
   }
   qrs::MatmulFp8Launch l;
   std::memset(&l, 0, sizeof(l));
   fp8_shape(&l, m, n, k, gated, b_scale_rows);
   l.quantize = quantize != 0;
+  l.out_format = quantize ? qrs::kOutF32 : to_format(out_dtype);
   l.scale_layout = scale_layout == QRS_SCALE_E8M0_BLOCK32 ? qrs::kScaleE8M0Block32 : qrs::kScaleF32Group128;
   l.vec = k % 16 == 0;
   l.a_stride = l.b_stride = static_cast<uint64_t>(k);

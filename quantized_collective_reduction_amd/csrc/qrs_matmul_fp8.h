@@ -1104,11 +1104,13 @@ Choice few_sized(const MatmulFp8Launch& l) {
 // Whether codes are widened: for outputs of binary32, and codes, whose scales are.
 bool wide(const MatmulFp8Launch& l) { return l.quantize || l.out_format == kOutF32; }
 
-template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM>
+template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM, bool WIDE_TOO = true>
 Choice mid(const MatmulFp8Launch& l) {
-  return {{kMatmulMid, TM, TN},
-          wide(l) ? mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, true> : mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, false>,
-          tiles_of(l, TM, FORM == kGatedForm ? TN / 2 : TN), 512};
+  Choice c = {{kMatmulMid, TM, TN}, mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, false>,
+              tiles_of(l, TM, FORM == kGatedForm ? TN / 2 : TN), 512};
+  if constexpr (WIDE_TOO)
+    if (wide(l)) c.kernel = mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, true>;
+  return c;
 }
 
 // Rows of operands that the busiest CU loads with tiles of TM tokens by TN
@@ -1138,7 +1140,13 @@ Choice choose_form(const MatmulFp8Launch& l) {
                                  : few_sized<AF, BF, 4, FORM>(l);
     return c.fits() ? c : general_tiles<AF, BF, true, FORM>(l);
   }
-  // The tile whose busiest CU loads least.
+  // The tile whose busiest CU loads least. The pipelined kernel's rows count a
+  // quarter more: its matrix units and the power limit bound it. us of bf16 outputs with
+  // <64, 32>, <64, 64>, <64, 128>, <128, 128>, <128, 256> and <256, 256>: 48 by 8192, k = 4096
+  // 12, 15, 21, 21, 33 and 51; 128 by 8192, k = 8192 43, 29, 40, 69, 89 and 108; 512 by 4096,
+  // k = 8192 77, 51, 37, 60, 82 and 120; 1024 by 4096, k = 4096 69, 45, 34, 30, 37 and 58;
+  // 1024 by 8192, k = 2048 93, 56, 41, 34, 25 and 33; 2048 by 8192, k = 2048 184, 109, 80, 64,
+  // 48 and 40. (Binary32 outputs the same but for <128, 256>, whose widened codes overflow the registers.)
   uint64_t least = ~uint64_t{0};
   Choice best = general_tiles<AF, BF, true, FORM>(l);
   auto offer = [&](uint64_t rows, const Choice& c) {
@@ -1148,14 +1156,18 @@ Choice choose_form(const MatmulFp8Launch& l) {
     }
   };
   offer(rows_a_cu<256, 256, FORM>(l) * 5 / 4, pipe<AF, BF, FORM>(l));
-  const bool group = l.quantize && l.scale_layout == kScaleF32Group128;  // 128 channels a tile
-  if (FORM != kGatedForm || !group) {
-    offer(rows_a_cu<128, 128, FORM>(l), mid<AF, BF, 128, 128, 1, 2, 4, FORM>(l));
-    offer(rows_a_cu<64, 128, FORM>(l), mid<AF, BF, 64, 128, 2, 1, 3, FORM>(l));
-    if (!group) offer(rows_a_cu<64, 64, FORM>(l), mid<AF, BF, 64, 64, 2, 2, 4, FORM>(l));
-  } else {
+  const bool group = l.quantize && l.scale_layout == kScaleF32Group128;  // 128 outputs a tile
+  if (FORM == kGatedForm && group) {
     offer(rows_a_cu<64, 256, FORM>(l), mid<AF, BF, 64, 256, 1, 2, 3, FORM>(l));
+    return best;
   }
+  if constexpr (FORM != kGrouped)  // whose scales overflow the registers, too
+    if (!wide(l)) offer(rows_a_cu<128, 256, FORM>(l), mid<AF, BF, 128, 256, 1, 2, 3, FORM, false>(l));
+  offer(rows_a_cu<128, 128, FORM>(l), mid<AF, BF, 128, 128, 1, 2, 4, FORM>(l));
+  offer(rows_a_cu<64, 128, FORM>(l), mid<AF, BF, 64, 128, 2, 1, 3, FORM>(l));
+  if (group) return best;
+  offer(rows_a_cu<64, 64, FORM>(l), mid<AF, BF, 64, 64, 2, 2, 4, FORM>(l));
+  if (!l.quantize || FORM == kPlain) offer(rows_a_cu<64, 32, FORM>(l), mid<AF, BF, 64, 32, 4, 2, 3, FORM>(l));
   return best;
 }
 

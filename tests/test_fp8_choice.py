@@ -6,7 +6,8 @@ import pytest
 
 import quantized_collective_reduction_amd as qrs
 
-FORMS = [dict(), dict(gated=True), dict(b_scale_rows=1), dict(scale_layout="f32_group128"),
+FORMS = [dict(), dict(out_dtype="bf16"), dict(gated=True), dict(gated=True, out_dtype="f16"), dict(b_scale_rows=1),
+         dict(b_scale_rows=1, out_dtype="bf16"), dict(scale_layout="f32_group128"),
          dict(scale_layout="e8m0_block32"), dict(gated=True, scale_layout="f32_group128"),
          dict(gated=True, scale_layout="e8m0_block32")]
 
@@ -48,17 +49,21 @@ def test_the_gpu_tests_reach_every_kernel():
 
     few = {("few_tokens", t) for t in [(8, 16), (16, 16), (32, 32)]}
     pipe = ("pipe", (256, 256))
-    mid = {("mid", (64, 64)), ("mid", (64, 128)), ("mid", (128, 128))}
-    for rows in (128, 1):
-        got = kernels(SIZES + MID + PIPE, b_scale_rows=rows)
-        assert few | mid | {pipe} <= got, few | mid - got
-    assert few | mid | {pipe} <= kernels(GATED + [(m, n // 2, k) for m, n, k in MID + PIPE], gated=True)
+    mid = {("mid", t) for t in [(64, 32), (64, 64), (64, 128), (128, 128)]}
+    wide = ("mid", (128, 256))  # of 16-bit outputs, with scales of 128 rows of b
+    sizes = SIZES + MID + PIPE
+    halves = GATED + [(m, n // 2, k) for m, n, k in MID + PIPE]
+    for out in ("f32", "bf16", "f16"):
+        more = {wide} if out != "f32" else set()
+        assert few | mid | {pipe} | more <= kernels(sizes, out_dtype=out)
+        assert few | mid | {pipe} <= kernels(sizes, b_scale_rows=1, out_dtype=out)
+        assert few | mid | {pipe} | more <= kernels(halves, gated=True, out_dtype=out)
     assert kernels([(66, 65, 100)]) == {("tiles", (64, 128))}
     assert kernels([(66, 65, 100)], gated=True) == {("tiles", (64, 256))}
-    large = CODE_SIZES + [(4096, 4096, 160), (4100, 8192, 272), (300, 4096, 400)]
+    large = CODE_SIZES + [(4096, 4096, 160), (4100, 8192, 272), (300, 4096, 400), (1000, 1024, 400)]
     assert few | {("mid", (64, 128)), ("mid", (128, 128)), pipe} <= kernels(large, scale_layout="f32_group128")
     few_codes = {("few_tokens", t) for t in [(8, 32), (16, 32), (32, 32)]}
     assert few_codes | mid | {pipe} <= kernels(large, scale_layout="e8m0_block32")
-    large = CODE_SIZES + [(4096, 2048, 160), (4100, 4096, 272), (300, 2048, 400)]
+    large = CODE_SIZES + [(4096, 2048, 160), (4100, 4096, 272), (300, 2048, 400), (1000, 512, 400)]
     assert few | {("mid", (64, 256)), pipe} <= kernels(large, scale_layout="f32_group128", gated=True)
-    assert few | mid | {pipe} <= kernels(large, scale_layout="e8m0_block32", gated=True)
+    assert few | mid - {("mid", (64, 32))} | {pipe} <= kernels(large, scale_layout="e8m0_block32", gated=True)

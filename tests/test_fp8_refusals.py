@@ -175,10 +175,11 @@ def test_launch_info_refusals(lib):
     info = qrs.MatmulInfo()
     ref = ctypes.byref(info)
     call = lib.qrs_matmul_float_launch_info
-    assert call(4, 256, 512, 0, 128, 0, 0, ref) == 0 and info.blocks > 0
-    for args in [(4, 256, 512, 0, 128, 2, 0, ref), (4, 200, 512, 0, 128, 1, 0, ref), (4, 256, 512, 0, 1, 1, 0, ref),
-                 (4, 256, 512, 1, 1, 0, 0, ref), (4, 256, 0, 0, 128, 0, 0, ref), (4, 256, 512, 0, 128, 1, ROW, ref),
-                 (4, 256, 512, 0, 128, 0, 0, None)]:
+    assert call(4, 256, 512, 0, 128, 0, BF16, 0, ref) == 0 and info.blocks > 0
+    for args in [(4, 256, 512, 0, 128, 2, BF16, 0, ref), (4, 200, 512, 0, 128, 1, BF16, 0, ref),
+                 (4, 256, 512, 0, 1, 1, BF16, 0, ref), (4, 256, 512, 1, 1, 0, BF16, 0, ref),
+                 (4, 256, 0, 0, 128, 0, BF16, 0, ref), (4, 256, 512, 0, 128, 1, BF16, ROW, ref),
+                 (4, 256, 512, 0, 128, 0, 7, 0, ref), (4, 256, 512, 0, 128, 0, BF16, 0, None)]:
         assert call(*args) == INVALID, args
 
 
