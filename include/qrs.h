@@ -472,11 +472,9 @@ qrs_status qrs_matmul_launch_info(int64_t m, int64_t n, int64_t k, int gated, in
  *
  * s is rounded once to the activations' type and stored in sum_out. Mean and
  * variance are those of the stored s to within 2^-33 of themselves (of the
- * largest |s - mean| for the mean), however large the mean is; y is computed in
- * binary32 to within 2^-24 * (4.1 |y - bias| + |y|), and in binary64 for rows
- * whose variance or mean is beyond 2^100 or var + eps below 2^-100; and it is
- * quantized in binary32 by qrs_quantize's rules, or with the whole row as one
- * group for QRS_SCALE_F32_ROW. A row that holds a NaN or an infinity, and one of
+ * largest |s - mean| for the mean), however large the mean is; y is computed from
+ * them in binary64, rounded once to binary32 and quantized by qrs_quantize's rules,
+ * or with the whole row as one group for QRS_SCALE_F32_ROW. A row that holds a NaN or an infinity, and one of
  * equal values with eps = 0, has NaN in y: its scales are NaN (E8M0 code 255), and
  * its codes are unspecified.
  *
@@ -499,8 +497,8 @@ qrs_status qrs_add_layer_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype 
  *   grad_bias   = sum over tokens of grad_y
  *
  * The sums along a row are binary64, of products d rounded to binary32; the rest
- * is binary32, and binary64 for rows as above and those whose mean(d) or
- * mean(d * u) is beyond 2^100; grad_x is rounded once to io_dtype. grad_weight
+ * is binary32, and binary64 for rows whose mean, variance, mean(d) or mean(d * u)
+ * is beyond 2^100 or var + eps below 2^-100; grad_x is rounded once to io_dtype. grad_weight
  * and grad_bias are added in binary32.
  *
  *   grad_x      may be grad_y or grad_sum themselves (same pointer and
@@ -563,10 +561,14 @@ qrs_status qrs_quantize_transposed(int64_t rows, int64_t cols, qrs_out_dtype in_
  * out[i][j] = sum over groups g of 128 of k of
  *             P[i][j][g] * fp32(a_scales[i][g] * b_scales[j / R][g]),
  * with P[i][j][g] the sum over k in g of a[i][k] * b[j][k]: a is [m, k] codes
- * (tokens), b is [n, k] codes (output channels), each E4M3FN or E5M2. P is a matrix
- * instruction's sum in binary32, its product with the scales is added by a fused
- * operation, and groups are added in a fixed order for a given shape; the result is
- * rounded once to out_dtype. NaN and infinite codes go through as in the formula.
+ * (tokens), b is [n, k] codes (output channels), each E4M3FN or E5M2. P is added in
+ * binary32, its product with the scales is added by a fused operation, and groups
+ * are added in a fixed order for a given shape; the result is rounded once to
+ * out_dtype. More than 32 tokens' P for 16-bit outputs may come from instructions
+ * that first add eight products of consecutive k with 2^-14 of the largest as the
+ * last place, within 2^-11 of the sum of the eight's magnitudes (in norm, 1.5e-5 of
+ * the result for normal values, where bfloat16's own rounding leaves 1.7e-3 and
+ * float16's 2e-4). NaN and infinite codes go through as in the formula.
  *
  * The gradients of the dequantized operands are such products themselves: of
  * grad_out's rows with b transposed (qrs_quantize_blocks), and of the transposes of

@@ -3,11 +3,14 @@
 //
 //   s = x + residual                   (rounded to the activations' type)
 //   mean, var of s along the row;  r = 1 / sqrt(var + eps)
-//   y = (s - mean) * r * weight + bias (binary32)
+//   y = (s - mean) * r * weight + bias (rounded to binary32)
 //   codes, scales = quantize(y)
 //
 // A row stays in the registers of one work-group from its load to its codes:
-// one pass over memory, bound by HBM.
+// one pass over memory. The binary64 operations, 42 to 56 vector instructions for
+// each element of a lane, take about as long as it: bf16 16384 x 8192 with E4M3FN
+// codes 170 us (5.5 TB/s; without them, in a norm by squares alone, 147), 8192 x 5120
+// fp32 92 us (5.9); its gradient 190 us (5.6).
 //
 // Mean and variance come from one reduction. A wave adds d = s - s0 and d^2 in
 // binary64, s0 being the first of its own elements. Then the mean of d, squared,

@@ -9,14 +9,17 @@
 // The matrix instructions for 8-bit floats add the products of eight consecutive
 // codes with 2^-14 of the largest one as the last place (measured: 448 * 448 + 4
 // is 448 * 448, where the 4 stands in the same eight): 1.5e-5 of the result's norm for
-// normal values, 100 times what binary32 sums leave. So codes are widened to
-// bfloat16, which holds every one of them (two codes an instruction), and the
+// normal values, 100 times what binary32 sums leave, a hundredth of what rounding to
+// 16 bits does. So outputs of 16 bits may use them, and for the others codes are
+// widened to bfloat16, which holds every one of them (two codes an instruction), and the
 // bfloat16 instructions, whose sums keep binary32 (1e-8 of the norm), multiply them at half the
-// rate. Kernels that wait for memory lose nothing by it.
+// rate. Kernels that wait for memory lose nothing by it and always widen.
 //
-// A group's sums of a 16 x 16 fragment are four instructions of 32 k; they are
-// then multiplied by the scales' product and added in binary32 by one fused
-// operation, and rounded once at the end.
+// A group's sums of a 16 x 16 fragment are one instruction of 128 k, or four of 32;
+// they are then multiplied by the scales' product and added in binary32 by one fused
+// operation, and rounded once at the end. That is a vector operation for every four
+// (fragments' elements by lanes) products of the matrix unit's rate, and the two run
+// side by side only where the code keeps both fed.
 //
 // b is the first operand of the matrix instructions and a the second: a lane
 // then holds four consecutive output channels of one token. Of a group's 128
