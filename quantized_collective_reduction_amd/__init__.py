@@ -1037,7 +1037,8 @@ def _quantize_blocks(by_block, x, codes, scales, codes_t, scales_t, x_dtype, str
         ld_c = _fp8_codes(codes, scales, "codes", (rows, cols), (br, _blocks(cols)), xd)
     if codes_t is not None:
         if codes_t.dim() != 2 or not rows <= codes_t.shape[1] <= _blocks(rows) * _BLOCK:
-            raise ValueError(f"codes_t: [{cols}, {rows} to {_blocks(rows) * _BLOCK}] expected, got {list(codes_t.shape)}")
+            raise ValueError(f"codes_t: [{cols}, {rows} to {_blocks(rows) * _BLOCK}] expected, "
+                             f"got {list(codes_t.shape)}")
         rows_t = codes_t.shape[1]
         ld_t = _fp8_codes(codes_t, scales_t, "codes_t", (cols, rows_t), (bc, _blocks(rows)), xd)
     ptr = [None if t is None else t.data_ptr() for t in (codes, scales, codes_t, scales_t)]

@@ -351,7 +351,8 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
     const char* dy_row = static_cast<const char*>(a.grad_y) + row * a.grad_y_stride * kSize;
     const char* s_row = static_cast<const char*>(a.sum) + row * a.sum_stride * kSize;
     // Without a grad_sum, s stands in and is taken as zero below.
-    const char* g_row = a.grad_sum != nullptr ? static_cast<const char*>(a.grad_sum) + row * a.grad_sum_stride * kSize : s_row;
+    const char* g_row = s_row;
+    if (a.grad_sum != nullptr) g_row = static_cast<const char*>(a.grad_sum) + row * a.grad_sum_stride * kSize;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const uint32_t c = (p * NT + lane) * E;

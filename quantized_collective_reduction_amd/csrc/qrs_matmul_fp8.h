@@ -180,7 +180,8 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulFp8Launch a) {
   for (int i = 0; i < FM; ++i)
     sa[i] = a.a_scales + static_cast<uint64_t>(min(i0 + 16 * i + lane % 16, a.m - 1)) * a.groups;
   // The wave's 16 FN rows of b lie in one block.
-  const float* sb = a.b_scales + static_cast<uint64_t>(j0 / kTileN + (wave >= 2 && FORM == kGatedForm ? a.up_block : 0)) * a.groups;
+  const uint32_t b_block = j0 / kTileN + (wave >= 2 && FORM == kGatedForm ? a.up_block : 0);
+  const float* sb = a.b_scales + static_cast<uint64_t>(b_block) * a.groups;
 
   for (uint32_t g = 0; g < a.groups; ++g) {
     const uint32_t r = threadIdx.x / 8, chunk = threadIdx.x % 8 * 16;
@@ -196,7 +197,8 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulFp8Launch a) {
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < kA + kB; ++t)
-      *reinterpret_cast<u32x4*>((t < kA ? la + (r + 32 * t) * T::kPitch : lb + (r + 32 * (t - kA)) * T::kPitch) + chunk) = w[t];
+      *reinterpret_cast<u32x4*>((t < kA ? la + (r + 32 * t) * T::kPitch : lb + (r + 32 * (t - kA)) * T::kPitch) + chunk) =
+          w[t];
     __syncthreads();
     auto fragment = [&](const char* rows, int n) {
       return *reinterpret_cast<const i32x4*>(rows + lane % 16 * T::kPitch + lane / 16 * 16 + n * 64);
@@ -235,7 +237,8 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulFp8Launch a) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      *reinterpret_cast<f32x4*>(lc + (16 * i + lane % 16) * T::kCPitch + (FN * wave + j) * 16 + lane / 16 * 4) = acc[i][j];
+      *reinterpret_cast<f32x4*>(lc + (16 * i + lane % 16) * T::kCPitch + (FN * wave + j) * 16 + lane / 16 * 4) =
+          acc[i][j];
   __syncthreads();
   constexpr uint32_t pieces = kTileN / kPiece;
   for (uint32_t t = threadIdx.x; t < kTileM * pieces; t += 256) {
@@ -382,8 +385,8 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
 #pragma unroll
     for (int t = 0; t < P::kLoads; ++t) {
       const uint32_t far = k + chunk[t % 2] < a.k ? 0 : kFar;  // past the end of k: zeros
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(base + (wave * P::kLoads + t) * 1024), 16, off_a[t] + far, k,
-                                               0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          ra, (lds_ptr)(base + (wave * P::kLoads + t) * 1024), 16, off_a[t] + far, k, 0, 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rb, (lds_ptr)(base + P::kSide * kGroup + (wave * P::kLoads + t) * 1024), 16, off_b[t] + far, k, 0, 0);
     }
@@ -921,15 +924,17 @@ __global__ __launch_bounds__(512, 2) void mid_kernel(const MatmulFp8Launch a) {
   constexpr int KF = kKeepA ? FM : FN, SF = kKeepA ? FN : FM;
   auto add = [&](const Fragments& f, const f32x4& sums, int x) {
     const int i = kKeepA ? x % KF : x / KF, j = kKeepA ? x / KF : x % KF;
+    const float* c = f.channel[j];
     if constexpr (FORM == kGrouped)
-      add_scaled(acc[i][j], sums, f.token[i], f32x4{f.channel[j][0], f.channel[j][1], f.channel[j][2], f.channel[j][3]});
+      add_scaled(acc[i][j], sums, f.token[i], f32x4{c[0], c[1], c[2], c[3]});
     else
-      add_scaled(acc[i][j], sums, f.token[i] * f.channel[j][0]);
+      add_scaled(acc[i][j], sums, f.token[i] * c[0]);
   };
   // Two codes' widening of a streamed or kept fragment: `word` of its 16.
   auto widen_word = [&](Wide<2>& to, const Fragments& f, bool kept, int index, int word) {
     const bool of_a = kept == kKeepA;
-    const uint32_t codes = static_cast<uint32_t>(of_a ? f.a[index][word / 8][word / 2 % 4] : f.b[index][word / 8][word / 2 % 4]);
+    const i32x4& chunk = of_a ? f.a[index][word / 8] : f.b[index][word / 8];
+    const uint32_t codes = static_cast<uint32_t>(chunk[word / 2 % 4]);
     u32x4 w = __builtin_bit_cast(u32x4, to.part[word / 4]);
     if (of_a)
       w[word % 4] = word % 2 ? widen2<AF, true>(codes) : widen2<AF, false>(codes);
@@ -974,7 +979,7 @@ __global__ __launch_bounds__(512, 2) void mid_kernel(const MatmulFp8Launch a) {
         if (x > 0 && live) {  // a quarter of the fragment before
           const f32x4& from = sums[(x - 1) % kRing];
           const int i = kKeepA ? (x - 1) % KF : (x - 1) / KF, j = kKeepA ? (x - 1) / KF : (x - 1) % KF;
-          const float scale = FORM == kGrouped ? now.token[i] * now.channel[j][t % kScalesB] : now.token[i] * now.channel[j][0];
+          const float scale = now.token[i] * now.channel[j][t % kScalesB];
           acc[i][j][t] = __builtin_fmaf(from[t], scale, acc[i][j][t]);
         }
       } else {
