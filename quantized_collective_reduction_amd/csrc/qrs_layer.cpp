@@ -469,7 +469,7 @@ qrs_status qrs_layer_norm_backward_workspace(int64_t tokens, int64_t h, size_t* 
   *bytes_out = 0;
   QRS_TRY(check_row_shape(tokens, h));
   *bytes_out = static_cast<size_t>(h) * 8 *
-               qrs::layer_norm_backward_parts(static_cast<uint64_t>(tokens), static_cast<uint32_t>(h));
+               qrs::layer_norm_backward_parts(static_cast<uint64_t>(tokens), static_cast<uint32_t>(h), false);
   return ok();
 }
 

@@ -510,7 +510,7 @@ __global__ __launch_bounds__(1024) void grad_params_kernel(const float* parts, f
 
 template <int IO, int NT, int P, bool VEC, bool STREAM>
 hipError_t launch_backward_as(const LayerNormBackwardLaunch& l, hipStream_t stream) {
-  const uint32_t parts = layer_norm_backward_parts(l.rows, l.h);
+  const uint32_t parts = layer_norm_backward_parts(l.rows, l.h, IO == kOutF32);
   const hipError_t e =
       launch_kernel(layer_norm_backward_kernel<IO, NT, P, VEC, STREAM>, dim3(parts), dim3(NT), stream, l);
   if (e != hipSuccess) return e;
@@ -554,15 +554,18 @@ hipError_t launch_layer_norm(const LayerNormLaunch& l, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-uint32_t layer_norm_backward_parts(uint64_t rows, uint32_t h) {
-  // One a CU, as each leaves two rows of partial sums; more where rows are narrow, if
-  // they have rows to load ahead. us with 256, 512 and 1024: bf16 16384 x 1024 92, 73 and
-  // 46; 8192 x 2048 66, 52 and 37; 8192 x 4096 71, 58 and 67; 16384 x 8192 226, 190 and 200;
-  // 1021 x 7168 24, 27 and 37; 500 x 2048 12, 13 and 13.
+uint32_t layer_norm_backward_parts(uint64_t rows, uint32_t h, bool f32) {
+  // One a CU, as each leaves two rows of partial sums; more where rows are narrow, or
+  // of 16 bits, which wait for vector instructions, if they have rows to load ahead.
+  // us with 256, 512 and 1024: bf16 16384 x 1024 92, 73 and 46; 8192 x 2048 66, 52 and
+  // 37; 4096 x 4096 42, 38 and 42; 1021 x 7168 25, 28 and 37; 2560 x 8192 47, 46 and 59;
+  // 8192 x 8192 120, 102; 16384 x 8192 226, 190 and 200; 4096 x 16384 112, 126 and 154;
+  // fp32 16384 x 1024 93, 69 and 56; 8192 x 2048 70, 54 and 58; 16384 x 4096 177, 192;
+  // 8192 x 5120 112, 120.
   uint32_t parts = 256;
   if (h <= 256 * kPiece && rows >= 4 * 1024)
     parts = 1024;
-  else if (rows >= (h <= 512 * kPiece ? 4 * 512 : 16 * 512 + 1))
+  else if (h <= 256 * kPiece ? rows >= 4 * 512 : !f32 && h <= 1024 * kPiece && rows >= 5 * 512)
     parts = 512;
   return static_cast<uint32_t>(rows < parts ? rows : parts);
 }
