@@ -269,6 +269,12 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulFp8Launch a) {
 //
 // In the gated form a wave's rows of b are 32 gates, their ups, 32 gates and
 // their ups.
+//
+// 4096 x 8192, k = 7168 to bf16 219 to 238 us (2.0 to 2.2 PFLOP/s, of 2.55 that a
+// product without scales reaches here), 8192 cubed 511 to 540: the scaled additions
+// beside the matrix instructions, and the power limit (without the checks of k's end
+// for every load, a tenth of the other instructions, the same time). Widened, 4096 x
+// 8192, k = 4096 to binary32 247 us (1.1 PFLOP/s, of 1.3 for bfloat16).
 struct Pipe {
   static constexpr int kSide = 256, kThreads = 512, kWaveM = 64, kWaveN = 128;
   static constexpr int FM = kWaveM / 16, FN = kWaveN / 16;
@@ -635,6 +641,8 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
 // brings the scales of the rows of b and of the tokens, one a lane.
 //
 // The waves' sums meet in LDS and are added in the order of the waves.
+//
+// One token by 8192 x 8192 12.5 us, 5.4 TB/s.
 template <int M8, int GW, int KW, int RB, int FORM>
 struct Few {
   static constexpr int kWaves = GW * KW, MT = (M8 + 1) / 2, FB = RB / 16;
@@ -800,7 +808,9 @@ __global__ __launch_bounds__(64 * GW * KW) void few_tokens_kernel(const MatmulFp
 // load, S - 1 stages ahead, with their scales, so that most of LDS holds operands in
 // flight, in whole lines. What bounds these tiles is how fast operands come
 // into a CU, and next the widening of their codes. Slots as in the pipelined tiles.
-// Two waves a SIMD hide each other's reads; one barrier a stage.
+// Two waves a SIMD hide each other's reads; one barrier a stage. 333 by 5120, k =
+// 7168 to bf16 30 us, to binary32 37; with stages of half the length and twice as
+// many, a quarter more bytes under way, 33 and 42.
 template <int TM, int TN, int KG, int WM, int S>
 struct Mid {
   static constexpr int kThreads = 512, kWavesN = 8 / KG / WM, WTM = TM / WM, WTN = TN / kWavesN;
