@@ -472,7 +472,8 @@ qrs_status qrs_matmul_launch_info(int64_t m, int64_t n, int64_t k, int gated, in
  *
  * s is rounded once to the activations' type and stored in sum_out. Mean and
  * variance are those of the stored s to within 2^-33 of themselves (of the
- * largest |s - mean| for the mean), however large the mean is; y is computed from
+ * largest |s - mean| for the mean), however large the mean is, and exact for a row
+ * of equal values, whose y is the bias; y is computed from
  * them in binary64, rounded once to binary32 and quantized by qrs_quantize's rules,
  * or with the whole row as one group for QRS_SCALE_F32_ROW. A row that holds a NaN or an infinity, and one of
  * equal values with eps = 0, has NaN in y: its scales are NaN (E8M0 code 255), and
@@ -498,7 +499,7 @@ qrs_status qrs_add_layer_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype 
  *
  * The sums along a row are binary64, of products d rounded to binary32; the rest
  * is binary32, and binary64 for rows whose mean, variance, mean(d) or mean(d * u)
- * is beyond 2^100 or var + eps below 2^-100; grad_x is rounded once to io_dtype. grad_weight
+ * is beyond 2^100, or var + eps below 2^-100 or 2^-32 of the mean's square; grad_x is rounded once to io_dtype. grad_weight
  * and grad_bias are added in binary32.
  *
  *   grad_x      may be grad_y or grad_sum themselves (same pointer and

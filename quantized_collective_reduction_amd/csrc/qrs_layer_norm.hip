@@ -17,8 +17,9 @@
 // is at most n - 1 times the variance of its n elements (s0, one of them, is that
 // far from the mean), so what sum d^2 - (sum d)^2 / n cancels is at most a factor
 // of n <= 65536, and it keeps 53 - 16 bits whatever the mean, the size of the
-// values or the outliers. The waves' means and sums of squares about them are then
-// joined exactly as their definition says.
+// values or the outliers. The waves are then joined by their distances from the first
+// one's s0, exactly as the definition says: no value as large as the mean is added or
+// multiplied by 1 / h, and in a row of equal values every distance is zero.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -53,14 +54,14 @@ __device__ __forceinline__ float first_lane(float v) {
 }
 
 // Sums of d = s - s0 and d^2 over a wave's elements, n of them and inv_n = 1 / n,
-// -> their mean and the sum of squares about it (zeros of no elements, with
+// -> the mean of d and the sum of squares about it (zeros of no elements, with
 // inv_n = 0).
 struct WaveMoments {
-  double mean, squares;
+  double dm, squares;
 };
-__device__ __forceinline__ WaveMoments wave_moments(float s0, double d1, double d2, double inv_n) {
+__device__ __forceinline__ WaveMoments wave_moments(double d1, double d2, double inv_n) {
   const double dm = d1 * inv_n;
-  return {s0 + dm, d2 - d1 * dm};
+  return {dm, d2 - d1 * dm};
 }
 
 // Sum over each row of 16 lanes, in a fixed order, in every lane of it.
@@ -71,25 +72,33 @@ __device__ __forceinline__ double sum16(double v) {
   return v + lanes(v, [](uint32_t x) { return dpp<kDppMirror>(x); });
 }
 
-// A row's mean, as a float and what that leaves, and 1 / sqrt(var + eps).
+// A row's mean, as a value s0 of the row and its distance from that, and as a
+// float and what that leaves, and 1 / sqrt(var + eps).
 struct Moments {
-  double mean, r, m;  // m = var + eps
-  float mean_hi, mean_lo, r32;
+  double distance, r, m;  // m = var + eps
+  float s0, mean_hi, mean_lo, r32;
 
-  __device__ __forceinline__ void finish(double mean64, double squares, double inv_h, float eps) {
-    mean = mean64;
+  __device__ __forceinline__ void finish(float first, double from_first, double squares, double inv_h, float eps) {
+    s0 = first;
+    distance = from_first;
     m = squares * inv_h + static_cast<double>(eps);
     r = inverse_root(m);
-    mean_hi = static_cast<float>(mean);
-    mean_lo = static_cast<float>(mean - mean_hi);
+    mean_hi = static_cast<float>(s0 + distance);
+    mean_lo = static_cast<float>((static_cast<double>(s0) - mean_hi) + distance);
     r32 = static_cast<float>(r);
   }
-  // Whether binary32 does not hold what follows.
+  // Whether binary32 does not hold what follows. mean_lo is off by 2^-49 of the mean:
+  // at most 2^-33 deviations while these are more than 2^-16 of the mean.
   __device__ __forceinline__ bool wide() const {
-    return !(m > 0x1p-100 && m < 0x1p100 && __builtin_fabs(mean) < 0x1p100);
+    const double mean = mean_hi;
+    return !(m > 0x1p-100 && m < 0x1p100 && __builtin_fabs(mean) < 0x1p100 && m > mean * mean * 0x1p-32);
   }
-  // s - mean: off by two roundings of itself, however large the mean is.
+  // s - mean: off by two roundings of itself, and 2^-33 deviations.
   __device__ __forceinline__ float centred(float s) const { return (s - mean_hi) - mean_lo; }
+  // (s - mean) * r, however large the mean is.
+  __device__ __forceinline__ double unit(float s) const {
+    return ((static_cast<double>(s) - s0) - distance) * r;
+  }
 };
 
 // ---- forward -----------------------------------------------------------
@@ -124,7 +133,7 @@ template <int IO, int SL, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a) {
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;  // P8: 8 elements a lane
   constexpr int kWaves = NT / 64;
-  __shared__ double part[2][kWaves][2], count[kWaves];
+  __shared__ double part[2][kWaves][3], count[kWaves];
   __shared__ uint32_t max_part[2][kWaves];
   const int lane = threadIdx.x;
   constexpr int kSize = kOutSize<IO>;
@@ -189,19 +198,26 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a)
         d2 = __builtin_fma(d, d, d2);
       }
     }
-    const WaveMoments wm = wave_moments(s0, wave_sum(d1), wave_sum(d2), inv_mine);
+    const WaveMoments wm = wave_moments(wave_sum(d1), wave_sum(d2), inv_mine);
     if (lane % 64 == 0) {
-      part[turn][lane / 64][0] = wm.mean;
-      part[turn][lane / 64][1] = wm.squares;
+      double* to = part[turn][lane / 64];
+      to[0] = s0;
+      to[1] = wm.dm;
+      to[2] = wm.squares;
     }
     lds_barrier();
-    // Lane l joins wave l % 16's part.
+    // Lane l joins wave l % 16's part, from the first wave's s0 on.
     const int i = lane % 16;
-    const double n = i < kWaves ? count[i] : 0.0, wave_mean = i < kWaves ? part[turn][i][0] : 0.0;
-    const double mean = sum16(n * wave_mean) * a.inv_h;
-    const double off = wave_mean - mean;
-    const double squares = sum16(__builtin_fma(n * off, off, i < kWaves ? part[turn][i][1] : 0.0));
-    const double r = inverse_root(squares * a.inv_h + static_cast<double>(a.eps));
+    const double first = part[turn][0][0];
+    double n = 0.0, far = 0.0, wave_squares = 0.0;
+    if (i < kWaves) {
+      n = count[i];
+      far = (part[turn][i][0] - first) + part[turn][i][1];
+      wave_squares = part[turn][i][2];
+    }
+    const double distance = sum16(n * far) * a.inv_h, off = far - distance;
+    const double squares = sum16(__builtin_fma(n * off, off, wave_squares));
+    const double r = inverse_root(squares * a.inv_h + static_cast<double>(a.eps)), shift = -distance * r;
 
     // y over s.
 #pragma unroll
@@ -220,7 +236,7 @@ __global__ __launch_bounds__(NT) void layer_norm_kernel(const LayerNormLaunch a)
       b[p].get(bv);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const double u = (static_cast<double>(s[p][j]) - mean) * r;
+        const double u = __builtin_fma(static_cast<double>(s[p][j]) - first, r, shift);
         const float y = static_cast<float>(__builtin_fma(u, static_cast<double>(wv[j]), static_cast<double>(bv[j])));
         s[p][j] = VEC || c + j < a.h ? y : 0.0f;
       }
@@ -330,7 +346,7 @@ hipError_t launch_norm_io(const LayerNormLaunch& l, hipStream_t stream) {
 template <int IO, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNormBackwardLaunch a) {
   constexpr int kWaves = NT / 64;
-  __shared__ double part[2][kWaves][4], count[kWaves];
+  __shared__ double part[2][kWaves][5], count[kWaves];
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;
   const int lane = threadIdx.x;
   constexpr int kSize = kOutSize<IO>;
@@ -397,28 +413,31 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
     }
     d1 = wave_sum(d1);
     g1 = wave_sum(g1);
-    const WaveMoments wm = wave_moments(s0, d1, wave_sum(d2), inv_mine);
+    const WaveMoments wm = wave_moments(d1, wave_sum(d2), inv_mine);
     gd = wave_sum(gd);
     if (lane % 64 == 0) {
       double* to = part[turn][lane / 64];
-      to[0] = wm.mean;
-      to[1] = wm.squares;
-      to[2] = g1;
-      to[3] = gd - g1 * (d1 * inv_mine);
+      to[0] = s0;
+      to[1] = wm.dm;
+      to[2] = wm.squares;
+      to[3] = g1;
+      to[4] = gd - g1 * wm.dm;
     }
     lds_barrier();
     const int i = lane % 16;
-    double n = 0.0, all[4] = {0.0, 0.0, 0.0, 0.0};  // of wave i
+    const float row_first = static_cast<float>(part[turn][0][0]);
+    double n = 0.0, far = 0.0, all[3] = {0.0, 0.0, 0.0};  // of wave i
     if (i < kWaves) {
       n = count[i];
+      far = (part[turn][i][0] - row_first) + part[turn][i][1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) all[e] = part[turn][i][e];
+      for (int e = 0; e < 3; ++e) all[e] = part[turn][i][2 + e];
     }
-    const double mean = sum16(n * all[0]) * a.inv_h, off = all[0] - mean;
-    const double squares = sum16(__builtin_fma(n * off, off, all[1])), sum_d = sum16(all[2]);
-    const double sum_du = sum16(__builtin_fma(all[2], off, all[3]));
+    const double distance = sum16(n * far) * a.inv_h, off = far - distance;
+    const double squares = sum16(__builtin_fma(n * off, off, all[0])), sum_d = sum16(all[1]);
+    const double sum_du = sum16(__builtin_fma(all[1], off, all[2]));
     Moments mo;
-    mo.finish(mean, squares, a.inv_h, a.eps);
+    mo.finish(row_first, distance, squares, a.inv_h, a.eps);
     const double mean_d = sum_d * a.inv_h, mean_du = sum_du * a.inv_h * mo.r;
     if (IO != kOutF32) {
       // Unpacked again: kept, they would cost the registers of a second work-group
@@ -445,7 +464,7 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
       if (__builtin_expect(wide, false)) {
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-          const double u = (static_cast<double>(s[j]) - mo.mean) * mo.r;
+          const double u = mo.unit(s[j]);
           dw[p][j] += static_cast<float>(dy[j] * u);
           g[j] = static_cast<float>(g[j] + mo.r * (static_cast<double>(wv[j]) * dy[j] - mean_d - u * mean_du));
         }
