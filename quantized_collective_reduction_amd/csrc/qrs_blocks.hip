@@ -39,6 +39,13 @@ __device__ __forceinline__ uint32_t max_bits(const float (&v)[kPiece]) {
   return m;
 }
 
+// f32_multiplier, with zero for NaN: what lies beside a matrix's rows in a block is
+// zero and has to stay so, whatever the rows hold.
+__device__ __forceinline__ float block_multiplier(uint32_t amax, float top, float* scale) {
+  const float mul = f32_multiplier(amax, top, scale);
+  return mul == mul ? mul : 0.0f;
+}
+
 // A piece of x; 16-bit types as a stream that leaves no copy in the caches (7168 x
 // 8192 bf16 both ways 45.4 us through them, 40.8 as a stream; 16384 x 8192 transposed
 // 92 and 74; but 8192 x 8192 fp32 85 and 92).
@@ -91,7 +98,7 @@ __global__ __launch_bounds__(256) void blocks_kernel(const BlocksLaunch a) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) amax = max(amax, maxima[i][0]);
-    block_mul = f32_multiplier(amax, kMax, &block_scale);
+    block_mul = block_multiplier(amax, kMax, &block_scale);
     if (threadIdx.x == 0) {
       const uint32_t tiles_r = static_cast<uint32_t>((a.rows + kSide - 1) / kSide);
       if (a.codes) a.scales[static_cast<uint64_t>(tr) * tiles_c + tc] = block_scale;
@@ -112,7 +119,7 @@ __global__ __launch_bounds__(256) void blocks_kernel(const BlocksLaunch a) {
       const uint32_t r = pr * kPiece + pc;
       if (pc < kPiece) {
         float scale;
-        row_mul[r] = f32_multiplier(mine, kMax, &scale);
+        row_mul[r] = block_multiplier(mine, kMax, &scale);
         if (r < rows) a.scales[(r0 + r) * tiles_c + tc] = scale;
       }
     }
@@ -132,7 +139,7 @@ __global__ __launch_bounds__(256) void blocks_kernel(const BlocksLaunch a) {
       if (c < kSide) {
         const uint32_t tiles_r = static_cast<uint32_t>((a.rows + kSide - 1) / kSide);
         float scale;
-        col_mul[c] = f32_multiplier(max(max(maxima[0][c], maxima[1][c]), max(maxima[2][c], maxima[3][c])), kMax, &scale);
+        col_mul[c] = block_multiplier(max(max(maxima[0][c], maxima[1][c]), max(maxima[2][c], maxima[3][c])), kMax, &scale);
         if (c < cols) a.scales_t[(c0 + c) * tiles_r + tr] = scale;
       }
     }
