@@ -101,6 +101,11 @@ struct Moments {
   }
 };
 
+// Whether binary32 holds values of about this size, and a few bits less, as normal numbers.
+__device__ __forceinline__ bool in_range(double v) {
+  return __builtin_fabs(v) >= 0x1p-100 && __builtin_fabs(v) < 0x1p100;
+}
+
 // ---- forward -----------------------------------------------------------
 
 // A format as a type.
@@ -344,7 +349,7 @@ hipError_t launch_norm_io(const LayerNormLaunch& l, hipStream_t stream) {
 // the workspace, and grad_params_kernel adds those rows in order: a fixed order
 // without atomics.
 template <int IO, int NT, int P8, bool VEC, bool STREAM>
-__global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNormBackwardLaunch a) {
+__global__ __launch_bounds__(NT, P8 <= 2 ? 2 : 1) void layer_norm_backward_kernel(const LayerNormBackwardLaunch a) {
   constexpr int kWaves = NT / 64;
   __shared__ double part[2][kWaves][5], count[kWaves];
   constexpr int E = kPiece16<IO>, P = P8 * 8 / E;
@@ -413,6 +418,39 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
     }
     d1 = wave_sum(d1);
     g1 = wave_sum(g1);
+    // A wave's products that may have left binary32's range are made again in binary64,
+    // unless there is no gradient (half precision's cannot; all of them in binary64 16384
+    // x 8192 bf16 195 us, so 190). Loaded once more, the operands cost other rows no
+    // registers.
+    if (IO != kOutF16 && __builtin_expect(!in_range(g1), false)) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float dy[E];
+        now.dy[p].get(dy);
+#pragma unroll
+        for (int j = 0; j < E; ++j) any |= abs_bits(dy[j]);
+      }
+      if (__ballot(any != 0) != 0) {
+        g1 = gd = 0.0;
+#pragma unroll 1
+        for (int p = 0; p < P; ++p) {
+          const uint32_t c = (p * NT + lane) * E;
+          float wv[E], dy[E], s[E];
+          load_piece<IO, VEC, E>(a.weight, c, a.h, wv);
+          load_piece<IO, VEC, E>(static_cast<const char*>(a.grad_y) + row * a.grad_y_stride * kSize, c, a.h, dy);
+          load_piece<IO, VEC, E>(static_cast<const char*>(a.sum) + row * a.sum_stride * kSize, c, a.h, s);
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            if (!(VEC ? c < a.h : c + j < a.h)) continue;
+            const double g = static_cast<double>(wv[j]) * dy[j];
+            g1 += g;
+            gd = __builtin_fma(g, static_cast<double>(s[j]) - s0, gd);
+          }
+        }
+        g1 = wave_sum(g1);
+      }
+    }
     const WaveMoments wm = wave_moments(d1, wave_sum(d2), inv_mine);
     gd = wave_sum(gd);
     if (lane % 64 == 0) {
@@ -449,7 +487,9 @@ __global__ __launch_bounds__(NT) void layer_norm_backward_kernel(const LayerNorm
         now.s[p].renew();
       }
     }
-    const bool wide = mo.wide() || !(__builtin_fabs(mean_d) < 0x1p100 && __builtin_fabs(mean_du) < 0x1p100);
+    // Means of zero, as of rows without a gradient, binary32 holds.
+    const double most = __builtin_fmax(__builtin_fabs(mean_d), __builtin_fabs(mean_du));
+    const bool wide = mo.wide() || !(most < 0x1p100) || (most < 0x1p-100 && most > 0.0);
     const float mean_d32 = static_cast<float>(mean_d), mean_du32 = static_cast<float>(mean_du);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
