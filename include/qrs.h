@@ -498,10 +498,12 @@ qrs_status qrs_add_layer_norm_quantize(int64_t tokens, int64_t h, qrs_out_dtype 
  *   grad_bias   = sum over tokens of grad_y
  *
  * The sums along a row are binary64, of products d rounded to binary32, or of exact
- * ones where d is beyond its range; the rest is binary32, and binary64 for rows whose mean, variance, mean(d) or mean(d * u) is beyond
- * 2^100, whose var + eps is below 2^-100 or 2^-32 of the mean's square, or whose
- * mean(d) and mean(d * u) are both below 2^-100; grad_x is rounded once to
- * io_dtype. grad_weight and grad_bias are added in binary32.
+ * ones where d is beyond its range; the rest is binary32, and binary64 for rows
+ * whose mean, variance, mean(d) or mean(d * u) is beyond 2^100, whose var + eps is
+ * below 2^-100 or 2^-32 of the mean's square, or whose mean(d) and mean(d * u) are
+ * both below 2^-100; grad_x is rounded once to io_dtype. grad_weight and grad_bias
+ * are added in binary32, in a fixed order: at most 64 rows at a time, then those
+ * sums, 65536 rows of them together at most, then those of the whole batch.
  *
  *   grad_x      may be grad_y or grad_sum themselves (same pointer and
  *               stride).
