@@ -306,7 +306,8 @@ hipError_t launch_norm_sized(const LayerNormLaunch& l, hipStream_t stream) {
     if (l.h <= 128 * 1 * kPiece) return launch_norm_as<IO, SL, 128, 1, VEC, STREAM>(l, 2048, stream);
     if (l.h <= 128 * 2 * kPiece) return launch_norm_as<IO, SL, 128, 2, VEC, STREAM>(l, 2048, stream);
     if (l.h <= 256 * 2 * kPiece) return launch_norm_as<IO, SL, 256, 2, VEC, STREAM>(l, 2048, stream);
-    if (IO == kOutF32 && l.h <= 768 * 1 * kPiece) return launch_norm_as<IO, SL, 768, 1, VEC, STREAM>(l, 256, stream);
+    if constexpr (IO == kOutF32)
+      if (l.h <= 768 * 1 * kPiece) return launch_norm_as<IO, SL, 768, 1, VEC, STREAM>(l, 256, stream);
   }
   if (l.h <= 512 * 2 * kPiece)
     return launch_norm_as<IO, SL, 512, 2, VEC, STREAM>(l, IO == kOutF32 ? 256 : 2048, stream);
@@ -605,9 +606,12 @@ hipError_t launch_backward_sized(const LayerNormBackwardLaunch& l, hipStream_t s
     if (l.h <= 128 * 1 * kPiece) return launch_backward_as<IO, 128, 1, VEC, STREAM>(l, stream);
     if (l.h <= 128 * 2 * kPiece) return launch_backward_as<IO, 128, 2, VEC, STREAM>(l, stream);
     if (l.h <= 256 * 2 * kPiece) return launch_backward_as<IO, 256, 2, VEC, STREAM>(l, stream);
-    if (IO == kOutF32 && l.h <= 512 * 2 * kPiece) return launch_backward_as<IO, 512, 2, VEC, STREAM>(l, stream);
   }
-  if (l.h <= 256 * 4 * kPiece) return launch_backward_as<IO, 256, 4, VEC, STREAM>(l, stream);
+  if constexpr (VEC && IO == kOutF32) {
+    if (l.h <= 512 * 2 * kPiece) return launch_backward_as<IO, 512, 2, VEC, STREAM>(l, stream);
+  } else {
+    if (l.h <= 256 * 4 * kPiece) return launch_backward_as<IO, 256, 4, VEC, STREAM>(l, stream);
+  }
   if constexpr (VEC)
     if (l.h <= 512 * 4 * kPiece) return launch_backward_as<IO, 512, 4, VEC, STREAM>(l, stream);
   if (l.h <= 1024 * 8 * kPiece) return launch_backward_as<IO, 1024, 8, VEC, STREAM>(l, stream);

@@ -1122,11 +1122,14 @@ Choice few_sized(const MatmulFp8Launch& l) {
 // Whether codes are widened: for outputs of binary32, and codes, whose scales are.
 bool wide(const MatmulFp8Launch& l) { return l.quantize || l.out_format == kOutF32; }
 
-template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM, bool WIDE_TOO = true>
+// The ways of adding that calls take a tile in.
+enum Ways : int { kNarrow = 1, kWide = 2, kBoth = 3 };
+
+template <XFormat AF, XFormat BF, int TM, int TN, int KG, int WM, int S, int FORM, int WAYS = kBoth>
 Choice mid(const MatmulFp8Launch& l) {
-  Choice c = {{kMatmulMid, TM, TN}, mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, false>,
+  Choice c = {{kMatmulMid, TM, TN}, mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, WAYS == kWide>,
               tiles_of(l, TM, FORM == kGatedForm ? TN / 2 : TN), 512};
-  if constexpr (WIDE_TOO)
+  if constexpr (WAYS == kBoth)
     if (wide(l)) c.kernel = mid_kernel<AF, BF, TM, TN, KG, WM, S, FORM, true>;
   return c;
 }
@@ -1175,12 +1178,14 @@ Choice choose_form(const MatmulFp8Launch& l) {
   };
   offer(rows_a_cu<256, 256, FORM>(l) * 5 / 4, pipe<AF, BF, FORM>(l));
   const bool group = l.quantize && l.scale_layout == kScaleF32Group128;  // 128 outputs a tile
-  if (FORM == kGatedForm && group) {
-    offer(rows_a_cu<64, 256, FORM>(l), mid<AF, BF, 64, 256, 1, 2, 3, FORM>(l));
-    return best;
+  if constexpr (FORM == kGatedForm) {
+    if (group) {
+      offer(rows_a_cu<64, 256, FORM>(l), mid<AF, BF, 64, 256, 1, 2, 3, FORM, kWide>(l));
+      return best;
+    }
   }
   if constexpr (FORM != kGrouped)  // whose scales overflow the registers, too
-    if (!wide(l)) offer(rows_a_cu<128, 256, FORM>(l), mid<AF, BF, 128, 256, 1, 2, 3, FORM, false>(l));
+    if (!wide(l)) offer(rows_a_cu<128, 256, FORM>(l), mid<AF, BF, 128, 256, 1, 2, 3, FORM, kNarrow>(l));
   offer(rows_a_cu<128, 128, FORM>(l), mid<AF, BF, 128, 128, 1, 2, 4, FORM>(l));
   offer(rows_a_cu<64, 128, FORM>(l), mid<AF, BF, 64, 128, 2, 1, 3, FORM>(l));
   if (group) return best;
