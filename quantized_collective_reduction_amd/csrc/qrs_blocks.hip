@@ -11,8 +11,8 @@
 // A work-group of 256 lanes holds a block in registers, 8 x 8 values a lane, so
 // one read of the matrix serves both outputs. A lane's eight rows of a column are
 // the eight bytes of a piece of the transpose, which goes through LDS and leaves in whole
-// lines. The kernel is a stream, bound by HBM: bf16 7168 x 8192 with blocks 32 us
-// (5.5 TB/s), with the transpose beside them 43 (5.5).
+// lines. The kernel is a stream, bound by HBM: bf16 7168 x 8192 with blocks 31 us
+// (5.7 TB/s), with the transpose beside them 40 (5.8).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -46,9 +46,13 @@ __device__ __forceinline__ float block_multiplier(uint32_t amax, float top, floa
   return mul == mul ? mul : 0.0f;
 }
 
-// A piece of x; 16-bit types as a stream that leaves no copy in the caches (7168 x
-// 8192 bf16 both ways 45.4 us through them, 40.8 as a stream; 16384 x 8192 transposed
-// 92 and 74; but 8192 x 8192 fp32 85 and 92).
+// A piece of x; 16-bit types as a stream that leaves no copy in the caches, of any size.
+// us through the caches and as a stream, bf16 both ways from memory: 1021 x 5120 12.5 and
+// 9.6, 4096 x 4096 17.9 and 15.1, 7168 x 8192 58.4 and 48.7; transposed alone 16384 x 8192
+// 93 and 74; a linear layer's gradients, whose operands an operation just wrote, 1021 x
+// 3584 x 4096 90.9 and 88.0, 4096 x 8192 x 7168 873 and 851. (Only a matrix of 130 to 240
+// MB that is read again and again gains by a copy: 4096 x 8192 27.7 and 31.8; and 8192 x
+// 8192 fp32 85 and 92.)
 template <int IO, bool VEC>
 __device__ __forceinline__ void load_values(const void* row, uint32_t c, uint32_t h, float* v) {
   if constexpr (VEC && IO != kOutF32) {
@@ -60,9 +64,17 @@ __device__ __forceinline__ void load_values(const void* row, uint32_t c, uint32_
   }
 }
 
-// STREAM: the transposed codes leave past the caches, as they do beside the rows' own
-// (bf16 7168 x 8192 47.8 us through the caches, 43.0 so; 16384 x 8192 122 and 116; alone
-// 75 and 89).
+// STREAM: the transposed codes leave past the caches, for matrices whose input and
+// outputs are more than half of the Infinity Cache's 256 MB and that write the rows' own
+// codes beside them. us of blocks through the caches and so, bf16 1021 x 5120 8.9 and 8.9,
+// 4096 x 4096 13.3 and 14.2, 4096 x 8192 28.6 and 27.6, 7168 x 8192 44.9 and 40.5, 16384 x
+// 8192 116 and 95 (alone, 16384 x 8192 75 and 89). Products that read the codes next find
+// them in the cache: with both products of 1021 tokens a weight of 3584 x 4096 66.7 and
+// 72.3, a linear layer's gradients 4096 x 3584 x 4096 234 and 238; so do larger ones (of
+// 4096 tokens, a weight of 8192 x 7168 497 and 511), but their own time gains more where
+// nothing reads them at once.
+constexpr uint64_t kStreamCodes = uint64_t{128} << 20;
+
 template <int IO, int XF, bool BY_BLOCK, bool VEC, bool STREAM>
 __global__ __launch_bounds__(256) void blocks_kernel(const BlocksLaunch a) {
   // The transposed codes: piece b (8 rows) of column c in slot b ^ (c / 8) of the
@@ -195,9 +207,10 @@ template <int IO, int XF, bool BY_BLOCK>
 hipError_t launch_typed(const BlocksLaunch& l, hipStream_t stream) {
   const uint64_t tiles = (l.rows + kSide - 1) / kSide * ((l.cols + kSide - 1) / kSide);
   if (tiles == 0 || tiles >= uint64_t{1} << 24) return hipErrorInvalidValue;  // a grid holds fewer than 2^32 work-items
-  return launch_kernel(!l.vec                 ? blocks_kernel<IO, XF, BY_BLOCK, false, false>
-                       : l.codes && l.codes_t ? blocks_kernel<IO, XF, BY_BLOCK, true, true>
-                                              : blocks_kernel<IO, XF, BY_BLOCK, true, false>,
+  const bool stream_t = l.codes && l.codes_t && l.rows * l.cols * (kOutSize<IO> + 2) > kStreamCodes;
+  return launch_kernel(!l.vec     ? blocks_kernel<IO, XF, BY_BLOCK, false, false>
+                       : stream_t ? blocks_kernel<IO, XF, BY_BLOCK, true, true>
+                                  : blocks_kernel<IO, XF, BY_BLOCK, true, false>,
                        dim3(static_cast<uint32_t>(tiles)), dim3(256), stream, l);
 }
 
