@@ -325,6 +325,7 @@ qrs_status qrs_quantize(int64_t tokens, int64_t h, qrs_x_dtype x_dtype, qrs_scal
  *   qrs_quantize_transposed    the transpose's codes, a scale for each 128 of
  *                              its columns, and the rows' beside them
  *   qrs_matmul_float             the product of such codes, also gated
+ *   qrs_matmul_float_single      the same, 16-bit outputs from binary32 sums, too
  *   qrs_matmul_float_quantize    the same, written as codes and scales
  *
  * Common to all of them: asynchronous on `stream` (a hipStream_t, NULL = the
@@ -572,7 +573,9 @@ qrs_status qrs_quantize_transposed(int64_t rows, int64_t cols, qrs_out_dtype in_
  * that first add eight products of consecutive k with 2^-14 of the largest as the
  * last place, within 2^-11 of the sum of the eight's magnitudes (in norm, 1.5e-5 of
  * the result for normal values, where bfloat16's own rounding leaves 1.7e-3 and
- * float16's 2e-4). NaN and infinite codes go through as in the formula.
+ * float16's 2e-4). Where large products may cancel and what is beside them counts,
+ * qrs_matmul_float_single keeps binary32 throughout. NaN and infinite codes go
+ * through as in the formula.
  *
  * The gradients of the dequantized operands are such products themselves: of
  * grad_out's rows with b transposed (qrs_quantize_blocks), and of the transposes of
@@ -596,6 +599,14 @@ qrs_status qrs_matmul_float(int64_t m, int64_t n, int64_t k, int gated, qrs_out_
                           int b_scale_rows, const void* b, int64_t b_row_stride, const float* b_scales, void* out,
                           int64_t out_row_stride, void* stream);
 
+/* qrs_matmul_float with P added in binary32 whatever out_dtype is: what it gives as
+ * QRS_OUT_F32, rounded once more. More than 32 tokens with 16-bit outputs take up to
+ * twice the time. */
+qrs_status qrs_matmul_float_single(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype,
+                                   qrs_x_dtype a_dtype, const void* a, int64_t a_row_stride, const float* a_scales,
+                                   qrs_x_dtype b_dtype, int b_scale_rows, const void* b, int64_t b_row_stride,
+                                   const float* b_scales, void* out, int64_t out_row_stride, void* stream);
+
 /*
  * The same product, gated or not, with scales of 128 rows of b, quantized in binary32 by
  * qrs_quantize's rules: one rank's partial sums as qrs_run reads them, or (gated, with
@@ -616,8 +627,8 @@ qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated,
                                    int64_t b_row_stride, const float* b_scales, void* codes, int64_t codes_row_stride,
                                    void* scales, void* workspace, size_t workspace_bytes, void* stream);
 
-/* qrs_matmul_launch_info of these two products; out_dtype is unused where
- * quantize = 1. */
+/* qrs_matmul_launch_info of these products; out_dtype is unused where quantize = 1,
+ * and QRS_OUT_F32 for qrs_matmul_float_single. */
 qrs_status qrs_matmul_float_launch_info(int64_t m, int64_t n, int64_t k, int gated, int b_scale_rows, int quantize,
                                         qrs_out_dtype out_dtype, qrs_scale_layout scale_layout,
                                         qrs_matmul_info* info_out);

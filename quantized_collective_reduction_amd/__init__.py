@@ -136,6 +136,7 @@ EXPORTED_SYMBOLS = (
     "qrs_quantize_blocks",
     "qrs_quantize_transposed",
     "qrs_matmul_float",
+    "qrs_matmul_float_single",
     "qrs_matmul_float_quantize",
     "qrs_matmul_float_quantize_workspace",
     "qrs_matmul_float_launch_info",
@@ -257,6 +258,8 @@ def load_library(path: str = LIB_PATH):
     lib.qrs_matmul_float.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, vp, c_i64, vp, c_int, c_int, vp, c_i64,
                                    vp, vp, c_i64, vp]
     lib.qrs_matmul_float.restype = c_int
+    lib.qrs_matmul_float_single.argtypes = lib.qrs_matmul_float.argtypes
+    lib.qrs_matmul_float_single.restype = c_int
     lib.qrs_matmul_float_quantize.argtypes = [c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int, vp, c_i64, vp, c_int, vp,
                                               c_i64, vp, vp, c_i64, vp, vp, c_sz, vp]
     lib.qrs_matmul_float_quantize_workspace.argtypes = [c_i64, c_i64, c_int, c_int, ctypes.POINTER(c_sz)]
@@ -1093,7 +1096,8 @@ def _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype):
     return m, n, k, ka, ld_a, kb, 1 if grouped else _BLOCK, ld_b
 
 
-def matmul_fp8(a, a_scales, b, b_scales, out, gated=False, a_dtype=None, b_dtype=None, stream=None):
+def matmul_fp8(a, a_scales, b, b_scales, out, gated=False, a_dtype=None, b_dtype=None, stream=None,
+               binary32_sums=False):
     """The product ``a @ b.T`` of 8-bit floating-point codes ``a [m, k]``
     (tokens) and ``b [n, k]`` (channels) with float32 scales for each 128 of k
     (qrs_matmul_float): ``a_scales [m, ceil(k / 128)]``, as "f32_group128" codes
@@ -1106,14 +1110,19 @@ def matmul_fp8(a, a_scales, b, b_scales, out, gated=False, a_dtype=None, b_dtype
 
     ``gated``: ``b`` is ``[2 n, k]``, n gate and then n up channels, ``b_scales``
     the gates' ceil(n / 128) rows and then the ups', and
-    ``out = silu(gate product) * up product``."""
+    ``out = silu(gate product) * up product``.
+
+    ``binary32_sums``: 16-bit outputs of more than 32 tokens come from products added in
+    binary32, as float32 ones do, at up to twice the time (qrs_matmul_float_single).
+    Otherwise eight consecutive products may be added to 2^-14 of the largest: not
+    for operands whose large products cancel."""
     lib = load_library()
     m, n, k, ka, ld_a, kb, scale_rows, ld_b = _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype)
     kind = _act_dtype(out, "out")
     ld_o = _matrix(out, "out", (m, n))
-    _check(lib.qrs_matmul_float(m, n, k, 1 if gated else 0, kind, ka, a.data_ptr(), ld_a, a_scales.data_ptr(), kb,
-                              scale_rows, b.data_ptr(), ld_b, b_scales.data_ptr(), out.data_ptr(), ld_o,
-                              _stream_handle(stream)))
+    call = lib.qrs_matmul_float_single if binary32_sums else lib.qrs_matmul_float
+    _check(call(m, n, k, 1 if gated else 0, kind, ka, a.data_ptr(), ld_a, a_scales.data_ptr(), kb, scale_rows,
+                b.data_ptr(), ld_b, b_scales.data_ptr(), out.data_ptr(), ld_o, _stream_handle(stream)))
 
 
 def matmul_fp8_quantize(a, a_scales, b, b_scales, codes, scales, x_dtype, scale_layout, gated=False, a_dtype=None,
@@ -1163,9 +1172,10 @@ def matmul_launch_info(m, n, k, gated=False, scale_layout=None) -> dict:
 
 
 def matmul_fp8_launch_info(m, n, k, gated=False, scale_layout=None, b_scale_rows=128, out_dtype="f32") -> dict:
-    """``matmul_launch_info`` of ``matmul_fp8`` with outputs of ``out_dtype`` and,
-    with a ``scale_layout``, of ``matmul_fp8_quantize``; ``b_scale_rows``: 128, or 1 for a row of scales for
-    each row of b (qrs_matmul_float_launch_info)."""
+    """``matmul_launch_info`` of ``matmul_fp8`` with outputs of ``out_dtype`` ("f32", too,
+    with ``binary32_sums``) and, with a ``scale_layout``, of ``matmul_fp8_quantize``;
+    ``b_scale_rows``: 128, or 1 for a row of scales for each row of b
+    (qrs_matmul_float_launch_info)."""
     lib = load_library()
     info = MatmulInfo()
     layout = ScaleLayout.F32_GROUP128 if scale_layout is None else _enum(scale_layout, _SCALE_NAMES, ScaleLayout)

@@ -667,6 +667,23 @@ qrs_status matmul_fp8(qrs::MatmulFp8Launch* l, int64_t m, int64_t n, int64_t k, 
   return launched(qrs::launch_matmul_fp8(*l, static_cast<hipStream_t>(stream)));
 }
 
+qrs_status matmul_fp8_values(bool binary32, int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype,
+                             qrs_x_dtype a_dtype, const void* a, int64_t a_row_stride, const float* a_scales,
+                             qrs_x_dtype b_dtype, int b_scale_rows, const void* b, int64_t b_row_stride,
+                             const float* b_scales, void* out, int64_t out_row_stride, void* stream) {
+  QRS_TRY(check_fp8_shape(m, n, k, gated));
+  QRS_TRY(check_float_type(out_dtype, "out_dtype"));
+  qrs::MatmulFp8Launch l;
+  std::memset(&l, 0, sizeof(l));
+  l.quantize = false;
+  l.binary32 = binary32;
+  l.out_format = to_format(out_dtype);
+  const Rows o = {"out", out, m, n, out_row_stride, type_size(out_dtype)};
+  const Rows none = {"scales", nullptr, 1, 1, 1, 1};
+  return matmul_fp8(&l, m, n, k, gated, a_dtype, a, a_row_stride, a_scales, b_dtype, b_scale_rows, b, b_row_stride,
+                    b_scales, o, none, stream);
+}
+
 qrs_status check_multiple(int64_t n) {
   if (n % 128 != 0) return fail(QRS_ERR_INVALID_ARG, "n %lld is not a multiple of 128", static_cast<long long>(n));
   return QRS_OK;
@@ -698,16 +715,16 @@ qrs_status qrs_matmul_float(int64_t m, int64_t n, int64_t k, int gated, qrs_out_
                           const void* a, int64_t a_row_stride, const float* a_scales, qrs_x_dtype b_dtype,
                           int b_scale_rows, const void* b, int64_t b_row_stride, const float* b_scales, void* out,
                           int64_t out_row_stride, void* stream) {
-  QRS_TRY(check_fp8_shape(m, n, k, gated));
-  QRS_TRY(check_float_type(out_dtype, "out_dtype"));
-  qrs::MatmulFp8Launch l;
-  std::memset(&l, 0, sizeof(l));
-  l.quantize = false;
-  l.out_format = to_format(out_dtype);
-  const Rows o = {"out", out, m, n, out_row_stride, type_size(out_dtype)};
-  const Rows none = {"scales", nullptr, 1, 1, 1, 1};
-  return matmul_fp8(&l, m, n, k, gated, a_dtype, a, a_row_stride, a_scales, b_dtype, b_scale_rows, b, b_row_stride,
-                    b_scales, o, none, stream);
+  return matmul_fp8_values(false, m, n, k, gated, out_dtype, a_dtype, a, a_row_stride, a_scales, b_dtype, b_scale_rows,
+                           b, b_row_stride, b_scales, out, out_row_stride, stream);
+}
+
+qrs_status qrs_matmul_float_single(int64_t m, int64_t n, int64_t k, int gated, qrs_out_dtype out_dtype,
+                                   qrs_x_dtype a_dtype, const void* a, int64_t a_row_stride, const float* a_scales,
+                                   qrs_x_dtype b_dtype, int b_scale_rows, const void* b, int64_t b_row_stride,
+                                   const float* b_scales, void* out, int64_t out_row_stride, void* stream) {
+  return matmul_fp8_values(true, m, n, k, gated, out_dtype, a_dtype, a, a_row_stride, a_scales, b_dtype, b_scale_rows,
+                           b, b_row_stride, b_scales, out, out_row_stride, stream);
 }
 
 qrs_status qrs_matmul_float_quantize(int64_t m, int64_t n, int64_t k, int gated, qrs_x_dtype x_dtype,

@@ -165,6 +165,7 @@ hipError_t launch_matmul(const MatmulLaunch& l, hipStream_t stream);
 struct MatmulFp8Launch : MatmulLaunch {
   XFormat a_format, b_format;  // kXE4M3FN or kXE5M2
   bool grouped;                // not gated, quantize = false
+  bool binary32;               // 16-bit outputs, too, of products added in binary32
   uint32_t groups;             // ceil(k / 128)
   uint32_t up_block;           // gated: the first of the ups' rows of b_scales
   float* workspace;            // fp8_workspace(..) bytes, 16-byte aligned

@@ -10,7 +10,8 @@
 // codes with 2^-14 of the largest one as the last place (measured: 448 * 448 + 4
 // is 448 * 448, where the 4 stands in the same eight): 1.5e-5 of the result's norm for
 // normal values, 100 times what binary32 sums leave, a hundredth of what rounding to
-// 16 bits does. So outputs of 16 bits may use them, and for the others codes are
+// 16 bits does. So outputs of 16 bits may use them (unless the caller asks for binary32
+// sums, as where large products cancel), and for the others codes are
 // widened to bfloat16, which holds every one of them (two codes an instruction), and the
 // bfloat16 instructions, whose sums keep binary32 (1e-8 of the norm), multiply them at half the
 // rate. Kernels that wait for memory lose nothing by it and always widen.
@@ -1119,8 +1120,9 @@ Choice few_sized(const MatmulFp8Launch& l) {
   return few<AF, BF, M8, 1, M8 == 2 ? 4 : 8, RB, FORM>(l);
 }
 
-// Whether codes are widened: for outputs of binary32, and codes, whose scales are.
-bool wide(const MatmulFp8Launch& l) { return l.quantize || l.out_format == kOutF32; }
+// Whether codes are widened: for outputs of binary32, and codes, whose scales are, and
+// where the caller asks for it.
+bool wide(const MatmulFp8Launch& l) { return l.quantize || l.out_format == kOutF32 || l.binary32; }
 
 // The ways of adding that calls take a tile in.
 enum Ways : int { kNarrow = 1, kWide = 2, kBoth = 3 };
