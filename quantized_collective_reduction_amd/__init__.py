@@ -1114,8 +1114,8 @@ def matmul_fp8(a, a_scales, b, b_scales, out, gated=False, a_dtype=None, b_dtype
 
     ``binary32_sums``: 16-bit outputs of more than 32 tokens come from products added in
     binary32, as float32 ones do, at up to twice the time (qrs_matmul_float_single).
-    Otherwise eight consecutive products may be added to 2^-14 of the largest: not
-    for operands whose large products cancel."""
+    Otherwise eight consecutive products may be cut to 2^-13 of the largest before they
+    are added: not for operands whose large products cancel."""
     lib = load_library()
     m, n, k, ka, ld_a, kb, scale_rows, ld_b = _fp8_operands(a, a_scales, b, b_scales, gated, a_dtype, b_dtype)
     kind = _act_dtype(out, "out")

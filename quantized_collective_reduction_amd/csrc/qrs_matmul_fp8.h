@@ -6,15 +6,16 @@
 // of its gated form silu(gate) * up (two products over the same tokens), and of
 // both as codes and scales.
 //
-// The matrix instructions for 8-bit floats add the products of eight consecutive
-// codes with 2^-14 of the largest one as the last place (measured: 448 * 448 + 4
-// is 448 * 448, where the 4 stands in the same eight): 1.5e-5 of the result's norm for
-// normal values, 100 times what binary32 sums leave, a hundredth of what rounding to
-// 16 bits does. So outputs of 16 bits may use them (unless the caller asks for binary32
-// sums, as where large products cancel), and for the others codes are
-// widened to bfloat16, which holds every one of them (two codes an instruction), and the
-// bfloat16 instructions, whose sums keep binary32 (1e-8 of the norm), multiply them at half the
-// rate. Kernels that wait for memory lose nothing by it and always widen.
+// The matrix instructions for 8-bit floats cut the products of eight consecutive codes
+// toward zero to multiples of 2^-13 of the largest one, taken by the codes' powers of two
+// (measured: beside 256 * 256 and beside 448 * 448, 7 is gone and 12 is 8, where they stand
+// in the same eight), and add them: 1.5e-5 of the result's norm for normal values, whose
+// other products mostly lie whole above that, 100 times what binary32 sums leave, a
+// hundredth of what rounding to 16 bits does. So outputs of 16 bits may use them (unless
+// the caller asks for binary32 sums, as where large products cancel), and for the others
+// codes are widened to bfloat16, which holds every one of them (two codes an instruction),
+// and the bfloat16 instructions, whose sums keep binary32 (1e-8 of the norm), multiply them
+// at half the rate. Kernels that wait for memory lose nothing by it and always widen.
 //
 // A group's sums of a 16 x 16 fragment are one instruction of 128 k, or four of 32;
 // they are then multiplied by the scales' product and added in binary32 by one fused
