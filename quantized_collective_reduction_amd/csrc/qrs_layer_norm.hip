@@ -9,8 +9,8 @@
 // A row stays in the registers of one work-group from its load to its codes:
 // one pass over memory. The binary64 operations, 42 to 56 vector instructions for
 // each element of a lane, take about as long as it: bf16 16384 x 8192 with E4M3FN
-// codes 170 us (5.5 TB/s; without them, in a norm by squares alone, 147), 8192 x 5120
-// fp32 92 us (5.9); its gradient 190 us (5.6).
+// codes 169 us (5.6 TB/s; without them, in a norm by squares alone, 147), 8192 x 5120
+// fp32 93 us (5.9); the first one's gradient 188 us (5.7).
 //
 // Mean and variance come from one reduction. A wave adds d = s - s0 and d^2 in
 // binary64, s0 being the first of its own elements. Then the mean of d, squared,
@@ -298,8 +298,9 @@ hipError_t launch_norm_as(const LayerNormLaunch& l, uint32_t blocks, hipStream_t
 // 16384 x 1024 128 x 1 28, 256 x 2 58; 8192 x 4096 256 x 2 45, 512 x 1 50; 16384 x 8192
 // 512 x 2 in 256, 512 and 2048 work-groups 202, 178 and 170, 256 x 4 213; 4096 x 7168
 // 52, 45 and 44; fp32 8192 x 5120 768 x 1 in 256 and 4096 92 and 110, 512 x 2 96 and 128.
-// Rows off 16-byte boundaries have two shapes. (Scratch memory takes part of rows
-// past 8192 elements.)
+// Rows off 16-byte boundaries have two shapes. Scratch memory takes part of the rows of
+// 1024 x 2 lanes of binary32 and of 1024 x 8 (fp32 2048 x 16384 130 us, 3.4 TB/s; bf16
+// 1024 x 32768 151, 1.6; off boundaries 4096 x 8191 178, 1.3, 2048 x 16383 1129, 0.2).
 template <int IO, int SL, bool VEC, bool STREAM>
 hipError_t launch_norm_sized(const LayerNormLaunch& l, hipStream_t stream) {
   if constexpr (VEC) {

@@ -87,7 +87,8 @@ __device__ __forceinline__ void finish_codes(const MatmulLaunch& a, uint32_t i, 
 }
 
 // Eight outputs of a row off 16-byte boundaries: the hardware stores 16 bytes at any
-// address of an element (333 x 5003 floats, k = 7168 39 us, with a store for each element 44).
+// address of an element (333 x 5003, k = 7168, of 8-bit floats from memory: floats 37 us, with a
+// store for each element 40; bf16 27.3 and 29.1).
 template <int OF>
 __device__ __forceinline__ void store_piece_anywhere(void* row, uint32_t c, const float* v) {
   if constexpr (OF == kOutF32) {

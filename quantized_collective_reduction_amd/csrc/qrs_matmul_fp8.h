@@ -273,10 +273,10 @@ __global__ __launch_bounds__(256) void tile_kernel(const MatmulFp8Launch a) {
 // their ups.
 //
 // 4096 x 8192, k = 7168 to bf16 219 to 238 us (2.0 to 2.2 PFLOP/s, of 2.55 that a
-// product without scales reaches here), 8192 cubed 511 to 540: the scaled additions
+// product without scales reaches here), 8192 cubed 501 to 540: the scaled additions
 // beside the matrix instructions, and the power limit (without the checks of k's end
 // for every load, a tenth of the other instructions, the same time). Widened, 4096 x
-// 8192, k = 4096 to binary32 247 us (1.1 PFLOP/s, of 1.3 for bfloat16).
+// 8192, k = 4096 to binary32 233 to 247 us (1.1 to 1.2 PFLOP/s, of 1.3 for bfloat16).
 struct Pipe {
   static constexpr int kSide = 256, kThreads = 512, kWaveM = 64, kWaveN = 128;
   static constexpr int FM = kWaveM / 16, FN = kWaveN / 16;
@@ -644,7 +644,8 @@ __global__ __launch_bounds__(Pipe::kThreads, 2) void pipe_kernel(const MatmulFp8
 //
 // The waves' sums meet in LDS and are added in the order of the waves.
 //
-// One token by 8192 x 8192 12.5 us, 5.4 TB/s.
+// One token by 8192 x 8192 12.5 to 13.3 us, 5.4 to 5.0 TB/s (three sets of weights in turn,
+// and more than the Infinity Cache holds).
 template <int M8, int GW, int KW, int RB, int FORM>
 struct Few {
   static constexpr int kWaves = GW * KW, MT = (M8 + 1) / 2, FB = RB / 16;
@@ -1108,9 +1109,9 @@ bool by_workspace(const MatmulFp8Launch& l) {
 }
 
 // Sixteen rows of b a wave: more work-groups, two of them a CU, keep more lines under
-// way than 32 rows do (one token, us with 16 and 32: 8192 x 8192 14.2 and 17.9,
-// 28672 x 8192 38.1 and 52.6; 16 tokens, 8192 x 8192 16.1 and 18.4), but for more
-// than 16 tokens, whose own lines would be two of three (21.0 and 20.0).
+// way than 32 rows do (one token, us with 16 and 32: 8192 x 8192 13.3 and 17.3,
+// 28672 x 8192 38.4 and 53.6; 16 tokens, 8192 x 8192 15.8 and 19.7), but for more
+// than 16 tokens, whose own lines would be two of three (32 tokens 22.9 and 19.9).
 template <XFormat AF, XFormat BF, int M8, int FORM>
 Choice few_sized(const MatmulFp8Launch& l) {
   constexpr int RB = M8 == 4 ? 32 : 16;
