@@ -25,7 +25,7 @@ def _chain(t, h, kind):
     """Additions, each off by half a step of its result, that a term goes through:
     with others of its work-group, with those of before, in the lanes and the
     row of the last kernel."""
-    groups = min(_work_groups(t, h), 256) if kind == "f32" else _work_groups(t, h)  # binary32: fewer, if any
+    groups = min(_work_groups(t, h), 256) if kind == "f32" and h > 2048 else _work_groups(t, h)
     rows = -(-t // groups)
     return min(rows, FOLD) + -(-rows // FOLD) + -(-groups // 32) + 32
 
