@@ -39,3 +39,25 @@ def test_products_beyond_binary32(gpu, t, h, w_exp, dy_exp, s_exp, kind):
         off = np.abs(got - ref)
         keep = near if what == "x" else np.ones_like(ref, bool)
         assert np.all(off[keep] <= tol[keep]), (what, np.max((off / tol)[keep]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("which", ["grad_y", "grad_sum"])
+@pytest.mark.parametrize("t,h", [(600, 1024), (5, 101), (300, 4096), (40, 20000)])
+def test_products_beyond_binary32_in_place(gpu, t, h, which, kind):
+    """A wave reads its gradient a second time where its products left the range: before
+    it is overwritten."""
+    rng = np.random.default_rng([t, h])
+    s, dy, gs = (values(rng, (t, h), kind) * np.float32(2.0 ** n) for n in (60, 70, 80))
+    w = round_to(values(rng, h, kind) * np.float32(2.0 ** 70), kind)
+    args = [device(round_to(dy, kind), kind), device(round_to(s, kind), kind), device(w, kind), 1e-5,
+            device(round_to(gs, kind), kind)]
+    want = torch.empty_like(args[0]), torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+    qrs.layer_norm_backward(*args, *want)
+    assert all(torch.isfinite(v).all() for v in want)
+    ref = layer_norm_backward(host(args[0]), host(args[1]), w, 1e-5, host(args[4]))
+    tol = _tolerances(host(args[0]), host(args[1]), w, host(args[4]), kind)
+    assert np.all(np.abs(host(want[0]) - ref[0]) <= tol[0])
+    gx, got = args[0 if which == "grad_y" else 4], [torch.empty(h, device="cuda") for _ in range(2)]
+    qrs.layer_norm_backward(*args, gx, *got)
+    assert torch.equal(gx, want[0]) and torch.equal(got[0], want[1]) and torch.equal(got[1], want[2])

@@ -71,3 +71,53 @@ def test_folded_sums_are_the_same_every_time(gpu):
         outs.append(out)
     for out in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(out, outs[0]))
+
+
+def _case(t, h, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    s, dy, gs = (torch.randn(t, h, device="cuda", generator=g).bfloat16() for _ in range(3))
+    return s, dy, gs, torch.randn(h, device="cuda", generator=g).bfloat16()
+
+
+@pytest.mark.parametrize("which", ["grad_y", "grad_sum"])
+def test_long_batches_in_place_and_strided(gpu, which):
+    """Three launches, the last one of fewer rows than the others have work-groups."""
+    t, h = 2 * 65536 + 300, 136
+    s, dy, gs, w = _case(t, h, 5)
+    want = torch.empty_like(s), torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+    qrs.layer_norm_backward(dy, s, w, 1e-5, gs, *want)
+    wide = torch.full((t, 2 * h), float("nan"), device="cuda", dtype=torch.bfloat16)
+    wide[:, :h] = dy if which == "grad_y" else gs
+    gx = wide[:, :h]
+    got = torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+    qrs.layer_norm_backward(gx if which == "grad_y" else dy, s, w, 1e-5, gs if which == "grad_y" else gx, gx, *got)
+    assert torch.equal(gx, want[0]) and torch.equal(got[0], want[1]) and torch.equal(got[1], want[2])
+    assert torch.isnan(wide[:, h:]).all()
+
+
+def test_long_batches_in_a_graph(gpu):
+    """Replayed over other inputs, with eager work between: each replay is the eager result."""
+    t, h = 70000, 264
+    s, dy, gs, w = _case(t, h, 6)
+    out = torch.empty_like(s), torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+    n = ctypes.c_size_t()
+    assert qrs.load_library().qrs_layer_norm_backward_workspace(t, h, ctypes.byref(n)) == 0
+    workspace = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        qrs.layer_norm_backward(dy, s, w, 1e-5, gs, *out, workspace=workspace)
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qrs.layer_norm_backward(dy, s, w, 1e-5, gs, *out, workspace=workspace)
+    for seed in (7, 8, 9):
+        for to, v in zip((s, dy, gs, w), _case(t, h, seed)):
+            to.copy_(v)
+        want = torch.empty_like(s), torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+        qrs.layer_norm_backward(dy, s, w, 1e-5, gs, *want)
+        for v in out:
+            v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), seed
