@@ -97,7 +97,7 @@ struct LayerNormBackwardLaunch : NormBackwardLaunch {
   float* grad_bias;  // nullptr: not wanted. workspace: layer_norm_backward_parts rows of 2 h floats
 };
 
-// Work-groups of the backward pass, and rows of its workspace; fewer, if any, for binary32.
+// Work-groups of a launch of the backward pass, and rows of its workspace; fewer, if any, for binary32.
 uint32_t layer_norm_backward_parts(uint64_t rows, uint32_t h, bool f32);
 
 hipError_t launch_layer_norm_backward(const LayerNormBackwardLaunch& l, hipStream_t stream);

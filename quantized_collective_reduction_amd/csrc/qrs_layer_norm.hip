@@ -350,6 +350,9 @@ hipError_t launch_norm_io(const LayerNormLaunch& l, hipStream_t stream) {
 // grad_weight and grad_bias in registers and leaves one row of partial sums in
 // the workspace, and grad_params_kernel adds those rows in order: a fixed order
 // without atomics.
+//
+// Two waves a SIMD where a lane has 16 elements at most: 256 registers, of which binary32
+// would take a few more.
 template <int IO, int NT, int P8, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT, P8 <= 2 ? 2 : 1) void layer_norm_backward_kernel(const LayerNormBackwardLaunch a) {
   constexpr int kWaves = NT / 64;
